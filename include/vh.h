@@ -122,6 +122,7 @@ typedef uint16_t vh_e16;   /* a 16-bit element: bf16, or fp16 under VH_FLAG_FP16
 #define VH_FLAG_PDL_KV 8u   /* VH_FLAG_PDL, and the cached K/V may be requested before the wait (vh_decode_fused) */
 #define VH_FLAG_PLANNED 16u /* the workspace holds this step's plan from vh_decode_plan (vh_decode_fused, vh_paged_decode_attn) */
 #define VH_FLAG_PLAN_THREE_CALL 32u /* vh_decode_plan: plan for vh_paged_decode_attn instead of vh_decode_fused */
+#define VH_FLAG_Q16 128u /* vh_mrope_kv_append: q_rot holds 16-bit elements instead of fp32 */
 #define VH_FLAG_HOST_IO 64u /* vh_decode_fused: the per-step inputs and out may be pinned host memory, read and written in place */
 
 /* Fill the RoPE table used by vh_rope_kv_append.  Source: "Engineering TTS
@@ -377,6 +378,126 @@ int vh_paged_decode_attn_noalloc(const float* q_rot, const vh_bf16* k_cache, con
                                  const int32_t* seq_lens, const int32_t* active,
                                  vh_bf16* out, float sm_scale, int num_ctas, int32_t* err_flag,
                                  int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* ---- prompts, several rotary axes, sliding windows ------------------------
+ *
+ * The three calls below serve models that read a prompt into the cache, that
+ * rotate with several axes of positions, or that attend over a bounded part
+ * of a long cache.  The source pages have no counterpart (they leave prompts
+ * to the host framework's attention); conventions, cache layouts, shapes and
+ * error bits are those of the calls above.
+ *
+ * Ragged batches: T new tokens, ordered by row; row b brings tokens
+ * token_start[b] .. token_start[b+1]-1 (token_start int32 [B+1] on the device,
+ * non-decreasing; rows without tokens are allowed), and seq_lens[b] counts
+ * them: its token t has the logical slot
+ *     i = seq_lens[b] - (token_start[b+1] - t).
+ * T is the size of the token arrays (a static upper bound for captured
+ * graphs); tokens before token_start[0] and from token_start[B] on belong to
+ * no row, and nothing of theirs is read or written.  Active rows need
+ * 0 <= token_start[b] <= token_start[b+1] <= T and, if they bring tokens,
+ * token_start[b+1] - token_start[b] <= seq_lens[b] <= max_pages_per_seq*P;
+ * others are flagged VH_ERR_SEQLEN and treated as inactive.
+ *
+ * Windows: with window W and S sinks, the query in slot i sees key j <= i if
+ * i - j < W (the last W tokens, itself among them) or j < S (the first S
+ * tokens).  W = 0: no window, every j <= i is seen.  Slots that no query of
+ * the call sees are never read, nor their page-table entries used: pages
+ * that fell behind the window may have been given back, and their entries
+ * may hold anything.  Keys or values that one query does not see never
+ * change its result, whatever they hold (NaN and infinities too).
+ */
+
+/* RoPE with one to four axes of positions (time, height, width, ...) and KV
+ * append for a ragged batch of new tokens.
+ * q      e16 [T][Hq][D], token t at q + t*q_stride; k_new, v_new e16
+ *        [T][Hkv][D] with k_stride, v_stride: strides in elements, multiples of
+ *        8, at least Hq*D or Hkv*D (so q, k and v may be slices of one packed
+ *        projection output)
+ * cos_sin float [max_pos][D] from vh_rope_table
+ * positions int32 [num_axes][T], or NULL: every axis has the token's slot i
+ * pair_axis HOST array of D/2 bytes, the axis of every rotation pair
+ *        (0 <= pair_axis[i] < num_axes), or NULL: axis 0 for all.  Read during
+ *        the call.  Pair i of token t turns by the angle
+ *        positions[pair_axis[i]][t] * theta^(-2i/D): sections (time first, then
+ *        height, then width) and axes that take turns are both such arrays.
+ * num_axes 1 .. 4
+ * q_norm_w, k_norm_w, norm_eps: per-head RMSNorm before the rotation, as for
+ *        vh_rope_kv_append
+ * token_start int32 [B+1], or NULL: one token a row (T == B, token b is row b's)
+ * q_rot  out: float [T][Hq][D], or e16 with VH_FLAG_Q16 (rounded to nearest
+ *        even; what vh_window_prompt_attn takes).  Must not overlap q.
+ * flags  VH_FLAG_FP16, VH_FLAG_ROPE_INTERLEAVED, VH_FLAG_Q16
+ * For every token of an active row: q_rot = rope(q); the cache slot i receives
+ * rne(rope(k_new)) and v_new, all in fp32 before the one rounding.  Tokens of
+ * inactive rows write nothing; so does a token with a position outside
+ * [0, max_pos) on any axis (VH_ERR_POS); a page id outside [0, num_pages) is
+ * flagged VH_ERR_PAGE and only the append of that token is skipped.
+ * T == 0 does nothing.  Live tokens own disjoint slots (not checked).
+ * Errors: VH_EINVAL, VH_EALIGN, VH_ENODEV, VH_ECUDA. */
+int vh_mrope_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       const float* cos_sin, int max_pos, const int32_t* positions,
+                       const uint8_t* pair_axis, int num_axes,
+                       const float* q_norm_w, const float* k_norm_w, float norm_eps,
+                       vh_e16* k_cache, vh_e16* v_cache, int64_t page_stride, int64_t token_stride,
+                       int64_t head_stride, int num_pages, const int32_t* page_table, int max_pages_per_seq,
+                       const int32_t* token_start, const int32_t* seq_lens, const int32_t* active,
+                       void* q_rot, int32_t* err_flag, unsigned flags,
+                       int T, int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* Single-token attention over a window and sinks, in one launch.
+ * Arguments, result and errors as for vh_paged_decode_attn (q_rot float
+ * [B][Hq][D], the query of row b in slot seq_lens[b]-1), with the window and
+ * sinks above (both >= 0); rows split across CTAs are merged inside the
+ * launch, so no vh_decode_combine follows.  Padding rows (active == 0) and
+ * rows flagged VH_ERR_SEQLEN are written as zeros; a page id outside
+ * [0, num_pages) is flagged VH_ERR_PAGE and its keys and values are taken as
+ * zeros.
+ * workspace: as for vh_decode_fused (at least vh_decode_workspace_bytes of the
+ * same shape and num_ctas, zero-filled once; the same buffer may serve both
+ * calls, one after the other).  Calls that may overlap on the device, captured
+ * graphs among them, need workspaces of their own.
+ * flags: VH_FLAG_FP16, VH_FLAG_PDL (as for vh_paged_decode_attn: lengths, flags
+ * and page ids are read before the previous kernel has completed). */
+int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e16* v_cache,
+                          int64_t page_stride, int64_t token_stride, int64_t head_stride, int num_pages,
+                          const int32_t* page_table, int max_pages_per_seq,
+                          const int32_t* seq_lens, const int32_t* active, int window, int sinks,
+                          vh_e16* out, float sm_scale, int num_ctas,
+                          void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
+                          int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* Bytes of workspace vh_window_prompt_attn needs for T tokens of B rows on
+ * the current device; 0 on bad arguments.  Holds the partial results of query
+ * blocks whose keys are split over CTAs (short chunks over long contexts). */
+size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
+
+/* Attention of a ragged batch of new tokens (prompts, or chunks of them)
+ * over the paged cache, which already holds the new tokens' keys and values.
+ * q      e16 [T][Hq][D], 16-byte aligned (q_rot of vh_mrope_kv_append with VH_FLAG_Q16)
+ * token_start, seq_lens, active, window, sinks: as above (token_start required)
+ * out    e16 [T][Hq][D]; tokens of inactive or flagged rows are written as
+ *        zeros, tokens of no row are left as they were.
+ * sm_scale: softmax scale; <= 0 means 1/sqrt(D).
+ * num_splits: CTAs that share the keys of one block of queries; 0 = automatic,
+ *        at most 64.  A larger num_splits than the workspace holds is cut to it.
+ * workspace: at least vh_prompt_workspace_bytes(...) bytes, 16-byte aligned; no
+ *        initialisation needed.  Calls that may overlap on the device need
+ *        workspaces of their own.
+ * flags: VH_FLAG_FP16.
+ * Scores and softmax statistics are fp32; the weights are rounded to the
+ * element type for the value product, which accumulates in fp32.
+ * T == 0 does nothing.  A page id outside [0, num_pages) that a query would
+ * read is flagged VH_ERR_PAGE and its keys and values are taken as zeros.
+ * Errors: VH_EINVAL, VH_EALIGN, VH_EWORKSPACE, VH_ENODEV, VH_ECUDA. */
+int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache,
+                          int64_t page_stride, int64_t token_stride, int64_t head_stride, int num_pages,
+                          const int32_t* page_table, int max_pages_per_seq,
+                          const int32_t* token_start, const int32_t* seq_lens, const int32_t* active,
+                          int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
+                          int T, int B, int Hq, int Hkv, int D, int page_size, void* stream);
 
 /* Self-test of the failure path of the kernels' pipeline waits.  The source
  * pages have no counterpart: every wait of the attention kernels on an

@@ -1,0 +1,95 @@
+// vh_window.h -- parameter blocks and launchers of the ragged-batch append,
+// the windowed decode attention and the prompt attention (internal; the
+// public interface is vh.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>  // CUtensorMap (the type only)
+#include <cuda_runtime.h>
+
+namespace vh {
+
+// A window that never ends, for W = 0 (slots are below 2^24).
+constexpr int kNoWindow = 1 << 28;
+
+struct MropeParams {
+  const uint16_t* q;
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  long long q_stride, k_stride, v_stride;  // elements between tokens
+  const float* cos_sin;
+  int max_pos;
+  const int32_t* positions;    // [num_axes][T], or null (slot index)
+  int num_axes;
+  unsigned long long axis[2];  // 2 bits a rotation pair, pair 0 lowest
+  const float* q_norm_w;       // [D], or null
+  const float* k_norm_w;
+  float norm_eps;
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  long long page_stride, token_stride, head_stride;
+  int num_pages;
+  const int32_t* page_table;   // null: contiguous cache
+  int max_pages_per_seq;
+  const int32_t* token_start;  // [B + 1], or null (one token a row)
+  const int32_t* seq_lens;
+  const int32_t* active;
+  void* q_rot;                 // float or 16-bit elements
+  int q16;
+  int rope_interleaved, f16;
+  int32_t* err_flag;
+  int T, B, Hq, Hkv, D, P;
+  int tokens_per_cta;
+};
+
+struct WindowDecodeParams {
+  // K and V caches as 4-D tensors (see vh_kernels.h): boxes of 16 tokens x Hc
+  // heads, and of 8 tokens x 1 head
+  CUtensorMap tmap_k, tmap_v, tmap_k8, tmap_v8;
+  int tm_tok_dim, full_boxes;
+  const float* q_rot;          // [B][Hq][D]
+  int num_pages;
+  const int32_t* page_table;   // null: contiguous cache
+  int max_pages_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* active;
+  int window, sinks;           // window >= 1 (kNoWindow: none), sinks >= 0
+  uint16_t* out;
+  float scale_log2;            // softmax scale * log2(e)
+  int* counters;               // [groups][B] pieces delivered per row; zero between calls
+  float* part_o;               // [groups][N][2][Hc*G][D]
+  float* part_lse;             // [groups][N][2][Hc*G], base 2
+  int32_t* err_flag;
+  int f16;
+  int B, Hq, Hkv, D, G, P;
+  int Hc, groups, N, stages, min_tiles;
+  int stage_bytes;             // K then V of one tile: [D/64][Hc][16 tokens][128 B swizzled] each
+  int q_off, cum_off, len_off, bar_off, smem_bytes;
+};
+
+struct PromptParams {
+  const uint16_t* q;           // [T][Hq][D]
+  const uint16_t* k_cache;
+  const uint16_t* v_cache;
+  long long page_stride, token_stride, head_stride;
+  int num_pages;
+  const int32_t* page_table;   // null: contiguous cache
+  int max_pages_per_seq;
+  const int32_t* token_start;
+  const int32_t* seq_lens;
+  const int32_t* active;
+  int window, sinks;
+  uint16_t* out;
+  float scale_log2;
+  int32_t* err_flag;
+  int f16;
+  int T, B, Hq, Hkv, D, G, P;
+};
+
+cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
+cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
+cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);
+
+}  // namespace vh

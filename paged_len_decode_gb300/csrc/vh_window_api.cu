@@ -1,0 +1,355 @@
+// vh_window_api.cu -- host side of the ragged-batch append, the windowed
+// decode attention and the prompt attention (declared in include/vh.h): checks
+// of scalars and alignment, launch plans, launches on the caller's stream.
+// Nothing here synchronises, allocates or reads device memory.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <unordered_map>
+
+#include "../../include/vh.h"
+#include "vh_plan.h"
+#include "vh_window.h"
+
+namespace {
+
+using vh::DeviceInfo;
+using vh::aligned16;
+using vh::device_info;
+using vh::too_many_tiles;
+using vh::valid_paging;
+using vh::valid_shape;
+using vh::valid_table;
+using vh::kMaxDevices;
+
+constexpr int kMaxHc = 8;
+constexpr int kMaxStages = 8;
+constexpr int kStageTarget = 65536;  // bytes in flight of a CTA, two CTAs on an SM
+
+// Kernel attributes of this file's kernels, set on the first call on a device.
+struct Prepared {
+  std::once_flag once;
+  bool ok = false;
+};
+Prepared g_prepared[kMaxDevices];
+
+bool prepared(const DeviceInfo& dev) {
+  Prepared& s = g_prepared[dev.index];
+  std::call_once(s.once, [&]() {
+    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess;
+    if (!s.ok) cudaGetLastError();
+  });
+  return s.ok;
+}
+
+size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Shared-memory plan and automatic CTA count of the windowed decode kernel.
+struct DecodePlan {
+  bool ok;
+  int Hc, groups, stages, stage_bytes, q_off, cum_off, len_off, bar_off, smem_bytes, auto_n;
+};
+
+bool layout_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev) {
+  p.G = p.Hq / p.Hkv;
+  // kv heads per CTA: the largest divisor of Hkv with tiles of at most 32 KB
+  // (and at most 8 one-head boxes a half tile, the producer warp's lanes), so
+  // that two CTAs share an SM; fewer if two stages do not fit beside the rows
+  int hc = std::min(p.Hkv, std::min(512 / p.D, kMaxHc));
+  for (;; --hc) {
+    if (hc < 1) return false;
+    if (p.Hkv % hc != 0) continue;
+    p.Hc = hc;
+    p.groups = p.Hkv / hc;
+    p.stage_bytes = 2 * 16 * hc * p.D * 2;
+    const size_t rows = align_up(4 * (static_cast<size_t>(p.B) + 1), 16) + align_up(4 * static_cast<size_t>(p.B), 16);
+    const size_t fixed = 1024 + static_cast<size_t>(hc) * p.G * p.D * 4 + rows + 8 * (2 * kMaxStages + 2) + 48 * 4 + 128;
+    const size_t budget = static_cast<size_t>(dev.smem_optin);
+    if (fixed + 2 * static_cast<size_t>(p.stage_bytes) > budget) continue;
+    p.stages = static_cast<int>(std::min<size_t>((budget - fixed) / p.stage_bytes,
+                                                 std::max(2, std::min(kMaxStages, kStageTarget / p.stage_bytes))));
+    size_t off = static_cast<size_t>(p.stages) * p.stage_bytes;
+    p.q_off = static_cast<int>(off);
+    off += static_cast<size_t>(hc) * p.G * p.D * 4;
+    p.cum_off = static_cast<int>(off);
+    off += align_up(4 * (static_cast<size_t>(p.B) + 1), 16);
+    p.len_off = static_cast<int>(off);
+    off += align_up(4 * static_cast<size_t>(p.B), 16);
+    p.bar_off = static_cast<int>(off);
+    off += 8 * (2 * static_cast<size_t>(p.stages) + 2) + 48 * 4;
+    p.smem_bytes = static_cast<int>(align_up(off, 128) + 1024);  // + up to 1024 to align the base
+    return true;
+  }
+}
+
+std::mutex g_mu;
+std::unordered_map<uint64_t, DecodePlan> g_decode_plans;
+
+// Plan of p's shape, computed once (the occupancy query costs more host time
+// than a launch).  The CTA count is at most vh_decode_fused's for the same
+// shape, so that one workspace serves both.
+bool plan_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev, int* auto_n) {
+  uint64_t key = static_cast<uint64_t>(dev.index);
+  key = (key << 16) | static_cast<uint64_t>(p.B);
+  key = (key << 11) | static_cast<uint64_t>(p.Hkv);
+  key = (key << 4) | static_cast<uint64_t>(p.Hq / p.Hkv);
+  key = (key << 2) | static_cast<uint64_t>(p.D / 64);
+  key = (key << 11) | static_cast<uint64_t>(p.P);
+  key = (key << 1) | (p.f16 ? 1u : 0u);
+  DecodePlan c{};
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    auto it = g_decode_plans.find(key);
+    if (it != g_decode_plans.end()) c = it->second;
+  }
+  if (c.auto_n == 0 && !c.ok) {
+    vh::WindowDecodeParams q = p;
+    vh::AttnParams f{};
+    f.B = p.B;
+    f.Hq = p.Hq;
+    f.Hkv = p.Hkv;
+    f.D = p.D;
+    f.P = p.P;
+    f.f16 = p.f16;
+    int fused_n = 0, per_sm = 0;
+    c.ok = layout_decode(q, dev) && vh::plan_attn(f, dev, true, &fused_n);
+    if (c.ok) {
+      if (vh::window_decode_occupancy(q, &per_sm) != cudaSuccess || per_sm < 1) {
+        cudaGetLastError();
+        per_sm = 1;
+      }
+      c = DecodePlan{true,      q.Hc,      q.groups,  q.stages,   q.stage_bytes, q.q_off,
+                     q.cum_off, q.len_off, q.bar_off, q.smem_bytes, 0};
+      c.auto_n = std::max(1, std::min(fused_n, dev.sm_count * per_sm / q.groups));
+    } else {
+      c.auto_n = -1;
+    }
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (g_decode_plans.size() >= 4096) g_decode_plans.clear();
+    g_decode_plans[key] = c;
+  }
+  if (!c.ok) return false;
+  p.G = p.Hq / p.Hkv;
+  p.Hc = c.Hc;
+  p.groups = c.groups;
+  p.stages = c.stages;
+  p.stage_bytes = c.stage_bytes;
+  p.q_off = c.q_off;
+  p.cum_off = c.cum_off;
+  p.len_off = c.len_off;
+  p.bar_off = c.bar_off;
+  p.smem_bytes = c.smem_bytes;
+  *auto_n = c.auto_n;
+  return true;
+}
+
+// Scalars that every call of this file checks alike.
+bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                 int num_pages, const int32_t* page_table, int max_pages_per_seq) {
+  return valid_shape(B, Hq, Hkv, D, P) && num_pages >= 1 && page_stride >= 1 && token_stride >= 1 &&
+         head_stride >= 1 && valid_paging(P, max_pages_per_seq) && !too_many_tiles(B, max_pages_per_seq, P) &&
+         valid_table(page_table, B, max_pages_per_seq, num_pages);
+}
+
+bool aligned_cache(const void* k, const void* v, int64_t page_stride, int64_t token_stride, int64_t head_stride) {
+  return aligned16(k) && aligned16(v) && page_stride % 8 == 0 && token_stride % 8 == 0 && head_stride % 8 == 0;
+}
+
+int status_of(cudaError_t e) { return e == cudaSuccess ? VH_OK : VH_ECUDA; }
+
+}  // namespace
+
+extern "C" {
+
+int vh_mrope_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const float* cos_sin, int max_pos, const int32_t* positions,
+                       const uint8_t* pair_axis, int num_axes, const float* q_norm_w, const float* k_norm_w,
+                       float norm_eps, vh_e16* k_cache, vh_e16* v_cache, int64_t page_stride, int64_t token_stride,
+                       int64_t head_stride, int num_pages, const int32_t* page_table, int max_pages_per_seq,
+                       const int32_t* token_start, const int32_t* seq_lens, const int32_t* active, void* q_rot,
+                       int32_t* err_flag, unsigned flags, int T, int B, int Hq, int Hkv, int D, int page_size,
+                       void* stream) {
+  if ((flags & ~(VH_FLAG_FP16 | VH_FLAG_ROPE_INTERLEAVED | VH_FLAG_Q16)) != 0 || T < 0 || max_pos < 1 ||
+      num_axes < 1 || num_axes > 4 || !(norm_eps >= 0.f) || !(norm_eps < 1e30f) ||
+      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
+                   max_pages_per_seq) ||
+      (!token_start && T != B) || q_stride < static_cast<int64_t>(Hq) * D || k_stride < static_cast<int64_t>(Hkv) * D ||
+      v_stride < static_cast<int64_t>(Hkv) * D)
+    return VH_EINVAL;
+  vh::MropeParams p{};
+  if (pair_axis)
+    for (int i = 0; i < D / 2; ++i) {
+      if (pair_axis[i] >= num_axes) return VH_EINVAL;
+      p.axis[i >> 5] |= static_cast<unsigned long long>(pair_axis[i]) << (2 * (i & 31));
+    }
+  if (T == 0) return VH_OK;
+  if (!q || !k_new || !v_new || !cos_sin || !k_cache || !v_cache || !seq_lens || !active || !q_rot) return VH_EINVAL;
+  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(cos_sin) || !aligned16(q_rot) ||
+      !aligned16(q_norm_w) || !aligned16(k_norm_w) || q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+      !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
+    return VH_EALIGN;
+  if (!device_info()) return VH_ENODEV;
+  p.q = q;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.positions = positions;
+  p.num_axes = num_axes;
+  p.q_norm_w = q_norm_w;
+  p.k_norm_w = k_norm_w;
+  p.norm_eps = norm_eps;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.token_start = token_start;
+  p.seq_lens = seq_lens;
+  p.active = active;
+  p.q_rot = q_rot;
+  p.q16 = (flags & VH_FLAG_Q16) != 0;
+  p.rope_interleaved = (flags & VH_FLAG_ROPE_INTERLEAVED) != 0;
+  p.f16 = (flags & VH_FLAG_FP16) != 0;
+  p.err_flag = err_flag;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.P = page_size;
+  return status_of(vh::launch_mrope_kv_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
+                          int64_t token_stride, int64_t head_stride, int num_pages, const int32_t* page_table,
+                          int max_pages_per_seq, const int32_t* seq_lens, const int32_t* active, int window, int sinks,
+                          vh_e16* out, float sm_scale, int num_ctas, void* workspace, size_t workspace_bytes,
+                          int32_t* err_flag, unsigned flags, int B, int Hq, int Hkv, int D, int page_size,
+                          void* stream) {
+  if (!q_rot || !k_cache || !v_cache || !seq_lens || !active || !out ||
+      (flags & ~(VH_FLAG_FP16 | VH_FLAG_PDL)) != 0 || window < 0 || sinks < 0 || num_ctas < 0 || num_ctas > 65535 ||
+      !(sm_scale == sm_scale) ||
+      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
+                   max_pages_per_seq))
+    return VH_EINVAL;
+  if (!aligned16(q_rot) || !aligned16(out) || !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
+    return VH_EALIGN;
+  if (!workspace) return VH_EWORKSPACE;
+  if (!aligned16(workspace)) return VH_EALIGN;
+  const DeviceInfo* dev = device_info();
+  if (!dev || !prepared(*dev)) return VH_ENODEV;
+  vh::WindowDecodeParams p{};
+  p.f16 = (flags & VH_FLAG_FP16) != 0;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.P = page_size;
+  int auto_n = 0;
+  if (!plan_decode(p, *dev, &auto_n)) return VH_EINVAL;
+  p.N = num_ctas > 0 ? num_ctas : auto_n;
+  p.min_tiles = 1;
+  const vh::WsLayout w = vh::ws_layout(B, Hq, Hkv, D, p.N);
+  if (workspace_bytes < w.total) return VH_EWORKSPACE;
+  // the tensor maps are those of the other attention calls
+  vh::AttnParams a{};
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.page_stride = page_stride;
+  a.token_stride = token_stride;
+  a.head_stride = head_stride;
+  a.num_pages = num_pages;
+  a.Hkv = Hkv;
+  a.Hc = p.Hc;
+  a.D = D;
+  a.P = page_size;
+  if (!vh::encode_cache_maps(a)) return VH_EINVAL;
+  p.tmap_k = a.tmap_k;
+  p.tmap_v = a.tmap_v;
+  p.tmap_k8 = a.tmap_k8;
+  p.tmap_v8 = a.tmap_v8;
+  p.tm_tok_dim = a.tm_tok_dim;
+  p.full_boxes = a.full_boxes;
+  p.q_rot = q_rot;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.seq_lens = seq_lens;
+  p.active = active;
+  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
+  p.sinks = std::min(sinks, vh::kNoWindow);
+  p.out = out;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  p.counters = reinterpret_cast<int*>(ws + w.counters);
+  p.part_lse = reinterpret_cast<float*>(ws + w.lse);
+  p.part_o = reinterpret_cast<float*>(ws + w.o);
+  p.err_flag = err_flag;
+  const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return status_of(vh::launch_window_decode(p, static_cast<cudaStream_t>(stream), (flags & VH_FLAG_PDL) != 0));
+}
+
+size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
+  if (T < 0 || !valid_shape(B, Hq, Hkv, D, 16) || !device_info()) return 0;
+  return 256;
+}
+
+int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
+                          int64_t token_stride, int64_t head_stride, int num_pages, const int32_t* page_table,
+                          int max_pages_per_seq, const int32_t* token_start, const int32_t* seq_lens,
+                          const int32_t* active, int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B,
+                          int Hq, int Hkv, int D, int page_size, void* stream) {
+  if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 64 ||
+      !(sm_scale == sm_scale) ||
+      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
+                   max_pages_per_seq))
+    return VH_EINVAL;
+  if (T == 0) return VH_OK;
+  if (!q || !k_cache || !v_cache || !token_start || !seq_lens || !active || !out) return VH_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
+    return VH_EALIGN;
+  if (!workspace) return VH_EWORKSPACE;
+  if (!aligned16(workspace)) return VH_EALIGN;
+  const DeviceInfo* dev = device_info();
+  if (!dev || !prepared(*dev)) return VH_ENODEV;
+  if (workspace_bytes < vh_prompt_workspace_bytes(T, B, Hq, Hkv, D)) return VH_EWORKSPACE;
+  vh::PromptParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.token_start = token_start;
+  p.seq_lens = seq_lens;
+  p.active = active;
+  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
+  p.sinks = std::min(sinks, vh::kNoWindow);
+  p.out = out;
+  const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err_flag = err_flag;
+  p.f16 = (flags & VH_FLAG_FP16) != 0;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.G = Hq / Hkv;
+  p.P = page_size;
+  return status_of(vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,624 @@
+// window_decode.cu -- single-token GQA attention over a sliding window and
+// sinks of a paged cache, rows split over CTAs and merged in the launch.
+//
+// Operation: row b, L = seq_lens[b]; V = {j < L: j < S or j >= L - W};
+//   o = sum_{j in V} softmax(scale <q_rot, K_j>) V_j,
+// with a running max and sum in fp32.
+//
+// Bound by HBM: 4 G flops for the 4 bytes of a key and value element.
+//  * Work list: a row's visible keys touch ns = ceil(min(S, L) / 16) tiles of
+//    16 tokens at its head and the tiles from the window's first key to its
+//    end; tiles between are not in the list.  The list of all rows is cut into
+//    N ranges that differ by at most a tile, one a CTA, so a row is split
+//    wherever its tiles straddle CTAs (a CTA has two partial rows at most).
+//  * The producer warp describes 32 tiles at a time, one a lane (row, page,
+//    visible keys), a batch ahead of its use, and copies each with tiled
+//    tensor copies: one box of 16 tokens x all heads of the CTA per 64
+//    columns of K and V, or for tiles whose visible keys lie in one half,
+//    8-token boxes of that half only.  A page id out of range becomes a page
+//    past the tensor, which the copy engine fills with zeros.
+//  * A consumer warp per kv head: S^T = K q^T and O^T += V^T P^T on
+//    mma.sync m16n8k16, the G heads padded to 8 columns, q and P split into a
+//    high part and a residual of the element type so that products keep 16
+//    bits of them (22 in fp16).  Keys outside V get -inf before the max, and
+//    their rows of V are zeroed in shared memory, so nothing they hold counts.
+//  * Merge: partial (o, lse) go to the workspace; a counter per row tells the
+//    last CTA to arrive, which adds the pieces in their order in the row, so
+//    the result does not depend on who is last.
+#include "vh_common.cuh"
+#include "vh_window.h"
+
+namespace vh {
+
+namespace {
+
+constexpr int kMaxHeads = 8;                 // kv heads (consumer warps) of a CTA
+constexpr int kThreadsMax = 32 * (kMaxHeads + 1);
+enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscPart = 34, kMiscInts = 48 };  // part: 4 ints each
+
+__device__ __forceinline__ int share_begin(int c, int n, int total) {
+  return c * (total / n) + min(c, total % n);
+}
+
+__device__ __forceinline__ int share_of(int t, int n, int total) {
+  const int q = total / n, r = total % n, big = r * (q + 1);
+  return t < big ? t / (q + 1) : r + (t - big) / q;
+}
+
+// The tiles of a row: `sink` tiles from tile 0, then tiles from `first` on.
+struct RowTiles {
+  int sink, first, count;
+  __device__ int tile(int k) const { return k < sink ? k : k - sink + first; }
+};
+
+__device__ __forceinline__ RowTiles tiles_of(int L, int window, int sinks) {
+  RowTiles r;
+  r.sink = (min(sinks, L) + kTile - 1) / kTile;
+  r.first = max(r.sink, max(0, L - window) / kTile);
+  r.count = r.sink + (L + kTile - 1) / kTile - r.first;
+  return r;
+}
+
+// Bit k: key 16 tile + k is visible.
+__device__ __forceinline__ uint32_t visible16(int tile, int L, int window, int sinks) {
+  auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : (x >= kTile ? 0xFFFFu : (1u << x) - 1u); };
+  const int j0 = tile * kTile;
+  return below(L - j0) & (below(sinks - j0) | (~below(L - window - j0) & 0xFFFFu));
+}
+
+// In-place inclusive prefix sum of cum[1..n] (cum[0] = 0).
+__device__ void scan_rows(int* cum, int n, int* tot) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + blockDim.x - 1) / blockDim.x;
+  const int lo = min(n, tid * per), hi = min(n, lo + per);
+  int sum = 0;
+  for (int i = lo; i < hi; ++i) sum += cum[1 + i];
+  int x = sum;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, off);
+    if (lane >= off) x += y;
+  }
+  if (lane == 31) tot[warp] = x;
+  __syncthreads();
+  int run = x - sum;
+  for (int w = 0; w < warp; ++w) run += tot[w];
+  for (int i = lo; i < hi; ++i) {
+    run += cum[1 + i];
+    cum[1 + i] = run;
+  }
+  __syncthreads();
+}
+
+// First row with cum[row + 1] > t, from row lo on.
+__device__ __forceinline__ int row_of(const int* cum, int lo, int B, int t) {
+  int hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cum[mid + 1] > t) hi = mid; else lo = mid + 1;
+  }
+  return lo;
+}
+
+template <int D, int G, typename E>
+__global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __grid_constant__ WindowDecodeParams p) {
+  constexpr int KS = D / 16;      // k-steps of the score product = m-tiles of the value product
+  constexpr int HALVES = D / 64;  // 128-byte column blocks of a K or V row
+  constexpr int PER = D / 32;
+  extern __shared__ __align__(128) unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int Hc = p.Hc, S = p.stages, HG = Hc * G;
+  const int c = blockIdx.x, gy = blockIdx.y, h0 = gy * Hc;
+  int* cum = reinterpret_cast<int*>(smem + p.cum_off);
+  int* lens = reinterpret_cast<int*>(smem + p.len_off);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.bar_off);
+  int* misc = reinterpret_cast<int*>(bars + 2 * S + 2);
+  volatile int* abort_flag = misc + kMiscAbort;
+  const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + S);
+  const uint32_t qfull = smem_addr(bars + 2 * S), qempty = smem_addr(bars + 2 * S + 1);
+  const int max_len = p.max_pages_per_seq * p.P;
+  const bool p8 = p.P == 8;
+  const float NEG_INF = __int_as_float(0xff800000);
+  pdl_launch_dependents();
+
+  // ---- work list (lengths, flags and page ids are read before the wait) -------
+  if (tid == 0) {
+    *abort_flag = 0;
+    misc[kMiscLost] = 0;
+    for (int s = 0; s < S; ++s) {
+      mbar_init(full0 + 8 * s, 1);
+      mbar_init(empty0 + 8 * s, Hc);
+    }
+    mbar_init(qfull, 1);
+    mbar_init(qempty, Hc);
+    fence_barrier_init();
+    cum[0] = 0;
+  }
+  for (int b = tid; b < p.B; b += blockDim.x) {
+    const int act = p.active[b], L = p.seq_lens[b];
+    const bool ok = act && L >= 1 && L <= max_len;
+    if (act && !ok && c == 0 && gy == 0) flag_error(p.err_flag, VH_ERR_SEQLEN);
+    cum[1 + b] = ok ? tiles_of(L, p.window, p.sinks).count : 0;
+    lens[b] = L;
+  }
+  __syncthreads();
+  scan_rows(cum, p.B, misc + kMiscTot);
+  const int T = cum[p.B];
+  const int n_eff = min(p.N, (T + p.min_tiles - 1) / p.min_tiles);  // 0 if there is no work
+  const bool works = c < n_eff;
+  const int t0 = works ? share_begin(c, n_eff, T) : 0, t1 = works ? share_begin(c + 1, n_eff, T) : 0;
+  const int b0 = works ? row_of(cum, 0, p.B, t0) : 0;
+  const int tpp = (p.P + kTile - 1) / kTile;  // tiles of a page
+
+  // ---- padding rows, dealt out to the CTAs, are written as zeros ---------------
+  auto zero_rows = [&]() {
+    for (int b = c; b < p.B; b += p.N) {
+      if (cum[b + 1] != cum[b]) continue;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + (static_cast<long long>(b) * p.Hq + gy * HG) * D);
+      for (int i = tid; i < HG * D / 8; i += blockDim.x) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+
+  if (warp == Hc) {
+    // ======================= producer warp =====================================
+    // a tile's description, one lane each
+    struct Tile {
+      int row, tok, page, page2;  // tok: first token in the page; page2: second page (8-token pages)
+      uint32_t mask;
+    };
+    auto describe = [&](int t) -> Tile {
+      Tile d{0, 0, 0, 0, 0u};
+      if (t >= t1) return d;
+      d.row = row_of(cum, b0, p.B, t);
+      const int L = lens[d.row], tk = tiles_of(L, p.window, p.sinks).tile(t - cum[d.row]);
+      d.mask = visible16(tk, L, p.window, p.sinks);
+      auto page_at = [&](int j) -> int {
+        const long long lp = static_cast<long long>(d.row) * p.max_pages_per_seq + j;
+        return p.page_table ? p.page_table[lp] : static_cast<int>(lp);
+      };
+      if (p8) {
+        if (d.mask & 0x00FFu) d.page = page_at(2 * tk);
+        if (d.mask & 0xFF00u) d.page2 = page_at(2 * tk + 1);
+      } else {
+        d.page = page_at(tk / tpp);
+        d.tok = (tk % tpp) * kTile;
+      }
+      return d;
+    };
+    Tile cur{}, nxt{};
+    if (works) {
+      cur = describe(t0 + lane);
+      nxt = describe(t0 + 32 + lane);
+      if (lane == 0) prefetch_tensormap(&p.tmap_k);
+      if (lane == 1) prefetch_tensormap(&p.tmap_v);
+    }
+    pdl_wait();
+    zero_rows();
+    if (!works) return;
+    // Boxes of this lane.  Whole tiles: lanes 0 .. 2 HALVES - 1 take (K or V,
+    // column block).  Else one box per (half, head, column block, K or V).
+    const int l_kv = lane & 1, l_hf = (lane >> 1) % HALVES;
+    const int l_head = (lane / (2 * HALVES)) % Hc, l_g = lane / (2 * HALVES * Hc);
+    const void* map16 = l_kv ? static_cast<const void*>(&p.tmap_v) : static_cast<const void*>(&p.tmap_k);
+    const void* map8 = l_kv ? static_cast<const void*>(&p.tmap_v8) : static_cast<const void*>(&p.tmap_k8);
+    const uint32_t off16 = static_cast<uint32_t>(l_kv * (p.stage_bytes / 2) + l_hf * Hc * 2048);
+    const uint32_t off8 = off16 + static_cast<uint32_t>(l_head * 2048 + l_g * 1024);
+    const uint64_t policy = l2_policy_evict_first();  // K and V are read once a launch
+    int stage = 0, round = 0, nseg = 0, prev_row = -1, issued = 0;
+    bool aborted = false;
+    for (int t = t0; t < t1; ++t, ++issued) {
+      const int w = (t - t0) & 31;
+      if (w == 0 && t > t0) {
+        cur = nxt;
+        nxt = describe(t + 32 + lane);
+      }
+      const int row = __shfl_sync(0xffffffffu, cur.row, w), tok = __shfl_sync(0xffffffffu, cur.tok, w);
+      const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, w);
+      int page = __shfl_sync(0xffffffffu, cur.page, w), page2 = __shfl_sync(0xffffffffu, cur.page2, w);
+      if (page < 0 || page >= p.num_pages || page2 < 0 || page2 >= p.num_pages) {
+        if (lane == 0) flag_error(p.err_flag, VH_ERR_PAGE);
+        if (page < 0 || page >= p.num_pages) page = p.num_pages;  // past the tensor: read as zeros
+        if (page2 < 0 || page2 >= p.num_pages) page2 = p.num_pages;
+      }
+      if (row != prev_row) {
+        // the next row's q, once the consumers have taken the last row's
+        if (nseg > 0 && !mbar_wait(qempty, (nseg - 1) & 1)) {
+          aborted = true;
+          break;
+        }
+        if (lane == 0) {
+          const long long qrow = static_cast<long long>(row) * p.Hq + static_cast<long long>(h0) * G;
+          mbar_arrive_expect_tx(qfull, static_cast<uint32_t>(HG * D * 4));
+          bulk_g2s(smem_addr(smem + p.q_off), p.q_rot + qrow * D, static_cast<uint32_t>(HG * D * 4), qfull);
+        }
+        ++nseg;
+        prev_row = row;
+      }
+      if (issued >= S && !mbar_wait(empty0 + 8 * stage, (round - 1) & 1)) {
+        aborted = true;
+        break;
+      }
+      if (*abort_flag) {
+        aborted = true;
+        break;
+      }
+      const bool lo_half = (mask & 0x00FFu) != 0, hi_half = (mask & 0xFF00u) != 0, both = lo_half && hi_half;
+      const uint32_t st = smem_addr(smem) + static_cast<uint32_t>(stage * p.stage_bytes), fb = full0 + 8 * stage;
+      if (lane == 0) mbar_arrive_expect_tx(fb, static_cast<uint32_t>(both ? p.stage_bytes : p.stage_bytes / 2));
+      __syncwarp();
+      if (both && p.full_boxes && !p8) {
+        if (lane < 2 * HALVES) tma_load_4d_hint(st + off16, map16, l_hf * 64, tok, h0, page, fb, policy);
+      } else if (l_g < 2 && (l_g ? hi_half : lo_half)) {
+        const int tk = p8 ? 0 : tok + 8 * l_g;
+        const int c1 = p.tm_tok_dim == 1 ? tk : h0 + l_head, c2 = p.tm_tok_dim == 1 ? h0 + l_head : tk;
+        tma_load_4d_hint(st + off8, map8, l_hf * 64, c1, c2, (p8 && l_g) ? page2 : page, fb, policy);
+      }
+      if (++stage == S) {
+        stage = 0;
+        ++round;
+      }
+    }
+    if (aborted) {
+      if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
+      *abort_flag = 1;
+      // copies in flight land before the shared memory goes away
+      for (int k = max(0, issued - S); k < issued; ++k) (void)mbar_wait(full0 + 8 * (k % S), (k / S) & 1);
+      if (nseg > 0) (void)mbar_wait(qfull, (nseg - 1) & 1);
+    }
+    return;
+  }
+
+  // ========================= consumer warps ======================================
+  pdl_wait();
+  zero_rows();
+  if (!works) return;
+  const int w = warp, h = h0 + w;
+  const int g4 = lane >> 2, t4 = lane & 3;
+  // ldmatrix rows of this lane; chunk c of row r of a swizzled box lies at c ^ (r & 7)
+  const int ka_row = (lane & 7) + 8 * ((lane >> 3) & 1), va_row = (lane & 7) + 8 * (lane >> 4);
+  const int ksw = (lane >> 4) ^ (ka_row & 7), vsw = ((lane >> 3) & 1) ^ (va_row & 7);
+  const uint32_t block_bytes = static_cast<uint32_t>(Hc) * 2048u;  // one column block of all heads
+  auto row_off = [&](int r) -> uint32_t { return static_cast<uint32_t>(w * 2048 + r * 128); };
+
+  uint32_t qh[KS][2], ql[KS][2];
+  float acc[KS][4];
+  float m0 = NEG_INF, m1 = NEG_INF, l0 = 0.f, l1 = 0.f;
+  int b = b0, rt0 = cum[b0], rt1 = cum[b0 + 1];
+  RowTiles rt = tiles_of(lens[b], p.window, p.sinks);
+  int nseg = 0, stage = 0, round = 0, npart = 0;
+  int part_row[2];
+  bool lost = false;
+  for (int t = t0; t < t1 && !lost; ++t) {
+    const bool next_row = t >= rt1;
+    if (next_row) {
+      do {
+        ++b;
+        rt0 = rt1;
+        rt1 = cum[b + 1];
+      } while (t >= rt1);
+      rt = tiles_of(lens[b], p.window, p.sinks);
+    }
+    if (next_row || t == t0) {
+      if (!mbar_wait(qfull, nseg & 1)) {
+        lost = true;
+        break;
+      }
+      const float* qrow = reinterpret_cast<const float*>(smem + p.q_off) + (w * G + (g4 < G ? g4 : 0)) * D;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        float2 x = make_float2(0.f, 0.f), y = x;
+        if (g4 < G) {
+          x = *reinterpret_cast<const float2*>(qrow + 16 * k + 2 * t4);
+          y = *reinterpret_cast<const float2*>(qrow + 16 * k + 2 * t4 + 8);
+        }
+        split2<E>(x.x, x.y, qh[k][0], ql[k][0]);
+        split2<E>(y.x, y.y, qh[k][1], ql[k][1]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(qempty);
+      ++nseg;
+      m0 = m1 = NEG_INF;
+      l0 = l1 = 0.f;
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
+    }
+    const uint32_t mask = visible16(rt.tile(t - rt0), lens[b], p.window, p.sinks);
+    if (!mbar_wait(full0 + 8 * stage, round & 1)) {
+      lost = true;
+      break;
+    }
+    unsigned char* stg = smem + stage * p.stage_bytes;
+    if (mask != 0xFFFFu) {
+      // rows of V that are not visible (or were not copied) meet P = 0: make them zeros
+      unsigned char* vst = stg + p.stage_bytes / 2;
+      constexpr int CH = D / 8;
+      for (int r = lane / CH; r < kTile; r += 32 / CH) {
+        if ((mask >> r) & 1u) continue;
+        const int ch = lane % CH;
+        *reinterpret_cast<uint4*>(vst + (ch >> 3) * block_bytes + row_off(r) + (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      __syncwarp();
+    }
+
+    // scores: lane holds keys g4 and g4 + 8, heads 2 t4 and 2 t4 + 1
+    float sh[4] = {0.f, 0.f, 0.f, 0.f}, sl[4] = {0.f, 0.f, 0.f, 0.f};
+    {
+      const uint32_t ka = smem_addr(stg) + row_off(ka_row);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4(ka + (k >> 2) * block_bytes + ((((2 * k) & 7) ^ ksw) << 4), a0, a1, a2, a3);
+        E::mma(sh, a0, a1, a2, a3, qh[k][0], qh[k][1]);
+        E::mma(sl, a0, a1, a2, a3, ql[k][0], ql[k][1]);
+      }
+    }
+    const bool va = (mask >> g4) & 1u, vb = (mask >> (g4 + 8)) & 1u;
+    const float s0 = va ? (sh[0] + sl[0]) * p.scale_log2 : NEG_INF;
+    const float s1 = va ? (sh[1] + sl[1]) * p.scale_log2 : NEG_INF;
+    const float s2 = vb ? (sh[2] + sl[2]) * p.scale_log2 : NEG_INF;
+    const float s3 = vb ? (sh[3] + sl[3]) * p.scale_log2 : NEG_INF;
+    float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+    }
+    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+    // (a max of -inf, from keys that hold infinities, is subtracted as 0)
+    const float ms0 = mn0 == NEG_INF ? 0.f : mn0, ms1 = mn1 == NEG_INF ? 0.f : mn1;
+    const float al0 = exp2f(m0 - ms0), al1 = exp2f(m1 - ms1);
+    const float p0 = exp2f(s0 - ms0), p2 = exp2f(s2 - ms0);
+    const float p1 = exp2f(s1 - ms1), p3 = exp2f(s3 - ms1);
+    l0 = l0 * al0 + (p0 + p2);
+    l1 = l1 * al1 + (p1 + p3);
+    m0 = mn0;
+    m1 = mn1;
+    uint32_t ph01, pl01, ph23, pl23;
+    split2<E>(p0, p1, ph01, pl01);
+    split2<E>(p2, p3, ph23, pl23);
+    const uint32_t bh0 = movm_t(ph01), bh1 = movm_t(ph23), bl0 = movm_t(pl01), bl1 = movm_t(pl23);
+    if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        acc[mt][0] *= al0;
+        acc[mt][1] *= al1;
+        acc[mt][2] *= al0;
+        acc[mt][3] *= al1;
+      }
+    }
+    {
+      const uint32_t va0 = smem_addr(stg) + static_cast<uint32_t>(p.stage_bytes / 2) + row_off(va_row);
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        uint32_t a0, a1, a2, a3;
+        ldsm_x4_t(va0 + (mt >> 2) * block_bytes + ((((2 * mt) & 7) ^ vsw) << 4), a0, a1, a2, a3);
+        E::mma(acc[mt], a0, a1, a2, a3, bh0, bh1);
+        E::mma(acc[mt], a0, a1, a2, a3, bl0, bl1);
+      }
+    }
+    if (mask != 0xFFFFu) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty0 + 8 * stage);
+    if (++stage == S) {
+      stage = 0;
+      ++round;
+    }
+
+    // ---- end of this CTA's share of a row: finished output, or a partial one ------
+    if (t + 1 == t1 || t + 1 == rt1) {
+      float L0 = l0, L1 = l1;
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        L0 += __shfl_xor_sync(0xffffffffu, L0, off);
+        L1 += __shfl_xor_sync(0xffffffffu, L1, off);
+      }
+      const int n0 = 2 * t4, n1 = 2 * t4 + 1;
+      if (rt0 >= t0 && rt1 <= t1) {
+        const float il0 = 1.f / L0, il1 = 1.f / L1;
+        uint16_t* o0 = p.out + (static_cast<long long>(b) * p.Hq + static_cast<long long>(h) * G + n0) * D;
+        uint16_t* o1 = o0 + D;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          const int d = mt * 16 + g4;
+          if (n0 < G) {
+            o0[d] = E::bits(acc[mt][0] * il0);
+            o0[d + 8] = E::bits(acc[mt][2] * il0);
+          }
+          if (n1 < G) {
+            o1[d] = E::bits(acc[mt][1] * il1);
+            o1[d + 8] = E::bits(acc[mt][3] * il1);
+          }
+        }
+      } else {
+        // piece slot 0 of a CTA belongs to its first row, slot 1 to a later one
+        const float il0 = L0 > 0.f ? 1.f / L0 : (L0 == 0.f ? 0.f : L0), il1 = L1 > 0.f ? 1.f / L1 : (L1 == 0.f ? 0.f : L1);
+        const long long base = ((static_cast<long long>(gy) * p.N + c) * 2 + (b == b0 ? 0 : 1)) * HG + w * G;
+        float* o0 = p.part_o + (base + n0) * D;
+        float* o1 = o0 + D;
+#pragma unroll
+        for (int mt = 0; mt < KS; ++mt) {
+          const int d = mt * 16 + g4;
+          if (n0 < G) {
+            o0[d] = acc[mt][0] * il0;
+            o0[d + 8] = acc[mt][2] * il0;
+          }
+          if (n1 < G) {
+            o1[d] = acc[mt][1] * il1;
+            o1[d + 8] = acc[mt][3] * il1;
+          }
+        }
+        if (g4 == 0) {
+          if (n0 < G) p.part_lse[base + n0] = m0 + log2f(L0);
+          if (n1 < G) p.part_lse[base + n1] = m1 + log2f(L1);
+        }
+        part_row[npart++ & 1] = b;
+      }
+    }
+  }
+  if (lost) {
+    if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
+    *abort_flag = 1;
+    *reinterpret_cast<volatile int*>(misc + kMiscLost) = 1;
+  }
+
+  // ---- count this CTA's pieces (the consumers agree on which there are) ------------
+  named_sync(1, 32 * Hc);
+  // (only consumers set this one, before the barrier: they all see the same)
+  if (*reinterpret_cast<volatile int*>(misc + kMiscLost) || npart == 0) return;
+  if (tid == 0) {
+    for (int k = 0; k < npart; ++k) {
+      const int rb = part_row[k];
+      const int first = share_of(cum[rb], n_eff, T), last = share_of(cum[rb + 1] - 1, n_eff, T);
+      // acquire-release at GPU scope: publishes this CTA's pieces (ordered before
+      // it by the barrier) and lets the last one see all others
+      int* counter = p.counters + static_cast<long long>(gy) * p.B + rb;
+      const bool mine = atom_add_acq_rel_gpu(counter, 1) == last - first;
+      if (mine) *counter = 0;  // ready for the next call
+      int* v = misc + kMiscPart + 4 * k;
+      v[0] = mine ? 1 : 0;
+      v[1] = first;
+      v[2] = last - first + 1;
+      v[3] = share_begin(first, n_eff, T) == cum[rb] ? 0 : 1;  // the first piece's slot
+    }
+  }
+  named_sync(1, 32 * Hc);
+
+  // ---- the last CTA of a row adds its pieces: warp w those of kv head w -------------
+  for (int k = 0; k < npart; ++k) {
+    const int* v = misc + kMiscPart + 4 * k;
+    if (!v[0]) continue;
+    const int first = v[1], np = v[2], slot0 = v[3];
+    auto piece = [&](int j) -> long long {
+      return ((static_cast<long long>(gy) * p.N + first + j) * 2 + (j == 0 ? slot0 : 0)) * HG + w * G;
+    };
+    float M[G], sum[G], o[G][PER];
+#pragma unroll
+    for (int n = 0; n < G; ++n) {
+      M[n] = NEG_INF;
+      sum[n] = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[n][i] = 0.f;
+    }
+    for (int j0 = 0; j0 < np; j0 += 32) {
+      // 32 pieces a round: lane j has piece j0 + j's weight for every head
+      const int nj = min(32, np - j0);
+      float wt[G];
+#pragma unroll
+      for (int n = 0; n < G; ++n) {
+        const float lse = lane < nj ? __ldcg(p.part_lse + piece(j0 + lane) + n) : NEG_INF;
+        float mx = lse;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        mx = fmaxf(mx, M[n]);
+        const float ms = mx == NEG_INF ? 0.f : mx;
+        const float sc = exp2f(M[n] - ms);
+        M[n] = mx;
+        wt[n] = exp2f(lse - ms);
+        float add = wt[n];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
+        sum[n] = sum[n] * sc + add;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) o[n][i] *= sc;
+      }
+      constexpr int U = G >= 8 ? 1 : (G == 4 ? 2 : 4);  // pieces loaded at a time
+      for (int j = 0; j < nj; j += U) {
+        float x[U][G][PER];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int n = 0; n < G; ++n) {
+            const float* src = p.part_o + (piece(j0 + min(j + u, nj - 1)) + n) * D + lane * PER;
+            if constexpr (PER == 4) {
+              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+              x[u][n][0] = f.x;
+              x[u][n][1] = f.y;
+              x[u][n][2] = f.z;
+              x[u][n][3] = f.w;
+            } else {
+              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+              x[u][n][0] = f.x;
+              x[u][n][1] = f.y;
+            }
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int n = 0; n < G; ++n) {
+            const float f = __shfl_sync(0xffffffffu, wt[n], min(j + u, 31));
+            if (j + u < nj) {
+#pragma unroll
+              for (int i = 0; i < PER; ++i) o[n][i] += f * x[u][n][i];
+            }
+          }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < G; ++n) {
+      const float il = 1.f / sum[n];
+      uint16_t* dst = p.out + (static_cast<long long>(part_row[k]) * p.Hq + static_cast<long long>(h) * G + n) * D + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = E::pack2(o[n][i] * il, o[n][i + 1] * il);
+    }
+  }
+}
+
+template <typename E>
+const void* select_t(int D, int G) {
+  if (D == 128) {
+    switch (G) {
+      case 1: return reinterpret_cast<const void*>(&window_decode_kernel<128, 1, E>);
+      case 2: return reinterpret_cast<const void*>(&window_decode_kernel<128, 2, E>);
+      case 4: return reinterpret_cast<const void*>(&window_decode_kernel<128, 4, E>);
+      case 8: return reinterpret_cast<const void*>(&window_decode_kernel<128, 8, E>);
+    }
+  } else if (D == 64) {
+    switch (G) {
+      case 1: return reinterpret_cast<const void*>(&window_decode_kernel<64, 1, E>);
+      case 2: return reinterpret_cast<const void*>(&window_decode_kernel<64, 2, E>);
+      case 4: return reinterpret_cast<const void*>(&window_decode_kernel<64, 4, E>);
+      case 8: return reinterpret_cast<const void*>(&window_decode_kernel<64, 8, E>);
+    }
+  }
+  return nullptr;
+}
+
+const void* select_kernel(int D, int G, bool f16) {
+  return f16 ? select_t<ElemF16>(D, G) : select_t<ElemBf16>(D, G);
+}
+
+}  // namespace
+
+cudaError_t prepare_window_decode(int max_smem) {
+  for (int D : {64, 128})
+    for (int G : {1, 2, 4, 8})
+      for (bool f16 : {false, true}) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(select_kernel(D, G, f16), cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+        if (e != cudaSuccess) return e;
+      }
+  return cudaSuccess;
+}
+
+cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm) {
+  return cudaOccupancyMaxActiveBlocksPerMultiprocessor(blocks_per_sm, select_kernel(p.D, p.G, p.f16 != 0),
+                                                       32 * (p.Hc + 1), p.smem_bytes);
+}
+
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.N, p.groups);
+  cfg.blockDim = dim3(32 * (p.Hc + 1));
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  void* args[] = {const_cast<WindowDecodeParams*>(&p)};
+  return cudaLaunchKernelExC(&cfg, select_kernel(p.D, p.G, p.f16 != 0), args);
+}
+
+}  // namespace vh
