@@ -375,34 +375,10 @@ def decode_step(q, k_new, v_new, cos_sin, k_cache, v_cache, page_table, seq_lens
     return out
 
 
-def _here(*tensors) -> None:
-    """Every tensor of a call lives on the current device (the launch goes there)."""
-    tensors = [t for t in tensors if t is not None]
-    if not all(t.is_cuda for t in tensors):
-        raise ValueError("every tensor must be a CUDA tensor")
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t.device.index != dev:
-            raise ValueError(f"tensor on cuda:{t.device.index}, but the current device is cuda:{dev}")
-
-
-def _tokens(t: torch.Tensor, heads: int, D: int, dtype, name: str):
-    """(pointer, token stride) of a [T, heads, D] tensor whose tokens may lie apart."""
-    if t.dim() != 3 or t.shape[1:] != (heads, D):
-        raise ValueError(f"{name} must have shape [T, {heads}, {D}]")
-    if t.shape[0] > 1 and t.stride(0) < heads * D or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
-        raise ValueError(f"the heads of one token of {name} must be contiguous")
-    return _ptr(t, dtype, name), t.stride(0) if t.shape[0] > 1 else heads * D
-
-
-def _rows(page_table, seq_lens, active, token_start, B):
-    for t, name in ((seq_lens, "seq_lens"), (active, "active")):
-        if t.shape != (B,):
-            raise ValueError(f"{name} must have shape ({B},)")
-    if token_start is not None and token_start.shape != (B + 1,):
-        raise ValueError(f"token_start must have shape ({B + 1},)")
-    if page_table is not None and (page_table.dim() != 2 or page_table.shape[0] != B):
-        raise ValueError(f"page_table must have shape ({B}, pages per row)")
+# The calls for prompts, several rotary axes and sliding windows are bound in
+# C++ (csrc/bind.cpp): they are short, and taking a dozen tensors apart in
+# Python would cost more than they run.
+from ._vh_bind import vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn  # noqa: E402
 
 
 def mrope_pair_axis(sections, D: int, cyclic: bool = False) -> list[int]:
@@ -421,79 +397,6 @@ def mrope_pair_axis(sections, D: int, cyclic: bool = False) -> list[int]:
     return [i % n if i % n and i // n < sections[i % n] else 0 for i in range(D // 2)]
 
 
-def vh_mrope_kv_append(q, k_new, v_new, cos_sin, k_cache, v_cache, page_table, seq_lens, active, q_rot,
-                       token_start=None, positions=None, pair_axis=None, err_flag=None, q_norm_w=None,
-                       k_norm_w=None, norm_eps: float = 1e-6, interleaved: bool = False, stream=None) -> torch.Tensor:
-    """RoPE with several axes of positions and KV append for T ragged tokens.
-    q [T, Hq, D], k_new, v_new [T, Hkv, D]: the tokens may lie apart (slices of a
-    packed projection).  token_start int32 [B + 1], or None: one token a row.
-    positions int32 [T] or [axes, T], or None (the slot); pair_axis: the axis of
-    each of the D/2 pairs (see mrope_pair_axis), or None (axis 0).  q_rot
-    [T, Hq, D] is float32, or the cache's type (VH_FLAG_Q16).  Returns q_rot."""
-    if q.dim() != 3:
-        raise ValueError("q must have shape [T, Hq, D]")
-    T, Hq, D = q.shape
-    kp, vp, ps, ts, hs, NP, P, Hkv, Dc = _cache_view(k_cache, v_cache)
-    et, B = k_cache.dtype, seq_lens.shape[0]
-    if Dc != D or q_rot.shape != q.shape or k_new.shape[0] != T or v_new.shape[0] != T:
-        raise ValueError("shape mismatch between q, k_new, v_new, q_rot and the cache")
-    if cos_sin.dim() != 2 or cos_sin.shape[1] != D:
-        raise ValueError(f"cos_sin must have shape [max_pos, {D}]")
-    _rows(page_table, seq_lens, active, token_start, B)
-    axes = 1
-    if positions is not None:
-        if positions.shape[-1] != T or positions.dim() > 2:
-            raise ValueError(f"positions must have shape ({T},) or (axes, {T})")
-        axes = positions.shape[0] if positions.dim() == 2 else 1
-    elif pair_axis is not None:
-        axes = max(1, min(4, max(pair_axis) + 1))
-    pa = None
-    if pair_axis is not None:
-        if len(pair_axis) != D // 2 or min(pair_axis) < 0 or max(pair_axis) > 255:
-            raise ValueError(f"pair_axis must hold {D // 2} axes")
-        pa = (ctypes.c_uint8 * (D // 2))(*pair_axis)
-    if q_rot.dtype not in (torch.float32, et):
-        raise TypeError(f"q_rot must be torch.float32 or {et}, got {q_rot.dtype}")
-    _here(q, k_new, v_new, cos_sin, k_cache, v_cache, page_table, seq_lens, active, q_rot, token_start, positions,
-          err_flag, q_norm_w, k_norm_w)
-    (qp, qs), (knp, kns), (vnp, vns) = (_tokens(q, Hq, D, et, "q"), _tokens(k_new, Hkv, D, et, "k_new"),
-                                        _tokens(v_new, Hkv, D, et, "v_new"))
-    _check(lib.vh_mrope_kv_append(
-        qp, knp, vnp, qs, kns, vns, _contig(cos_sin, torch.float32, "cos_sin"), cos_sin.shape[0],
-        None if positions is None else _contig(positions, torch.int32, "positions"), pa, axes,
-        _norm_w(q_norm_w, D, "q_norm_w"), _norm_w(k_norm_w, D, "k_norm_w"), float(norm_eps),
-        kp, vp, ps, ts, hs, NP, *_table(page_table, B, NP),
-        None if token_start is None else _contig(token_start, torch.int32, "token_start"),
-        _contig(seq_lens, torch.int32, "seq_lens"), _contig(active, torch.int32, "active"),
-        _contig(q_rot, q_rot.dtype, "q_rot"),
-        None if err_flag is None else _contig(err_flag, torch.int32, "err_flag"),
-        _elem_flags(k_cache, interleaved) | (VH_FLAG_Q16 if q_rot.dtype == et else 0), T, B, Hq, Hkv, D, P,
-        _stream(stream)), "vh_mrope_kv_append")
-    return q_rot
-
-
-def vh_window_decode_attn(q_rot, k_cache, v_cache, page_table, seq_lens, active, out, workspace, window: int = 0,
-                          sinks: int = 0, sm_scale: float = 0.0, num_ctas: int = 0, err_flag=None, pdl: bool = False,
-                          stream=None) -> torch.Tensor:
-    """Attention of one new token a row (q_rot float32 [B, Hq, D]) over the last
-    `window` cached tokens (0: all) and the first `sinks`, in one launch.
-    `workspace`: from alloc_workspace (zero-filled before its first use).  Returns out."""
-    B, Hq, D = q_rot.shape
-    kp, vp, ps, ts, hs, NP, P, Hkv, Dc = _cache_view(k_cache, v_cache)
-    if Dc != D or out.shape != (B, Hq, D):
-        raise ValueError("shape mismatch between q_rot, out and the cache")
-    _rows(page_table, seq_lens, active, None, B)
-    _here(q_rot, k_cache, v_cache, page_table, seq_lens, active, out, workspace, err_flag)
-    _check(lib.vh_window_decode_attn(
-        _contig(q_rot, torch.float32, "q_rot"), kp, vp, ps, ts, hs, NP, *_table(page_table, B, NP),
-        _contig(seq_lens, torch.int32, "seq_lens"), _contig(active, torch.int32, "active"), int(window), int(sinks),
-        _contig(out, k_cache.dtype, "out"), float(sm_scale), int(num_ctas),
-        _contig(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-        None if err_flag is None else _contig(err_flag, torch.int32, "err_flag"),
-        _elem_flags(k_cache) | (VH_FLAG_PDL if pdl else 0), B, Hq, Hkv, D, P, _stream(stream)), "vh_window_decode_attn")
-    return out
-
-
 def vh_prompt_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
     n = lib.vh_prompt_workspace_bytes(T, B, Hq, Hkv, D)
     if n == 0:
@@ -504,27 +407,3 @@ def vh_prompt_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
 def alloc_prompt_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
     """Device scratch for vh_window_prompt_attn (torch allocation)."""
     return torch.empty(vh_prompt_workspace_bytes(T, B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
-
-
-def vh_window_prompt_attn(q, k_cache, v_cache, page_table, token_start, seq_lens, active, out, workspace,
-                          window: int = 0, sinks: int = 0, sm_scale: float = 0.0, num_splits: int = 0, err_flag=None,
-                          stream=None) -> torch.Tensor:
-    """Attention of T ragged new tokens (q [T, Hq, D] of the cache's type, already
-    rotated) over the cache, which holds their keys and values: each sees the last
-    `window` tokens up to itself (0: all) and the first `sinks`.  `workspace`:
-    from alloc_prompt_workspace.  Returns out."""
-    T, Hq, D = q.shape
-    kp, vp, ps, ts, hs, NP, P, Hkv, Dc = _cache_view(k_cache, v_cache)
-    et, B = k_cache.dtype, seq_lens.shape[0]
-    if Dc != D or out.shape != q.shape:
-        raise ValueError("shape mismatch between q, out and the cache")
-    _rows(page_table, seq_lens, active, token_start, B)
-    _here(q, k_cache, v_cache, page_table, token_start, seq_lens, active, out, workspace, err_flag)
-    _check(lib.vh_window_prompt_attn(
-        _contig(q, et, "q"), kp, vp, ps, ts, hs, NP, *_table(page_table, B, NP),
-        _contig(token_start, torch.int32, "token_start"), _contig(seq_lens, torch.int32, "seq_lens"),
-        _contig(active, torch.int32, "active"), int(window), int(sinks), _contig(out, et, "out"), float(sm_scale),
-        int(num_splits), _contig(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
-        None if err_flag is None else _contig(err_flag, torch.int32, "err_flag"),
-        _elem_flags(k_cache), T, B, Hq, Hkv, D, P, _stream(stream)), "vh_window_prompt_attn")
-    return out

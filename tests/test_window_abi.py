@@ -129,7 +129,7 @@ def binding_args(op):
     ("append", dict(k_new=torch.zeros(4, 2, 64)), "mismatch"), ("append", dict(q_rot=torch.zeros(5, 4, 32)), "mismatch"),
     ("append", dict(positions=torch.zeros(3, 4, dtype=torch.int32)), "positions"), ("append", dict(pair_axis=[0] * 31), "pair_axis"),
     ("append", dict(token_start=torch.zeros(3, dtype=torch.int32)), "token_start"), ("append", dict(cos_sin=torch.zeros(8, 32)), "cos_sin"),
-    ("decode", dict(seq_lens=torch.zeros(2, dtype=torch.int32)), "seq_lens"), ("decode", dict(out=torch.zeros(3, 4, 32)), "mismatch"),
+    ("decode", dict(seq_lens=torch.zeros(2, dtype=torch.int32)), "active"), ("decode", dict(out=torch.zeros(3, 4, 32)), "mismatch"),
     ("prompt", dict(active=torch.zeros(2, dtype=torch.int32)), "active"), ("prompt", dict(page_table=torch.zeros(2, 2)), "page_table"),
     ("prompt", dict(out=torch.zeros(4, 4, 64)), "mismatch"),
     ("append", {}, "CUDA"), ("decode", {}, "CUDA"), ("prompt", {}, "CUDA"),       # host tensors
