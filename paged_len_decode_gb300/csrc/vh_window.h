@@ -67,7 +67,19 @@ struct WindowDecodeParams {
   int q_off, cum_off, len_off, bar_off, smem_bytes;
 };
 
+// The prompt kernel's ring of K and V stages and its shared memory: the
+// queries of both row tiles, the stages, and up to 1024 bytes to align them.
+constexpr int kPromptRows = 256;  // (token, head) rows of a block
+template <int D>
+constexpr int kPromptStages = D == 128 ? 5 : 8;
+template <int D>
+constexpr int kPromptSmem = (2 + kPromptStages<D>) * 128 * D * 2 + 1024;
+
 struct PromptParams {
+  // queries as a 3-D tensor (head_dim, q head, token), boxes of 64 x G x 128/G;
+  // K and V as 4-D tensors (see vh_kernels.h), boxes of 64 x `box` tokens x 1 head
+  CUtensorMap tmap_q, tmap_k, tmap_v;
+  int tm_tok_dim, box;
   const uint16_t* q;           // [T][Hq][D]
   const uint16_t* k_cache;
   const uint16_t* v_cache;
@@ -84,12 +96,17 @@ struct PromptParams {
   int32_t* err_flag;
   int f16;
   int T, B, Hq, Hkv, D, G, P;
+  int blocks;                  // T / (256 / G) + B: an upper bound (rows fill their last block partly)
+  int splits;                  // CTAs that share the keys of a block
+  float* part_o;               // [blocks][Hkv][splits][256][D], if splits > 1
+  float* part_lse;             // [blocks][Hkv][splits][256], base 2
 };
 
 cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl);
+cudaError_t prepare_window_prompt();  // once per device, every variant
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace vh

@@ -8,6 +8,8 @@
 #include <mutex>
 #include <unordered_map>
 
+#include <cudaTypedefs.h>  // PFN_cuTensorMapEncodeTiled
+
 #include "../../include/vh.h"
 #include "vh_plan.h"
 #include "vh_window.h"
@@ -37,7 +39,7 @@ Prepared g_prepared[kMaxDevices];
 bool prepared(const DeviceInfo& dev) {
   Prepared& s = g_prepared[dev.index];
   std::call_once(s.once, [&]() {
-    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess;
+    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt() == cudaSuccess;
     if (!s.ok) cudaGetLastError();
   });
   return s.ok;
@@ -154,6 +156,69 @@ bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int6
 
 bool aligned_cache(const void* k, const void* v, int64_t page_stride, int64_t token_stride, int64_t head_stride) {
   return aligned16(k) && aligned16(v) && page_stride % 8 == 0 && token_stride % 8 == 0 && head_stride % 8 == 0;
+}
+
+// The driver's tensor-map encoder, looked up once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    cudaGetLastError();
+    return nullptr;
+  }();
+  return fn;
+}
+
+bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
+                    box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Tensor maps of the prompt kernel.  A K or V box is a run of tokens that
+// never crosses a page and divides a key tile of 128: all 128, or the largest
+// power of two in the page size (a row's only page may end inside the box).
+bool encode_prompt_maps(vh::PromptParams& p) {
+  int box = 128;
+  if (p.max_pages_per_seq > 1)
+    while (p.P % box != 0) box /= 2;
+  p.box = box;
+  auto dim = [](long long x) { return static_cast<cuuint64_t>(x); };
+  {
+    const cuuint64_t dims[3] = {dim(p.D), dim(p.Hq), dim(p.T)}, strides[2] = {dim(2LL * p.D), dim(2LL * p.D * p.Hq)};
+    const cuuint32_t b[3] = {64, static_cast<cuuint32_t>(p.G), static_cast<cuuint32_t>(128 / p.G)};
+    if (!encode(&p.tmap_q, p.q, 3, dims, strides, b)) return false;
+  }
+  // token before head; if the encoder refuses strides in that order, head before token
+  for (p.tm_tok_dim = 1; p.tm_tok_dim <= 2; ++p.tm_tok_dim) {
+    const bool tf = p.tm_tok_dim == 1;
+    const cuuint64_t dims[4] = {dim(p.D), dim(tf ? p.P : p.Hkv), dim(tf ? p.Hkv : p.P), dim(p.num_pages)};
+    const cuuint64_t strides[3] = {dim(2 * (tf ? p.token_stride : p.head_stride)),
+                                   dim(2 * (tf ? p.head_stride : p.token_stride)), dim(2 * p.page_stride)};
+    const cuuint32_t b[4] = {64, static_cast<cuuint32_t>(tf ? box : 1), static_cast<cuuint32_t>(tf ? 1 : box), 1};
+    if (encode(&p.tmap_k, p.k_cache, 4, dims, strides, b) && encode(&p.tmap_v, p.v_cache, 4, dims, strides, b)) return true;
+  }
+  return false;
+}
+
+// Blocks of the prompt kernel (an upper bound) and the CTAs that share a
+// block's keys: as many as fill the SMs once.
+long long prompt_blocks(int T, int B, int Hq, int Hkv) {
+  return static_cast<long long>(T) / (vh::kPromptRows / (Hq / Hkv)) + B;
+}
+
+int prompt_splits(int T, int B, int Hq, int Hkv, const DeviceInfo& dev) {
+  return static_cast<int>(std::max(1LL, std::min(64LL, dev.sm_count / (prompt_blocks(T, B, Hq, Hkv) * Hkv))));
+}
+
+size_t prompt_split_bytes(int T, int B, int Hq, int Hkv, int D) {
+  return static_cast<size_t>(prompt_blocks(T, B, Hq, Hkv)) * Hkv * vh::kPromptRows * (static_cast<size_t>(D) + 1) * 4;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? VH_OK : VH_ECUDA; }
@@ -298,8 +363,11 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
 }
 
 size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
-  if (T < 0 || !valid_shape(B, Hq, Hkv, D, 16) || !device_info()) return 0;
-  return 256;
+  if (T < 0 || !valid_shape(B, Hq, Hkv, D, 16)) return 0;
+  const DeviceInfo* dev = device_info();
+  if (!dev) return 0;
+  const int splits = prompt_splits(T, B, Hq, Hkv, *dev);
+  return 256 + (splits > 1 ? splits * prompt_split_bytes(T, B, Hq, Hkv, D) : 0);
 }
 
 int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
@@ -349,6 +417,18 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
   p.D = D;
   p.G = Hq / Hkv;
   p.P = page_size;
+  const long long blocks = prompt_blocks(T, B, Hq, Hkv);
+  if (Hkv > 65535 || !encode_prompt_maps(p)) return VH_EINVAL;
+  p.blocks = static_cast<int>(blocks);
+  const size_t per = prompt_split_bytes(T, B, Hq, Hkv, D);
+  p.splits = num_splits > 0 ? num_splits : prompt_splits(T, B, Hq, Hkv, *dev);
+  p.splits = static_cast<int>(std::min<size_t>(p.splits, std::max<size_t>(1, workspace_bytes / per)));
+  // no more CTAs than a block can have key tiles
+  const long long longest = std::min<long long>(static_cast<long long>(max_pages_per_seq) * page_size,
+                                                static_cast<long long>(p.window) + vh::kPromptRows);
+  p.splits = static_cast<int>(std::min<long long>(p.splits, longest / 128 + 2 + p.sinks / 128));
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = p.part_o + static_cast<size_t>(blocks) * Hkv * p.splits * vh::kPromptRows * D;
   return status_of(vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));
 }
 
