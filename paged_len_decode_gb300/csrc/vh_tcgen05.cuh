@@ -50,13 +50,34 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
       : "memory");
 }
 
+// the same for 8 columns (little register use, off the common path)
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// One lane of the warp, the same in every call (the warp is converged).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Shared-memory operand, rows of 128 bytes under the 128-byte swizzle (8-row
-// atoms of 1024 bytes).  Contraction along the row (K-major): `next8` bytes
-// from 8 rows to the next 8, `block` unused.  Contraction down the rows
-// (MN-major): `next8` as before, `block` bytes from 64 elements to the next 64.
-__device__ __forceinline__ uint64_t tc_operand(uint32_t addr, uint32_t block, uint32_t next8) {
-  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) |
-         (static_cast<uint64_t>(next8 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// atoms of 1024 bytes, one after the other).  Contraction along the row
+// (K-major): `block` unused.  Contraction down the rows (MN-major): `block`
+// bytes from 64 elements to the next 64.  The low word holds the address in
+// units of 16 bytes, so a step through the operand is an addition to it; the
+// high word is the same for all.
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t tc_operand(uint32_t addr, uint32_t block) {
+  return ((addr & 0x3FFFFu) >> 4) | ((block >> 4) << 16);
 }
 
 // Instruction descriptor of kind::f16 with fp32 accumulators: A rows M, B
@@ -67,20 +88,28 @@ __host__ __device__ constexpr uint32_t tc_kind_f16(int M, int N, bool bf16, bool
 }
 
 // d (+)= a b, one k-step of 16; issued by one thread.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
       : "memory");
 }
 // the same with a in tensor memory
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint64_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(kind), "r"(static_cast<uint32_t>(add))
+      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
       : "memory");
+}
+
+// d = a + b on two fp32 lanes at once.
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+  unsigned long long ra = (static_cast<unsigned long long>(__float_as_uint(a.y)) << 32) | __float_as_uint(a.x);
+  unsigned long long rb = (static_cast<unsigned long long>(__float_as_uint(b.y)) << 32) | __float_as_uint(b.x), rd;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+  return make_float2(__uint_as_float(static_cast<uint32_t>(rd)), __uint_as_float(static_cast<uint32_t>(rd >> 32)));
 }
 
 // Tiled tensor copy of one 3-D box (see tma_load_4d).

@@ -73,7 +73,10 @@ constexpr int kPromptRows = 256;  // (token, head) rows of a block
 template <int D>
 constexpr int kPromptStages = D == 128 ? 5 : 8;
 template <int D>
-constexpr int kPromptSmem = (2 + kPromptStages<D>) * 128 * D * 2 + 1024;
+constexpr int kPromptQueries = D == 128 ? 1 : 2;  // blocks of queries held at a time
+template <int D>
+constexpr int kPromptSmem = (2 * kPromptQueries<D> + kPromptStages<D>) * 128 * D * 2 + 1024;
+constexpr int kPromptUnits = 20;  // most (block, kv head, split) units of a CTA
 
 struct PromptParams {
   // queries as a 3-D tensor (head_dim, q head, token), boxes of 64 x G x 128/G;
@@ -98,6 +101,7 @@ struct PromptParams {
   int T, B, Hq, Hkv, D, G, P;
   int blocks;                  // T / (256 / G) + B: an upper bound (rows fill their last block partly)
   int splits;                  // CTAs that share the keys of a block
+  int ctas;
   float* part_o;               // [blocks][Hkv][splits][256][D], if splits > 1
   float* part_lse;             // [blocks][Hkv][splits][256], base 2
 };

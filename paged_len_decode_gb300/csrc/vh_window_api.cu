@@ -427,6 +427,9 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
   const long long longest = std::min<long long>(static_cast<long long>(max_pages_per_seq) * page_size,
                                                 static_cast<long long>(p.window) + vh::kPromptRows);
   p.splits = static_cast<int>(std::min<long long>(p.splits, longest / 128 + 2 + p.sinks / 128));
+  // one CTA an SM, or whole rounds of them where a CTA could not list its units
+  const long long units = blocks * Hkv * p.splits, round = static_cast<long long>(dev->sm_count) * vh::kPromptUnits;
+  p.ctas = static_cast<int>(std::min(units, dev->sm_count * ((units + round - 1) / round)));
   p.part_o = static_cast<float*>(workspace);
   p.part_lse = p.part_o + static_cast<size_t>(blocks) * Hkv * p.splits * vh::kPromptRows * D;
   return status_of(vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));

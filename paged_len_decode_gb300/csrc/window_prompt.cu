@@ -21,7 +21,9 @@
 //    A tile that one of the two row tiles does not see is skipped for it.
 //  * Warps: two warpgroups for the softmax of a row tile each (a thread owns a
 //    row, so its maximum and sum need no exchange), one warp that issues the
-//    products, one that copies K and V through a ring of stages.
+//    products, one that copies K and V through a ring of stages.  A CTA works
+//    through several blocks; the copies of the next one run while the last
+//    products and outputs of this one are under way.
 //  * Softmax.  Running maximum and sum in fp32; the accumulator is rescaled
 //    only when a row's maximum has grown by more than 2^8 since the last time
 //    (weights stay below 2^8, far inside fp32, bf16 and fp16), so it is rare.
@@ -45,7 +47,8 @@ namespace {
 
 constexpr int kRows = 128;       // rows of a row tile
 constexpr int kKeys = 128;       // keys of a key tile
-constexpr int kThreads = 320;    // two softmax warpgroups, product warp, copy warp
+constexpr int kThreads = 384;    // two softmax warpgroups, and one whose warps issue products and copies
+constexpr int kProductWarp = 8, kCopyWarp = 9;  // (K and queries; the next one V)
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
@@ -88,52 +91,99 @@ __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
   return below(above) & (~below(low) | below(sink));
 }
 
-// One query by one warp, over the visible keys of the block's tiles [k0, k1)
-// alone: lanes over head_dim, keys one at a time.  For rows that a value they
-// do not see has reached (0 times infinity).  o: the lane's D / 32 elements.
-template <typename E, int D>
-__device__ __noinline__ void attend_alone(const PromptParams& p, const Block& blk, int k0, int k1, int h, int i,
-                                          const uint16_t* q, float (&o)[D / 32], float& m, float& l) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31;
-  const float NEG_INF = __int_as_float(0xff800000);
-  float qf[PER];
-#pragma unroll
-  for (int e = 0; e < PER; e += 2) {
-    const float2 w = E::to_float2(*reinterpret_cast<const uint32_t*>(q + lane * PER + e));
-    qf[e] = w.x;
-    qf[e + 1] = w.y;
-  }
-  m = NEG_INF;
-  l = 0.f;
-#pragma unroll
-  for (int e = 0; e < PER; ++e) o[e] = 0.f;
-  for (int k = k0; k < k1; ++k) {
-    const int j0 = blk.tile(k) * kKeys;
-    for (int j = j0; j < j0 + kKeys && j <= i; ++j) {
-      if (j >= p.sinks && i - j >= p.window) continue;
-      const long long lp = static_cast<long long>(blk.row) * p.max_pages_per_seq + j / p.P;
-      const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-      const bool ok = page >= 0 && page < p.num_pages;
-      const long long off = ok ? page * p.page_stride + (j % p.P) * p.token_stride + h * p.head_stride + lane * PER : 0;
-      float s = 0.f, v[PER];
-#pragma unroll
-      for (int e = 0; e < PER; e += 2) {
-        const float2 kk = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.k_cache + off + e)) : make_float2(0.f, 0.f);
-        const float2 vv = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.v_cache + off + e)) : make_float2(0.f, 0.f);
-        s += qf[e] * kk.x + qf[e + 1] * kk.y;
-        v[e] = vv.x;
-        v[e + 1] = vv.y;
+// One CTA's work: a block's queries for one kv head, and a share of its key tiles.
+struct Unit {
+  Block blk;
+  int h, bi, z;
+  int k0, k1;  // k0 == k1: nothing to do
+};
+
+// Unit u of the grid, by one warp.  The rows of inactive and flagged requests
+// are written as zeros here.
+__device__ __forceinline__ Unit unit_of(const PromptParams& p, long long u, int lane) {
+  Unit r{};
+  r.z = static_cast<int>(u % p.splits);
+  const long long v = u / p.splits;
+  r.h = static_cast<int>(v % p.Hkv);
+  // heavy blocks (long contexts, under a causal mask) first
+  r.bi = p.blocks - 1 - static_cast<int>(v / p.Hkv);
+  r.blk = block_of(p, r.bi, lane, lane == 0 && r.h == 0 && r.z == 0);
+  if (r.blk.ntok <= 0) return r;
+  if (!r.blk.ok) {
+    if (r.z == 0)
+      for (int t = 0; t < r.blk.ntok; ++t) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((r.blk.first + t) * static_cast<long long>(p.Hq) + r.h * p.G) * p.D);
+        for (int x = lane; x < p.G * p.D / 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
       }
+    return r;
+  }
+  const int splits = min(p.splits, r.blk.count);
+  if (r.z < splits) {
+    r.k0 = share_begin(r.z, splits, r.blk.count);
+    r.k1 = share_begin(r.z + 1, splits, r.blk.count);
+  }
+  return r;
+}
+
+// The rows `rows` (bits) of this warp's 32, one after the other by the whole
+// warp, over the keys that they see among the unit's tiles, one at a time: for
+// rows that a value they do not see has reached (0 times infinity).  Lanes over
+// head_dim.  Out of line, so that the common path keeps its registers.
+template <typename E, int D>
+__device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, int m, uint32_t rows) {
+  constexpr int PER = D / 32;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
+  const float NEG_INF = __int_as_float(0xff800000);
+  while (rows) {
+    const int r = warp * 32 + __ffs(rows) - 1;
+    rows &= rows - 1;
+    const int token = m * (kRows / p.G) + r / p.G, i = u.blk.slot + token;
+    const long long at = ((u.blk.first + token) * static_cast<long long>(p.Hq) + u.h * p.G + r % p.G) * D + lane * PER;
+    float q[PER], o[PER], top = NEG_INF, sum = 0.f;
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-      s *= p.scale_log2;
-      const float mn = fmaxf(m, s), ms = mn == NEG_INF ? 0.f : mn;
-      const float al = exp2f(m - ms), w = exp2f(s - ms);
-      m = mn;
-      l = l * al + w;
+    for (int e = 0; e < PER; e += 2) {
+      const float2 w = E::to_float2(*reinterpret_cast<const uint32_t*>(p.q + at + e));
+      q[e] = w.x;
+      q[e + 1] = w.y;
+      o[e] = o[e + 1] = 0.f;
+    }
+    for (int k = u.k0; k < u.k1; ++k) {
+      const int j0 = u.blk.tile(k) * kKeys;
+      for (int j = j0; j < j0 + kKeys && j <= i; ++j) {
+        if (j >= p.sinks && i - j >= p.window) continue;
+        const long long lp = static_cast<long long>(u.blk.row) * p.max_pages_per_seq + j / p.P;
+        const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
+        const bool ok = page >= 0 && page < p.num_pages;
+        const long long off = ok ? page * p.page_stride + (j % p.P) * p.token_stride + u.h * p.head_stride + lane * PER : 0;
+        float s = 0.f, v[PER];
 #pragma unroll
-      for (int e = 0; e < PER; ++e) o[e] = o[e] * al + w * v[e];
+        for (int e = 0; e < PER; e += 2) {
+          const float2 kk = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.k_cache + off + e)) : make_float2(0.f, 0.f);
+          const float2 vv = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.v_cache + off + e)) : make_float2(0.f, 0.f);
+          s += q[e] * kk.x + q[e + 1] * kk.y;
+          v[e] = vv.x;
+          v[e + 1] = vv.y;
+        }
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+        s *= p.scale_log2;
+        const float now = fmaxf(top, s), shift = now == NEG_INF ? 0.f : now;
+        const float by = exp2f(top - shift), w = exp2f(s - shift);
+        top = now;
+        sum = sum * by + w;
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[e] = o[e] * by + w * v[e];
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    if (p.splits > 1) {
+      const long long part = ((static_cast<long long>(u.bi) * p.Hkv + u.h) * p.splits + u.z) * (2 * kRows) + m * kRows + r;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) p.part_o[part * D + lane * PER + e] = o[e] * inv;
+      if (lane == 0) p.part_lse[part] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+    } else {
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(p.out + at + e) = E::pack2(o[e] * inv, o[e + 1] * inv);
     }
   }
 }
@@ -145,313 +195,349 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   constexpr uint32_t kQTile = kRows * D * 2;   // bytes of a row tile's queries: [D/64][128 rows][128 B]
   constexpr uint32_t kStage = kKeys * D * 2;   // bytes of K or V of a key tile, likewise
   constexpr uint32_t kBlockBytes = kKeys * 128;  // one 64-element column block
-  constexpr int ST = kPromptStages<D>;
+  constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
   constexpr uint32_t kScores = tc_kind_f16(kRows, kKeys, !E::kF16, false);
   constexpr uint32_t kValues = tc_kind_f16(kRows, D, !E::kF16, true);
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ uint64_t s_bars[2 * ST + 7];
+  __shared__ Unit s_units[kPromptUnits];
+  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 8];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y;
-  // heavy blocks (long contexts, under a causal mask) first
-  const int bi = gridDim.x - 1 - blockIdx.x;
-  const Block blk = block_of(p, bi, lane, warp == 0 && lane == 0 && h == 0 && blockIdx.z == 0);
-  if (blk.ntok <= 0) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per_tile = kRows / p.G;  // tokens of a row tile
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
-  if (!blk.ok) {
-    if (blockIdx.z == 0)
-      for (int t = 0; t < blk.ntok; ++t) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + (blk.first + t) * tok_stride + static_cast<long long>(h) * p.G * D);
-        for (int x = tid; x < p.G * D / 8; x += kThreads) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    return;
-  }
-  const int splits = min(p.splits, blk.count);
-  if (static_cast<int>(blockIdx.z) >= splits) return;
-  const int k0 = share_begin(blockIdx.z, splits, blk.count), k1 = share_begin(blockIdx.z + 1, splits, blk.count);
-  const int last = blk.slot + blk.ntok - 1;      // slot of the last query
-  const int low = max(0, blk.slot - p.window + 1);  // first key of the first query's window
-  // row tile m sees key tile t?
-  auto sees = [&](int m, int t) -> bool {
-    const int f = blk.slot + m * per_tile;
-    if (f > last) return false;
-    const int e = min(last, f + per_tile - 1);
-    return t <= e / kKeys && (t < blk.sink_tiles || t >= max(0, f - p.window + 1) / kKeys);
-  };
-  // some query of the block sees slot j?
-  auto seen = [&](int j) -> bool { return j <= last && (j < p.sinks || j >= low); };
+  const long long units = static_cast<long long>(p.blocks) * p.Hkv * p.splits;
+  const int mine = static_cast<int>((units - blockIdx.x + gridDim.x - 1) / gridDim.x);  // <= kPromptUnits
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base, sKV = base + 2 * kQTile;
+  const uint32_t sQ = base, sKV = base + QB * 2 * kQTile;
   const uint32_t bars = smem_addr(s_bars);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (ST + s); };
-  const uint32_t q_full = bars + 8 * (2 * ST);
-  auto s_full = [&](int m) { return bars + 8 * (2 * ST + 1 + m); };
-  auto p_full = [&](int m) { return bars + 8 * (2 * ST + 3 + m); };
-  auto o_full = [&](int m) { return bars + 8 * (2 * ST + 5 + m); };
+  auto q_full = [&](int b) { return bars + 8 * (2 * ST + b); };
+  auto q_empty = [&](int b) { return bars + 8 * (2 * ST + QB + b); };
+  auto s_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + m); };
+  auto p_full = [&](int m, int half) { return bars + 8 * (2 * ST + 2 * QB + 2 + 2 * m + half); };
+  auto o_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 6 + m); };
   volatile int* abort_flag = &s_abort;
+  for (int n = warp; n < mine; n += kThreads / 32) {
+    const Unit u = unit_of(p, blockIdx.x + static_cast<long long>(n) * gridDim.x, lane);
+    if (lane == 0) s_units[n] = u;
+  }
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < ST; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    mbar_init(q_full, 1);
+    for (int b = 0; b < QB; ++b) {
+      mbar_init(q_full(b), 1);
+      mbar_init(q_empty(b), 1);
+    }
     for (int m = 0; m < 2; ++m) {
       mbar_init(s_full(m), 1);
-      mbar_init(p_full(m), kRows);
+      mbar_init(p_full(m, 0), kRows);
+      mbar_init(p_full(m, 1), kRows);
       mbar_init(o_full(m), 1);
     }
     fence_barrier_init();
   }
-  if (warp == 8) tmem_alloc(smem_addr(&s_tmem), kTmem);
+  if (warp == kProductWarp) tmem_alloc(smem_addr(&s_tmem), kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   auto t_scores = [&](int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
   auto t_out = [&](int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
+  // row tile m of the block sees key tile t?
+  auto sees = [&](const Block& b, int m, int t) -> bool {
+    const int last = b.slot + b.ntok - 1, f = b.slot + m * per_tile;
+    if (f > last) return false;
+    const int e = min(last, f + per_tile - 1);
+    return t <= e / kKeys && (t < b.sink_tiles || t >= max(0, f - p.window + 1) / kKeys);
+  };
   auto give_up = [&]() {
     if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
     *abort_flag = 1;
   };
 
-  if (warp == 9) {
-    // ======================= copies ==============================================
-    const int ntile = blk.ntok > per_tile ? 2 : 1;
-    if (lane == 0) {
-      prefetch_tensormap(&p.tmap_k);
-      prefetch_tensormap(&p.tmap_v);
-      mbar_arrive_expect_tx(q_full, static_cast<uint32_t>(ntile) * kQTile);
-      for (int m = 0; m < ntile; ++m)
-        for (int hf = 0; hf < HALVES; ++hf)
-          tma_load_3d(sQ + m * kQTile + hf * kBlockBytes, &p.tmap_q, hf * 64, h * p.G, blk.first + m * per_tile, q_full);
-    }
-    const int nbox = kKeys / p.box;
-    int issued = 0;
-    bool lost = false;
-    for (int k = k0; k < k1 && !lost; ++k) {
-      const int j0 = blk.tile(k) * kKeys;
-      // page and first token of this lane's box (at most 16 boxes a tile)
-      int page = p.num_pages, tok = 0;
-      if (lane < nbox) {
-        const int j = j0 + lane * p.box;
-        if (j <= last && (j < p.sinks || j + p.box > low)) {
-          const long long lp = static_cast<long long>(blk.row) * p.max_pages_per_seq + j / p.P;
-          page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-          tok = j % p.P;
-          if (page < 0 || page >= p.num_pages) {
-            flag_error(p.err_flag, VH_ERR_PAGE);
-            page = p.num_pages;
+  if (warp >= kProductWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    const bool leader = elect_one();
+    if (warp == kCopyWarp || warp == kCopyWarp + 1) {
+      // ======================= copies: K and the queries, and V =======================
+      // tile number x of all units: K is stage 2 x of the ring, V the next one
+      const int kv = warp - kCopyWarp;
+      const void* map = kv ? static_cast<const void*>(&p.tmap_v) : static_cast<const void*>(&p.tmap_k);
+      if (leader) {
+        if (kv == 0) prefetch_tensormap(&p.tmap_q);
+        prefetch_tensormap(map);
+      }
+      const int nbox = kKeys / p.box;
+      int issued = kv, nq = 0;  // number in the ring, blocks of queries
+      bool lost = false;
+      for (int n = 0; n < mine && !lost; ++n) {
+        const Unit& u = s_units[n];
+        const Block& blk = u.blk;
+        if (u.k0 == u.k1) continue;
+        const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
+        for (int k = u.k0; k < u.k1 && !lost; ++k, issued += 2) {
+          const int j0 = blk.tile(k) * kKeys;
+          // page and first token of this lane's box (at most 16 boxes a tile)
+          int page = p.num_pages, tok = 0;
+          if (lane < nbox) {
+            const int j = j0 + lane * p.box;
+            if (j <= last && (j < p.sinks || j + p.box > low)) {
+              const long long lp = static_cast<long long>(blk.row) * p.max_pages_per_seq + j / p.P;
+              page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
+              tok = j % p.P;
+              if (page < 0 || page >= p.num_pages) {
+                flag_error(p.err_flag, VH_ERR_PAGE);
+                page = p.num_pages;
+              }
+            }
           }
-        }
-      }
-      for (int kv = 0; kv < 2; ++kv, ++issued) {
-        const int s = issued % ST;
-        if (issued >= ST && !mbar_wait(empty(s), ((issued / ST) - 1) & 1)) {
-          give_up();
-          lost = true;
-          break;
-        }
-        if (*abort_flag) {
-          lost = true;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(full(s), kStage);
-        __syncwarp();
-        if (lane < nbox) {
-          const void* map = kv ? static_cast<const void*>(&p.tmap_v) : static_cast<const void*>(&p.tmap_k);
-          const int c1 = p.tm_tok_dim == 1 ? tok : h, c2 = p.tm_tok_dim == 1 ? h : tok;
-#pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            tma_load_4d(sKV + s * kStage + hf * kBlockBytes + lane * p.box * 128, map, hf * 64, c1, c2, page, full(s));
-        }
-      }
-    }
-    if (lost) {
-      // copies in flight land before the shared memory goes away
-      for (int x = max(0, issued - ST); x < issued; ++x) (void)mbar_wait(full(x % ST), (x / ST) & 1);
-      (void)mbar_wait(q_full, 0);
-    }
-  } else if (warp == 8) {
-    // ======================= products =============================================
-    // a key tile's K is stage 2 (k - k0) of the ring, its V the next one
-    int done_p[2] = {0, 0};
-    bool lost = !mbar_wait(q_full, 0) || !mbar_wait(full(0), 0);
-    auto scores = [&](int m, int k) {
-      if (lane != 0) return;
-      const uint32_t kb = sKV + ((2 * (k - k0)) % ST) * kStage, qb = sQ + m * kQTile;
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        const uint32_t off = (s >> 2) * kBlockBytes + (s & 3) * 32;
-        tc_mma(t_scores(m), tc_operand(qb + off, 16, 1024), tc_operand(kb + off, 16, 1024), kScores, s > 0);
-      }
-      tc_commit(s_full(m));
-    };
-    if (!lost) {
-      tc_fence_after();
-      for (int m = 0; m < 2; ++m)
-        if (sees(m, blk.tile(k0))) scores(m, k0);
-      if (lane == 0) tc_commit(empty(0));
-    }
-    for (int k = k0; k < k1 && !lost; ++k) {
-      const int vi = 2 * (k - k0) + 1, t = blk.tile(k);
-      if (!mbar_wait(full(vi % ST), (vi / ST) & 1)) {
-        lost = true;
-        break;
-      }
-      const uint32_t vb = sKV + (vi % ST) * kStage;
-      if (!(seen(t * kKeys) && seen(t * kKeys + kKeys - 1) && (t * kKeys >= low || t * kKeys + kKeys <= p.sinks))) {
-        // slots that nobody sees may hold anything: their values become zeros
-        for (int r = lane / 8; r < kKeys; r += 4) {
-          if (seen(t * kKeys + r)) continue;
-#pragma unroll
-          for (int hf = 0; hf < HALVES; ++hf)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
-                         "r"(0u)
-                         : "memory");
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      const bool more = k + 1 < k1;
-      if (more && !mbar_wait(full((vi + 1) % ST), ((vi + 1) / ST) & 1)) {
-        lost = true;
-        break;
-      }
-      for (int m = 0; m < 2 && !lost; ++m) {
-        if (sees(m, t)) {
-          if (!mbar_wait(p_full(m), done_p[m] & 1)) {
+          const int s = issued % ST;
+          if ((issued >= ST && !mbar_wait(empty(s), ((issued / ST) - 1) & 1)) || *abort_flag) {
             lost = true;
             break;
           }
-          tc_fence_after();
-          if (lane == 0) {
+          if (leader) mbar_arrive_expect_tx(full(s), kStage);
+          for (int x = 0; x < nbox; ++x) {
+            const int pg = __shfl_sync(0xffffffffu, page, x), tk = __shfl_sync(0xffffffffu, tok, x);
+            if (leader) {
+              const int c1 = p.tm_tok_dim == 1 ? tk : u.h, c2 = p.tm_tok_dim == 1 ? u.h : tk;
+              const uint32_t dst = sKV + s * kStage + x * p.box * 128;
 #pragma unroll
-            for (int s = 0; s < kKeys / 16; ++s)
-              tc_mma_ta(t_out(m), t_scores(m) + s * 8, tc_operand(vb + s * 2048, kBlockBytes, 1024), kValues,
-                        done_p[m] > 0 || s > 0);
+              for (int hf = 0; hf < HALVES; ++hf) tma_load_4d(dst + hf * kBlockBytes, map, hf * 64, c1, c2, pg, full(s));
+            }
           }
-          ++done_p[m];
+          if (k == u.k0 && kv == 0) {
+            // the block's queries, once the products of the block that had
+            // their place have read it (its first keys are on their way already)
+            const int b = nq % QB, ntile = blk.ntok > per_tile ? 2 : 1;
+            if (nq >= QB && !mbar_wait(q_empty(b), ((nq / QB) - 1) & 1)) {
+              lost = true;
+              issued += 2;
+              break;
+            }
+            if (leader) {
+              mbar_arrive_expect_tx(q_full(b), static_cast<uint32_t>(ntile) * kQTile);
+              for (int m = 0; m < ntile; ++m)
+                for (int hf = 0; hf < HALVES; ++hf)
+                  tma_load_3d(sQ + (2 * b + m) * kQTile + hf * kBlockBytes, &p.tmap_q, hf * 64, u.h * p.G,
+                              blk.first + m * per_tile, q_full(b));
+            }
+            ++nq;
+          }
         }
-        if (more && sees(m, blk.tile(k + 1))) scores(m, k + 1);
-        if (m == 0 && lane == 0 && !more) tc_commit(o_full(0));
       }
-      if (!lost && lane == 0) {
-        tc_commit(empty(vi % ST));
-        if (more) tc_commit(empty((vi + 1) % ST));
-        else tc_commit(o_full(1));
+      if (lost) {
+        give_up();
+        // copies in flight land before the shared memory goes away
+        for (int x = max(kv, issued - 2 * ST); x < issued; x += 2)
+          if (x + ST >= issued) (void)mbar_wait(full(x % ST), (x / ST) & 1);
+        for (int x = max(0, nq - QB); x < nq; ++x) (void)mbar_wait(q_full(x % QB), (x / QB) & 1);
       }
-    }
-    if (lost) {
-      give_up();
-      // products in flight end before the tensor memory is freed
-      if (lane == 0) tc_commit(o_full(0));
-      (void)mbar_wait(o_full(0), 0);
+    } else if (warp == kProductWarp) {
+      // ======================= products =============================================
+      int x = 0, nq = 0, done_p[2] = {0, 0}, in_block[2];
+      bool lost = false;
+      for (int n = 0; n < mine && !lost; ++n) {
+        const Unit& u = s_units[n];
+        const Block& blk = u.blk;
+        if (u.k0 == u.k1) continue;
+        const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
+        const int qb = nq % QB;
+        auto seen = [&](int j) -> bool { return j <= last && (j < p.sinks || j >= low); };  // by some query
+        auto scores = [&](int m, int kx) {
+          const uint32_t kb = tc_operand(sKV + ((2 * kx) % ST) * kStage, 16), qa = tc_operand(sQ + (2 * qb + m) * kQTile, 16);
+          if (leader) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+              const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
+              tc_mma(t_scores(m), qa + off, kb + off, kScores, s > 0);
+            }
+            tc_commit(s_full(m));
+          }
+        };
+        if (!mbar_wait(q_full(qb), (nq / QB) & 1) || !mbar_wait(full((2 * x) % ST), ((2 * x) / ST) & 1)) {
+          lost = true;
+          break;
+        }
+        ++nq;
+        in_block[0] = in_block[1] = 0;
+        tc_fence_after();
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          if (sees(blk, m, blk.tile(u.k0))) scores(m, x);
+        if (leader) {
+          tc_commit(empty((2 * x) % ST));
+          if (u.k1 == u.k0 + 1) tc_commit(q_empty(qb));
+        }
+        for (int k = u.k0; k < u.k1 && !lost; ++k, ++x) {
+          const int vi = 2 * x + 1, t = blk.tile(k);
+          const bool more = k + 1 < u.k1;
+          if (!mbar_wait(full(vi % ST), (vi / ST) & 1) ||
+              (more && !mbar_wait(full((vi + 1) % ST), ((vi + 1) / ST) & 1))) {
+            lost = true;
+            break;
+          }
+          const uint32_t vb = sKV + (vi % ST) * kStage;
+          if (!(seen(t * kKeys) && seen(t * kKeys + kKeys - 1) && (t * kKeys >= low || t * kKeys + kKeys <= p.sinks))) {
+            // slots that nobody sees may hold anything: their values become zeros
+            for (int r = lane / 8; r < kKeys; r += 4) {
+              if (seen(t * kKeys + r)) continue;
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            if (!lost && sees(blk, m, t)) {
+              // the weights arrive in two halves of 64 keys
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                lost = lost || !mbar_wait(p_full(m, half), done_p[m] & 1);
+                tc_fence_after();
+                const uint32_t va = tc_operand(vb, kBlockBytes);
+                const bool add = in_block[m] > 0;
+                if (leader && !lost) {
+#pragma unroll
+                  for (int s = 4 * half; s < 4 * half + 4; ++s)
+                    tc_mma_ta(t_out(m), t_scores(m) + s * 8, va + s * (2048 >> 4), kValues, add || s > 0);
+                }
+              }
+              ++done_p[m];
+              ++in_block[m];
+            }
+            if (!lost && more && sees(blk, m, blk.tile(k + 1))) scores(m, x + 1);
+            if (!more && leader) tc_commit(o_full(m));
+          }
+          if (!lost && leader) {
+            tc_commit(empty(vi % ST));
+            if (more) tc_commit(empty((vi + 1) % ST));
+            if (k + 2 == u.k1) tc_commit(q_empty(qb));  // the block's last scores are issued
+          }
+        }
+      }
+      if (lost) {
+        give_up();
+        // products in flight end before the tensor memory is freed: the queries'
+        // barrier serves for that (nothing else waits on it any more)
+        if (leader) tc_commit(q_empty(0));
+        (void)mbar_wait(q_empty(0), ((nq > 0 ? nq - 1 : 0) / QB) & 1);
+      }
     }
   } else {
     // ======================= softmax of row tile m =================================
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     const int m = warp >> 2;
     const int r = tid & (kRows - 1);  // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int token = m * per_tile + r / p.G;
-    const bool valid = token < blk.ntok;
-    const int i = min(blk.slot + token, last);
-    const int f = blk.slot + m * per_tile;                 // first and last query of the tile
-    const int e = min(last, f + per_tile - 1);
     const float NEG_INF = __int_as_float(0xff800000);
-    float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
-    float sum = 0.f;
-    int n = 0;
+    int tiles = 0, blocks = 0;
     bool lost = false;
-    for (int k = k0; k < k1; ++k) {
-      const int t = blk.tile(k);
-      if (!sees(m, t)) continue;
-      if (!mbar_wait(s_full(m), n & 1)) {
+    for (int nu = 0; nu < mine && !lost; ++nu) {
+      const Unit& u = s_units[nu];
+      const Block& blk = u.blk;
+      if (u.k0 == u.k1) continue;
+      const int last = blk.slot + blk.ntok - 1;
+      const bool valid = token < blk.ntok;
+      const int i = min(blk.slot + token, last);
+      const int f = blk.slot + m * per_tile;                 // first and last query of the tile
+      const int e = min(last, f + per_tile - 1);
+      float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
+      float2 sum2 = make_float2(0.f, 0.f);
+      int n = 0;
+      for (int k = u.k0; k < u.k1; ++k) {
+        const int t = blk.tile(k);
+        if (!sees(blk, m, t)) continue;
+        if (!mbar_wait(s_full(m), tiles & 1)) {
+          lost = true;
+          break;
+        }
+        tc_fence_after();
+        uint32_t sc[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(m) + lanes + c * 32, sc[c]);
+        tmem_wait_ld();
+        const int j0 = t * kKeys;
+        if (j0 + kKeys - 1 > f || (j0 <= e - p.window && j0 + kKeys > p.sinks)) {
+          // an edge of the causal mask, of the window or of the sinks
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int jc = j0 + c * 32;
+            const uint32_t vis = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (!((vis >> x) & 1u)) sc[c][x] = 0xff800000u;
+          }
+        }
+        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+        for (int x = 0; x < 32; x += 2)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(sc[c][x]), __uint_as_float(sc[c][x + 1])));
+        const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        if (n == 0) {
+          top = now;
+        } else if (__any_sync(0xffffffffu, now > top + kGrow)) {
+          // the products of the earlier key tiles are complete (the scores' commit
+          // came after theirs), and the next waits for this tile's weights
+          const float to = fmaxf(top, now);
+          const float by = exp2f(top - (to == NEG_INF ? 0.f : to));
+#pragma unroll 1
+          for (int c = 0; c < D; c += 8) {
+            uint32_t o[8];
+            tmem_ld8(t_out(m) + lanes + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+            tmem_st8(t_out(m) + lanes + c, o);
+          }
+          sum2.x *= by;
+          sum2.y *= by;
+          top = to;
+        }
+        const float shift = top == NEG_INF ? 0.f : -top;
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[32];
+          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const int c = 2 * half + (x >> 4), y = 2 * (x & 15);
+            const float2 a = ffma2(make_float2(__uint_as_float(sc[c][y]), __uint_as_float(sc[c][y + 1])), scale2, shift2);
+            const float2 v = make_float2(exp2f(a.x), exp2f(a.y));
+            add[x & 1] = fadd2(add[x & 1], v);
+            w[x] = E::pack2(v.x, v.y);
+          }
+          sum2 = fadd2(sum2, fadd2(add[0], add[1]));
+          tmem_st32(t_scores(m) + lanes + half * 32, w);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_full(m, half));
+        }
+        ++n;
+        ++tiles;
+      }
+      const float sum = sum2.x + sum2.y;
+      if (lost || !mbar_wait(o_full(m), blocks & 1)) {
         lost = true;
         break;
       }
+      ++blocks;
       tc_fence_after();
-      uint32_t sc[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(m) + lanes + c * 32, sc[c]);
-      tmem_wait_ld();
-      const int j0 = t * kKeys;
-      if (j0 + kKeys - 1 > f || (j0 <= e - p.window && j0 + kKeys > p.sinks)) {
-        // an edge of the causal mask, of the window or of the sinks
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int jc = j0 + c * 32;
-          const uint32_t vis = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
-#pragma unroll
-          for (int x = 0; x < 32; ++x)
-            if (!((vis >> x) & 1u)) sc[c][x] = 0xff800000u;
-        }
-      }
-      float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-#pragma unroll
-      for (int x = 0; x < 32; ++x)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], __uint_as_float(sc[c][x]));
-      const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      if (n == 0) {
-        top = now;
-      } else if (__any_sync(0xffffffffu, now > top + kGrow)) {
-        // the products of the earlier key tiles are complete (the scores' commit
-        // came after theirs), and the next waits for this tile's weights
-        const float to = fmaxf(top, now);
-        const float by = exp2f(top - (to == NEG_INF ? 0.f : to));
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(t_out(m) + lanes + c * 32, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-          tmem_st32(t_out(m) + lanes + c * 32, o);
-        }
-        sum *= by;
-        top = to;
-      }
-      const float shift = top == NEG_INF ? 0.f : top;
-      float add[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float w = exp2f(fmaf(__uint_as_float(sc[c][x]), p.scale_log2, -shift));
-          add[x & 3] += w;
-          sc[c][x] = __float_as_uint(w);
-        }
-      sum += (add[0] + add[1]) + (add[2] + add[3]);
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[32];
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const int e0 = c * 64 + 2 * x;
-          w[x] = E::pack2(__uint_as_float(sc[e0 >> 5][e0 & 31]), __uint_as_float(sc[(e0 + 1) >> 5][(e0 + 1) & 31]));
-        }
-        tmem_st32(t_scores(m) + lanes + c * 32, w);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(p_full(m));
-      ++n;
-    }
-    if (lost) give_up();
-    if (!lost && !mbar_wait(o_full(m), 0)) {
-      lost = true;
-      give_up();
-    }
-    if (!lost) {
-      tc_fence_after();
-      const long long row_at = (blk.first + token) * tok_stride + (static_cast<long long>(h) * p.G + r % p.G) * D;
-      const long long part =
-          ((static_cast<long long>(bi) * p.Hkv + h) * p.splits + blockIdx.z) * (2 * kRows) + m * kRows + r;
+      const long long row_at = (blk.first + token) * tok_stride + (static_cast<long long>(u.h) * p.G + r % p.G) * D;
+      const long long part0 = ((static_cast<long long>(u.bi) * p.Hkv + u.h) * p.splits + u.z) * (2 * kRows) + m * kRows;
       const float inv = sum > 0.f ? 1.f / sum : (n == 0 || top == NEG_INF ? 0.f : 1.f / sum);
       bool nan = false;
 #pragma unroll
@@ -468,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           o[x] = __float_as_uint(v);
         }
         if (valid && p.splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + c * 32);
+          float4* dst = reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + c * 32);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
@@ -486,34 +572,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         }
         __syncwarp();
       }
-      if (p.splits > 1 && valid) p.part_lse[part] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+      if (p.splits > 1 && valid) p.part_lse[part0 + r] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
       // rows that ended with a NaN, once more over what they see alone
-      uint32_t again = __ballot_sync(0xffffffffu, nan && valid);
-      while (again) {
-        const int src = __ffs(again) - 1;
-        again &= again - 1;
-        const int rr = (warp & 3) * 32 + src, tok = m * per_tile + rr / p.G;
-        const long long at = (blk.first + tok) * tok_stride + (static_cast<long long>(h) * p.G + rr % p.G) * D;
-        float o[D / 32], mm, ll;
-        attend_alone<E, D>(p, blk, k0, k1, h, blk.slot + tok, p.q + at, o, mm, ll);
-        const float il = ll == 0.f ? 0.f : 1.f / ll;
-        if (p.splits > 1) {
-          const long long pp =
-              ((static_cast<long long>(bi) * p.Hkv + h) * p.splits + blockIdx.z) * (2 * kRows) + m * kRows + rr;
-#pragma unroll
-          for (int x = 0; x < D / 32; ++x) p.part_o[pp * D + lane * (D / 32) + x] = o[x] * il;
-          if (lane == 0) p.part_lse[pp] = ll > 0.f ? mm + log2f(ll) : (ll == 0.f ? NEG_INF : ll);
-        } else {
-#pragma unroll
-          for (int x = 0; x < D / 32; x += 2)
-            *reinterpret_cast<uint32_t*>(p.out + at + lane * (D / 32) + x) = E::pack2(o[x] * il, o[x + 1] * il);
-        }
-      }
+      const uint32_t again = __ballot_sync(0xffffffffu, nan && valid);
+      if (again) attend_alone<E, D>(p, u, m, again);
     }
+    if (lost) give_up();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_free(tmem, kTmem);
+  if (warp == kProductWarp) tmem_free(tmem, kTmem);
 }
 
 // Sum of a row's partial results over the CTAs that shared its block's keys:
@@ -571,7 +639,7 @@ __global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_consta
 
 template <typename E, int D>
 cudaError_t launch_t(const PromptParams& p, cudaStream_t stream) {
-  window_prompt_kernel<E, D><<<dim3(p.blocks, p.Hkv, p.splits), kThreads, kPromptSmem<D>, stream>>>(p);
+  window_prompt_kernel<E, D><<<p.ctas, kThreads, kPromptSmem<D>, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || p.splits == 1) return e;
   cudaLaunchConfig_t cfg{};
