@@ -21,7 +21,7 @@
 //    A tile that one of the two row tiles does not see is skipped for it.
 //  * Warps: two warpgroups for the softmax of a row tile each (a thread owns a
 //    row, so its maximum and sum need no exchange), one warp that issues the
-//    products, one that copies K and V through a ring of stages.  A CTA works
+//    products, two that copy K and V through a ring of stages.  A CTA works
 //    through several blocks; the copies of the next one run while the last
 //    products and outputs of this one are under way.
 //  * Softmax.  Running maximum and sum in fp32; the accumulator is rescaled
@@ -48,7 +48,7 @@ namespace {
 constexpr int kRows = 128;       // rows of a row tile
 constexpr int kKeys = 128;       // keys of a key tile
 constexpr int kThreads = 384;    // two softmax warpgroups, and one whose warps issue products and copies
-constexpr int kProductWarp = 8, kCopyWarp = 9;  // (K and queries; the next one V)
+constexpr int kProductWarp = 8, kCopyWarp = 9;  // the copy warp takes K and the queries, the next one V
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
@@ -341,18 +341,41 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       }
     } else if (warp == kProductWarp) {
       // ======================= products =============================================
-      int x = 0, nq = 0, done_p[2] = {0, 0}, in_block[2];
+      // The tensor cores wait whenever this warp does more between two products
+      // than they have queued, so all that a tile needs is known before: its
+      // place in the ring, and which row tiles see it.
+      uint32_t ki = 0, kp = 0, vi = 1, vp = 0;  // ring place and phase of the next K and V
+      auto next = [&](uint32_t& i, uint32_t& ph) {
+        i += 2;
+        if (i >= ST) {
+          i -= ST;
+          ph ^= 1u;
+        }
+      };
+      int nq = 0;
+      uint32_t weights[2] = {0, 0};  // phases of the weights' barriers
       bool lost = false;
+      const uint32_t k_operand = tc_operand(sKV, 16), v_operand = tc_operand(sKV, kBlockBytes);
       for (int n = 0; n < mine && !lost; ++n) {
-        const Unit& u = s_units[n];
-        const Block& blk = u.blk;
-        if (u.k0 == u.k1) continue;
+        const Block blk = s_units[n].blk;
+        const int k0 = s_units[n].k0, k1 = s_units[n].k1;
+        if (k0 == k1) continue;
         const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
         const int qb = nq % QB;
-        auto seen = [&](int j) -> bool { return j <= last && (j < p.sinks || j >= low); };  // by some query
-        auto scores = [&](int m, int kx) {
-          const uint32_t kb = tc_operand(sKV + ((2 * kx) % ST) * kStage, 16), qa = tc_operand(sQ + (2 * qb + m) * kQTile, 16);
+        // the key tiles of the list that row tile m sees: below s_end, and from w_begin to w_end
+        int s_end[2], w_begin[2], w_end[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          const int f = blk.slot + m * per_tile, e = min(last, f + per_tile - 1);
+          s_end[m] = f > last ? 0 : min(blk.sink_tiles, e / kKeys + 1);
+          w_begin[m] = blk.sink_tiles + max(0, max(0, f - p.window + 1) / kKeys - blk.from);
+          w_end[m] = f > last ? 0 : blk.sink_tiles + e / kKeys + 1 - blk.from;
+        }
+        auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
+        const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
+        auto scores = [&](int m) {
           if (leader) {
+            const uint32_t qa = q_operand + m * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
@@ -361,33 +384,35 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             tc_commit(s_full(m));
           }
         };
-        if (!mbar_wait(q_full(qb), (nq / QB) & 1) || !mbar_wait(full((2 * x) % ST), ((2 * x) / ST) & 1)) {
+        if (!mbar_wait(q_full(qb), (nq / QB) & 1) || !mbar_wait(full(ki), kp)) {
           lost = true;
           break;
         }
         ++nq;
-        in_block[0] = in_block[1] = 0;
-        tc_fence_after();
+        bool see[2] = {sees_k(0, k0), sees_k(1, k0)}, add[2] = {false, false};
 #pragma unroll
         for (int m = 0; m < 2; ++m)
-          if (sees(blk, m, blk.tile(u.k0))) scores(m, x);
+          if (see[m]) scores(m);
         if (leader) {
-          tc_commit(empty((2 * x) % ST));
-          if (u.k1 == u.k0 + 1) tc_commit(q_empty(qb));
+          tc_commit(empty(ki));
+          if (k0 + 1 == k1) tc_commit(q_empty(qb));
         }
-        for (int k = u.k0; k < u.k1 && !lost; ++k, ++x) {
-          const int vi = 2 * x + 1, t = blk.tile(k);
-          const bool more = k + 1 < u.k1;
-          if (!mbar_wait(full(vi % ST), (vi / ST) & 1) ||
-              (more && !mbar_wait(full((vi + 1) % ST), ((vi + 1) / ST) & 1))) {
+        next(ki, kp);
+        for (int k = k0; k < k1; ++k) {
+          const bool more = k + 1 < k1;
+          const bool see_next[2] = {more && sees_k(0, k + 1), more && sees_k(1, k + 1)};
+          if (!mbar_wait(full(vi), vp)) {
             lost = true;
             break;
           }
-          const uint32_t vb = sKV + (vi % ST) * kStage;
-          if (!(seen(t * kKeys) && seen(t * kKeys + kKeys - 1) && (t * kKeys >= low || t * kKeys + kKeys <= p.sinks))) {
-            // slots that nobody sees may hold anything: their values become zeros
+          if (k + 1 == blk.count || k + 1 == blk.sink_tiles || k == blk.sink_tiles) {
+            // an end of what the block sees may lie inside this tile: slots that
+            // nobody sees may hold anything, so their values become zeros
+            const uint32_t vb = sKV + vi * kStage;
+            const int j0 = blk.tile(k) * kKeys;
             for (int r = lane / 8; r < kKeys; r += 4) {
-              if (seen(t * kKeys + r)) continue;
+              const int j = j0 + r;
+              if (j <= last && (j < p.sinks || j >= low)) continue;
 #pragma unroll
               for (int hf = 0; hf < HALVES; ++hf)
                 asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
@@ -397,41 +422,46 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             fence_proxy_async_smem();
             __syncwarp();
           }
+          const uint32_t va = v_operand + vi * (kStage >> 4);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            if (!lost && sees(blk, m, t)) {
+            if (see[m]) {
               // the weights arrive in two halves of 64 keys
 #pragma unroll
               for (int half = 0; half < 2; ++half) {
-                lost = lost || !mbar_wait(p_full(m, half), done_p[m] & 1);
+                lost = lost || !mbar_wait(p_full(m, half), weights[m]);
                 tc_fence_after();
-                const uint32_t va = tc_operand(vb, kBlockBytes);
-                const bool add = in_block[m] > 0;
                 if (leader && !lost) {
 #pragma unroll
                   for (int s = 4 * half; s < 4 * half + 4; ++s)
-                    tc_mma_ta(t_out(m), t_scores(m) + s * 8, va + s * (2048 >> 4), kValues, add || s > 0);
+                    tc_mma_ta(t_out(m), t_scores(m) + s * 8, va + s * (2048 >> 4), kValues, add[m] || s > 0);
                 }
               }
-              ++done_p[m];
-              ++in_block[m];
+              weights[m] ^= 1u;
+              add[m] = true;
             }
-            if (!lost && more && sees(blk, m, blk.tile(k + 1))) scores(m, x + 1);
-            if (!more && leader) tc_commit(o_full(m));
+            if (m == 0 && more) lost = lost || !mbar_wait(full(ki), kp);
+            if (see_next[m] && !lost) scores(m);
+            if (!more && leader && !lost) tc_commit(o_full(m));
           }
-          if (!lost && leader) {
-            tc_commit(empty(vi % ST));
-            if (more) tc_commit(empty((vi + 1) % ST));
-            if (k + 2 == u.k1) tc_commit(q_empty(qb));  // the block's last scores are issued
+          if (lost) break;
+          if (leader) {
+            tc_commit(empty(vi));
+            if (more) tc_commit(empty(ki));
+            if (k + 2 == k1) tc_commit(q_empty(qb));  // the block's last scores are issued
           }
+          next(vi, vp);
+          if (more) next(ki, kp);
+          see[0] = see_next[0];
+          see[1] = see_next[1];
         }
       }
       if (lost) {
         give_up();
-        // products in flight end before the tensor memory is freed: the queries'
-        // barrier serves for that (nothing else waits on it any more)
-        if (leader) tc_commit(q_empty(0));
-        (void)mbar_wait(q_empty(0), ((nq > 0 ? nq - 1 : 0) / QB) & 1);
+        // products in flight end before the tensor memory is freed (row tile 0's output
+        // barrier serves for that; its softmax has given up or will)
+        if (leader) tc_commit(o_full(0));
+        for (int x = 0; x < 2; ++x) (void)mbar_wait(o_full(0), x);
       }
     }
   } else {
