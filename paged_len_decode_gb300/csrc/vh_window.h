@@ -68,14 +68,15 @@ struct WindowDecodeParams {
 };
 
 // The prompt kernel's ring of K and V stages and its shared memory: the
-// queries of both row tiles, the stages, and up to 1024 bytes to align them.
+// queries of both row tiles, the stages, 32 KB through which outputs leave, and
+// up to 1024 bytes to align them.
 constexpr int kPromptRows = 256;  // (token, head) rows of a block
 template <int D>
-constexpr int kPromptStages = D == 128 ? 5 : 8;
+constexpr int kPromptStages = D == 128 ? 4 : 6;
 template <int D>
 constexpr int kPromptQueries = D == 128 ? 1 : 2;  // blocks of queries held at a time
 template <int D>
-constexpr int kPromptSmem = (2 * kPromptQueries<D> + kPromptStages<D>) * 128 * D * 2 + 1024;
+constexpr int kPromptSmem = (2 * kPromptQueries<D> + kPromptStages<D>) * 128 * D * 2 + 32768 + 1024;
 constexpr int kPromptUnits = 20;  // most (block, kv head, split) units of a CTA
 
 struct PromptParams {

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   const int mine = static_cast<int>((units - blockIdx.x + gridDim.x - 1) / gridDim.x);  // <= kPromptUnits
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sQ = base, sKV = base + QB * 2 * kQTile;
+  const uint32_t sQ = base, sKV = base + QB * 2 * kQTile, sOut = sKV + ST * kStage;
   const uint32_t bars = smem_addr(s_bars);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (ST + s); };
@@ -505,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           for (int c = 0; c < 4; ++c) {
             const int jc = j0 + c * 32;
             const uint32_t vis = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
+            if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
 #pragma unroll
             for (int x = 0; x < 32; ++x)
               if (!((vis >> x) & 1u)) sc[c][x] = 0xff800000u;
@@ -514,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
 #pragma unroll
         for (int x = 0; x < 32; x += 2)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmaxf(mx[c], fmaxf(__uint_as_float(sc[c][x]), __uint_as_float(sc[c][x + 1])));
+          for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], __uint_as_float(sc[c][x]), __uint_as_float(sc[c][x + 1]));
         const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         if (n == 0) {
           top = now;
@@ -566,43 +567,72 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       }
       ++blocks;
       tc_fence_after();
-      const long long row_at = (blk.first + token) * tok_stride + (static_cast<long long>(u.h) * p.G + r % p.G) * D;
       const long long part0 = ((static_cast<long long>(u.bi) * p.Hkv + u.h) * p.splits + u.z) * (2 * kRows) + m * kRows;
       const float inv = sum > 0.f ? 1.f / sum : (n == 0 || top == NEG_INF ? 0.f : 1.f / sum);
       bool nan = false;
+      // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
+      // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
+      // lines each (4500 cycles a block against 1500).
+      const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
+      auto leave = [&](const uint32_t (&w)[32], auto line) {
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
-        if (n > 0) {
-          tmem_ld32(t_out(m) + lanes + c * 32, o);
-          tmem_wait_ld();
-        }
+        for (int x = 0; x < 8; ++x)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[4 * x]),
+                       "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
+                       : "memory");
+        __syncwarp();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float v = n > 0 ? __uint_as_float(o[x]) * inv : 0.f;
-          nan |= !(v == v);
-          o[x] = __float_as_uint(v);
-        }
-        if (valid && p.splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + (part0 + r) * D + c * 32);
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            dst[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]), __uint_as_float(o[4 * x + 2]),
-                                 __uint_as_float(o[4 * x + 3]));
-        } else if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row_at + c * 32);
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = E::pack2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
-            dst[x] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+        for (int x = 0; x < 8; ++x) {
+          const int row = 4 * x + (lane >> 3), tok = m * per_tile + ((warp & 3) * 32 + row) / p.G;
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stage + swz128(row, lane & 7)));
+          if (tok < blk.ntok) *reinterpret_cast<uint4*>(line(row, tok) + (lane & 7) * 16) = v;
         }
         __syncwarp();
+      };
+      if (p.splits > 1) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(t_out(m) + lanes + c * 32, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float v = n > 0 ? __uint_as_float(o[x]) * inv : 0.f;
+            nan |= !(v == v);
+            o[x] = __float_as_uint(v);
+          }
+          leave(o, [&](int row, int) {
+            return reinterpret_cast<unsigned char*>(p.part_o + (part0 + (warp & 3) * 32 + row) * D + c * 32);
+          });
+        }
+        if (valid) p.part_lse[part0 + r] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+      } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t o[32];
+            tmem_ld32(t_out(m) + lanes + c * 64 + half * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float v0 = __uint_as_float(o[2 * x]) * inv, v1 = __uint_as_float(o[2 * x + 1]) * inv;
+              nan |= !(v0 == v0) || !(v1 == v1);
+              w[half * 16 + x] = E::pack2(v0, v1);
+            }
+          }
+          leave(w, [&](int row, int tok) {
+            return reinterpret_cast<unsigned char*>(p.out + (blk.first + tok) * tok_stride +
+                                                    (static_cast<long long>(u.h) * p.G + ((warp & 3) * 32 + row) % p.G) * D + c * 64);
+          });
+        }
       }
-      if (p.splits > 1 && valid) p.part_lse[part0 + r] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
       // rows that ended with a NaN, once more over what they see alone
       const uint32_t again = __ballot_sync(0xffffffffu, nan && valid);
       if (again) attend_alone<E, D>(p, u, m, again);
