@@ -468,9 +468,8 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
                           void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
                           int B, int Hq, int Hkv, int D, int page_size, void* stream);
 
-/* Bytes of workspace vh_window_prompt_attn needs for T tokens of B rows on
- * the current device; 0 on bad arguments.  Holds the partial results of query
- * blocks whose keys are split over CTAs (short chunks over long contexts). */
+/* Bytes of workspace vh_window_prompt_attn needs for T tokens of B rows; 0 on
+ * bad arguments.  Holds the counter from which the CTAs draw their work. */
 size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
 
 /* Attention of a ragged batch of new tokens (prompts, or chunks of them)
@@ -480,11 +479,13 @@ size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D);
  * out    e16 [T][Hq][D]; tokens of inactive or flagged rows are written as
  *        zeros, tokens of no row are left as they were.
  * sm_scale: softmax scale; <= 0 means 1/sqrt(D).
- * num_splits: CTAs that share the keys of one block of queries; 0 = automatic,
- *        at most 64.  A larger num_splits than the workspace holds is cut to it.
- * workspace: at least vh_prompt_workspace_bytes(...) bytes, 16-byte aligned; no
- *        initialisation needed.  Calls that may overlap on the device need
- *        workspaces of their own.
+ * num_splits: CTAs that share the keys of one block of queries (a cluster, which
+ *        adds their results over distributed shared memory): 1, 2, 4, 8 or 16,
+ *        or 0 = automatic.  Cut to the largest cluster that the device runs.
+ * workspace: at least vh_prompt_workspace_bytes(...) bytes, 16-byte aligned,
+ *        zero-filled before its first use; every completed call leaves it zero
+ *        (refill it after a call that set VH_ERR_TIMEOUT).  Calls that may overlap
+ *        on the device, captured graphs among them, need workspaces of their own.
  * flags: VH_FLAG_FP16.
  * Scores and softmax statistics are fp32; the weights are rounded to the
  * element type for the value product, which accumulates in fp32.

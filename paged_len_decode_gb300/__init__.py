@@ -405,5 +405,5 @@ def vh_prompt_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
 
 
 def alloc_prompt_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
-    """Device scratch for vh_window_prompt_attn (torch allocation)."""
-    return torch.empty(vh_prompt_workspace_bytes(T, B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
+    """Zero-filled device scratch for vh_window_prompt_attn (torch allocation)."""
+    return torch.zeros(vh_prompt_workspace_bytes(T, B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")

@@ -77,7 +77,6 @@ template <int D>
 constexpr int kPromptQueries = D == 128 ? 1 : 2;  // blocks of queries held at a time
 template <int D>
 constexpr int kPromptSmem = (2 * kPromptQueries<D> + kPromptStages<D>) * 128 * D * 2 + 32768 + 1024;
-constexpr int kPromptUnits = 20;  // most (block, kv head, split) units of a CTA
 
 struct PromptParams {
   // queries as a 3-D tensor (head_dim, q head, token), boxes of 64 x G x 128/G;
@@ -101,17 +100,16 @@ struct PromptParams {
   int f16;
   int T, B, Hq, Hkv, D, G, P;
   int blocks;                  // T / (256 / G) + B: an upper bound (rows fill their last block partly)
-  int splits;                  // CTAs that share the keys of a block
+  int splits;                  // CTAs that share the keys of a block (a cluster): 1, 2, 4, 8 or 16
   int ctas;
-  float* part_o;               // [blocks][Hkv][splits][256][D], if splits > 1
-  float* part_lse;             // [blocks][Hkv][splits][256], base 2
+  int* counter;                // the next unit to be drawn (splits == 1); zero between calls
 };
 
 cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl);
-cudaError_t prepare_window_prompt();  // once per device, every variant
+cudaError_t prepare_window_prompt(int* max_splits);  // once per device, every variant
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace vh

@@ -33,13 +33,14 @@ constexpr int kStageTarget = 65536;  // bytes in flight of a CTA, two CTAs on an
 struct Prepared {
   std::once_flag once;
   bool ok = false;
+  int max_splits = 1;  // largest cluster of the prompt kernel
 };
 Prepared g_prepared[kMaxDevices];
 
 bool prepared(const DeviceInfo& dev) {
   Prepared& s = g_prepared[dev.index];
   std::call_once(s.once, [&]() {
-    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt() == cudaSuccess;
+    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(&s.max_splits) == cudaSuccess;
     if (!s.ok) cudaGetLastError();
   });
   return s.ok;
@@ -207,18 +208,16 @@ bool encode_prompt_maps(vh::PromptParams& p) {
   return false;
 }
 
-// Blocks of the prompt kernel (an upper bound) and the CTAs that share a
-// block's keys: as many as fill the SMs once.
-long long prompt_blocks(int T, int B, int Hq, int Hkv) {
-  return static_cast<long long>(T) / (vh::kPromptRows / (Hq / Hkv)) + B;
-}
-
-int prompt_splits(int T, int B, int Hq, int Hkv, const DeviceInfo& dev) {
-  return static_cast<int>(std::max(1LL, std::min(64LL, dev.sm_count / (prompt_blocks(T, B, Hq, Hkv) * Hkv))));
-}
-
-size_t prompt_split_bytes(int T, int B, int Hq, int Hkv, int D) {
-  return static_cast<size_t>(prompt_blocks(T, B, Hq, Hkv)) * Hkv * vh::kPromptRows * (static_cast<size_t>(D) + 1) * 4;
+// CTAs that share a block's keys: as many as leave no SM idle, and no more than
+// a block can have key tiles.
+int prompt_splits(const vh::PromptParams& p, const DeviceInfo& dev, int max_splits) {
+  const int per = vh::kPromptRows / p.G;
+  const long long blocks = (p.T + per - 1) / per + (p.B - 1) / 2;  // rows fill their last blocks by half, say
+  const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
+                                                static_cast<long long>(p.window) + p.sinks + per);
+  int s = 1;
+  while (2 * s <= max_splits && blocks * p.Hkv * 2 * s <= dev.sm_count && longest >= 128LL * 2 * s) s *= 2;
+  return s;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? VH_OK : VH_ECUDA; }
@@ -363,11 +362,7 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
 }
 
 size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
-  if (T < 0 || !valid_shape(B, Hq, Hkv, D, 16)) return 0;
-  const DeviceInfo* dev = device_info();
-  if (!dev) return 0;
-  const int splits = prompt_splits(T, B, Hq, Hkv, *dev);
-  return 256 + (splits > 1 ? splits * prompt_split_bytes(T, B, Hq, Hkv, D) : 0);
+  return T < 0 || !valid_shape(B, Hq, Hkv, D, 16) ? 0 : 256;
 }
 
 int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
@@ -376,7 +371,8 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
                           const int32_t* active, int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
                           void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B,
                           int Hq, int Hkv, int D, int page_size, void* stream) {
-  if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 64 ||
+  if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 16 ||
+      (num_splits & (num_splits - 1)) != 0 ||
       !(sm_scale == sm_scale) ||
       !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
                    max_pages_per_seq))
@@ -417,21 +413,14 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
   p.D = D;
   p.G = Hq / Hkv;
   p.P = page_size;
-  const long long blocks = prompt_blocks(T, B, Hq, Hkv);
-  if (Hkv > 65535 || !encode_prompt_maps(p)) return VH_EINVAL;
+  const int max_splits = g_prepared[dev->index].max_splits;
+  p.splits = num_splits > 0 ? std::min(num_splits, max_splits) : prompt_splits(p, *dev, max_splits);
+  const long long blocks = static_cast<long long>(T) / (vh::kPromptRows / p.G) + B, units = blocks * Hkv * p.splits;
+  if (units > INT32_MAX / 2 || !encode_prompt_maps(p)) return VH_EINVAL;
   p.blocks = static_cast<int>(blocks);
-  const size_t per = prompt_split_bytes(T, B, Hq, Hkv, D);
-  p.splits = num_splits > 0 ? num_splits : prompt_splits(T, B, Hq, Hkv, *dev);
-  p.splits = static_cast<int>(std::min<size_t>(p.splits, std::max<size_t>(1, workspace_bytes / per)));
-  // no more CTAs than a block can have key tiles
-  const long long longest = std::min<long long>(static_cast<long long>(max_pages_per_seq) * page_size,
-                                                static_cast<long long>(p.window) + vh::kPromptRows);
-  p.splits = static_cast<int>(std::min<long long>(p.splits, longest / 128 + 2 + p.sinks / 128));
-  // one CTA an SM, or whole rounds of them where a CTA could not list its units
-  const long long units = blocks * Hkv * p.splits, round = static_cast<long long>(dev->sm_count) * vh::kPromptUnits;
-  p.ctas = static_cast<int>(std::min(units, dev->sm_count * ((units + round - 1) / round)));
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = p.part_o + static_cast<size_t>(blocks) * Hkv * p.splits * vh::kPromptRows * D;
+  // CTAs draw units one after the other; a cluster's CTAs have one each
+  p.ctas = static_cast<int>(p.splits > 1 ? units : std::min<long long>(units, dev->sm_count));
+  p.counter = static_cast<int*>(workspace);
   return status_of(vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -12,8 +12,7 @@
 //    less and K and V are read once for the whole group.  The rows form two
 //    tiles of 128, whose products and softmax alternate: while one tile's
 //    scores are turned into weights, the tensor cores work for the other.  A
-//    block holds tokens of one request; block i belongs to the last row b with
-//    token_start[b] / tokens + b <= i, so the grid needs no work list.
+//    block holds tokens of one request.
 //  * Keys.  Tiles of 128 slots: those that hold sinks, then those from the
 //    first query's window to the last query.  Each is copied box by box through
 //    the page table; boxes that nobody sees, and bad page ids, become a page
@@ -21,9 +20,11 @@
 //    A tile that one of the two row tiles does not see is skipped for it.
 //  * Warps: two warpgroups for the softmax of a row tile each (a thread owns a
 //    row, so its maximum and sum need no exchange), one warp that issues the
-//    products, two that copy K and V through a ring of stages.  A CTA works
-//    through several blocks; the copies of the next one run while the last
-//    products and outputs of this one are under way.
+//    products, two that copy K and V through a ring of stages, and one that
+//    draws the CTA's next block from a counter while this one is computed
+//    (requests with the longest contexts first, so that the last blocks are
+//    short).  The copies of the next block run while the last products and
+//    outputs of this one are under way.
 //  * Softmax.  Running maximum and sum in fp32; the accumulator is rescaled
 //    only when a row's maximum has grown by more than 2^8 since the last time
 //    (weights stay below 2^8, far inside fp32, bf16 and fp16), so it is rare.
@@ -36,7 +37,9 @@
 //    harmless unless it is infinite or NaN; a row that ends with a NaN is
 //    therefore computed again over its visible keys alone, one warp a row.
 //  * Few blocks (short chunks over long contexts): the key tiles of a block are
-//    shared by `splits` CTAs, whose partial results a second kernel adds.
+//    shared by a cluster of up to 16 CTAs, which leave their partial results in
+//    shared memory and add them over distributed shared memory, each a share of
+//    the rows.
 #include "vh_ragged.cuh"
 #include "vh_tcgen05.cuh"
 #include "vh_window.h"
@@ -48,42 +51,116 @@ namespace {
 constexpr int kRows = 128;       // rows of a row tile
 constexpr int kKeys = 128;       // keys of a key tile
 constexpr int kThreads = 384;    // two softmax warpgroups, and one whose warps issue products and copies
-constexpr int kProductWarp = 8, kCopyWarp = 9;  // the copy warp takes K and the queries, the next one V
+constexpr int kProductWarp = 8, kCopyWarp = 9, kDrawWarp = 11;  // the copy warp takes K and the queries, the next one V
+constexpr int kSlots = 2;        // blocks drawn: this one and the next
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
-// A block of queries and the list of its key tiles.
-struct Block {
-  int row, first, ntok;  // request, first token, tokens (0: none)
-  int slot;              // slot of the first token
-  int len;
-  bool ok;
+// One CTA's work: queries of one request and kv head, and a share of their key tiles.
+struct Unit {
+  int row, first, ntok;         // request, first token, tokens
+  int slot;                     // slot of the first token
+  int h, z;                     // kv head, share of the keys
   int sink_tiles, from, count;  // key tiles: 0 .. sink_tiles - 1, then `from` on; `count` in all
+  int k0, k1;                   // this CTA's of them; k0 == k1: nothing to do
+  int more;                     // 0: no unit, the CTA is done
   __device__ int tile(int k) const { return k < sink_tiles ? k : k - sink_tiles + from; }
 };
 
-__device__ __forceinline__ Block block_of(const PromptParams& p, int i, int lane, bool report) {
-  Block r{};
-  const int per = 2 * kRows / p.G;
-  r.row = warp_last_at_most(p.B, i, lane, [&](int b) { return p.token_start[b] / per + b; });
-  if (r.row < 0) return r;
-  const RaggedRow g =
-      ragged_row(p.token_start, p.seq_lens, p.active, r.row, p.T, p.max_pages_per_seq * p.P, p.err_flag, report);
-  r.first = g.start + (i - (g.start / per + r.row)) * per;
-  r.ntok = min(per, min(g.end, p.T) - r.first);
-  if (g.start < 0 || r.first < 0) r.ntok = 0;
-  r.ok = g.ok;
-  r.len = g.len;
-  if (r.ntok <= 0 || !g.ok) return r;
-  r.slot = g.len - (g.end - r.first);
-  const int last = r.slot + r.ntok - 1;
-  r.sink_tiles = (min(p.sinks, last + 1) + kKeys - 1) / kKeys;
-  r.from = max(r.sink_tiles, max(0, r.slot - p.window + 1) / kKeys);
-  r.count = r.sink_tiles + last / kKeys + 1 - r.from;
-  return r;
+__device__ __forceinline__ int share_begin(int c, int n, int total) { return c * (total / n) + min(c, total % n); }
+
+// The key tiles of `ntok` queries from `slot` on.
+__device__ __forceinline__ void list_tiles(const PromptParams& p, int slot, int ntok, int& sink_tiles, int& from, int& count) {
+  const int last = slot + ntok - 1;
+  sink_tiles = (min(p.sinks, last + 1) + kKeys - 1) / kKeys;
+  from = max(sink_tiles, max(0, slot - p.window + 1) / kKeys);
+  count = sink_tiles + last / kKeys + 1 - from;
 }
 
-__device__ __forceinline__ int share_begin(int c, int n, int total) { return c * (total / n) + min(c, total % n); }
+// What the drawing warp knows of up to 32 requests, one a lane: with these, a
+// block is found without reading memory, and blocks of requests with more key
+// tiles come first.  (With more requests, block i belongs to the last row b
+// with token_start[b] / tokens + b <= i, a search in memory.)
+struct Rows {
+  RaggedRow r;
+  int blocks, before;  // of this request, and of those that come before it
+};
+
+__device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
+  Rows x{};
+  const int per = 2 * kRows / p.G;
+  int weight = -1;
+  if (lane < p.B) {
+    x.r = ragged_row(p.token_start, p.seq_lens, p.active, lane, p.T, p.max_pages_per_seq * p.P, p.err_flag, blockIdx.x == 0);
+    const int n = x.r.start >= 0 ? min(x.r.end, p.T) - x.r.start : 0;
+    x.blocks = n > 0 ? (n + per - 1) / per : 0;
+    if (x.r.ok && n > 0) {
+      int a, b;
+      list_tiles(p, x.r.len - min(n, per), min(n, per), a, b, weight);
+    }
+  }
+  int rank = 0;
+  for (int j = 0; j < p.B; ++j) {
+    const int w = __shfl_sync(0xffffffffu, weight, j);
+    rank += (w > weight || (w == weight && j < lane)) ? 1 : 0;
+  }
+  for (int j = 0; j < p.B; ++j) {
+    const int k = __shfl_sync(0xffffffffu, rank, j), n = __shfl_sync(0xffffffffu, x.blocks, j);
+    x.before += k < rank ? n : 0;
+  }
+  return x;
+}
+
+// Unit u, by one warp.  Tokens of inactive and flagged requests are written as
+// zeros here.
+__device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows, int u, int lane) {
+  Unit r{};
+  r.more = 1;
+  const int per = 2 * kRows / p.G;
+  r.z = u % p.splits;
+  const int v = u / p.splits;
+  r.h = v % p.Hkv;
+  const int i = v / p.Hkv;
+  RaggedRow g{};
+  int n;  // number of the block in its request
+  if (p.B <= 32) {
+    const uint32_t hit = __ballot_sync(0xffffffffu, lane < p.B && i >= rows.before && i < rows.before + rows.blocks);
+    if (hit == 0) return r;
+    r.row = __ffs(hit) - 1;
+    g.start = __shfl_sync(0xffffffffu, rows.r.start, r.row);
+    g.end = __shfl_sync(0xffffffffu, rows.r.end, r.row);
+    g.len = __shfl_sync(0xffffffffu, rows.r.len, r.row);
+    g.ok = __shfl_sync(0xffffffffu, rows.r.ok ? 1 : 0, r.row) != 0;
+    // the last block of a request sees the most
+    n = __shfl_sync(0xffffffffu, rows.blocks, r.row) - 1 - (i - __shfl_sync(0xffffffffu, rows.before, r.row));
+  } else {
+    const int bi = p.blocks - 1 - i;
+    r.row = warp_last_at_most(p.B, bi, lane, [&](int b) { return p.token_start[b] / per + b; });
+    if (r.row < 0) return r;
+    g = ragged_row(p.token_start, p.seq_lens, p.active, r.row, p.T, p.max_pages_per_seq * p.P, p.err_flag,
+                   lane == 0 && r.h == 0 && r.z == 0);
+    n = bi - (g.start / per + r.row);
+  }
+  r.first = g.start + n * per;
+  r.ntok = min(per, min(g.end, p.T) - r.first);
+  if (g.start < 0 || n < 0 || r.ntok <= 0) return r;
+  if (!g.ok) {
+    if (r.z == 0)
+      for (int t = 0; t < r.ntok; ++t) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + ((r.first + t) * static_cast<long long>(p.Hq) + r.h * p.G) * p.D);
+        for (int x = lane; x < p.G * p.D / 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    return r;
+  }
+  r.slot = g.len - (g.end - r.first);
+  list_tiles(p, r.slot, r.ntok, r.sink_tiles, r.from, r.count);
+  const int splits = min(p.splits, r.count);
+  if (r.z < splits) {
+    r.k0 = share_begin(r.z, splits, r.count);
+    r.k1 = share_begin(r.z + 1, splits, r.count);
+  }
+  return r;
+}
 
 // Keys c of 32 that are visible, as bits: c < above, and c >= low or c < sink.
 __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
@@ -91,38 +168,12 @@ __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
   return below(above) & (~below(low) | below(sink));
 }
 
-// One CTA's work: a block's queries for one kv head, and a share of its key tiles.
-struct Unit {
-  Block blk;
-  int h, bi, z;
-  int k0, k1;  // k0 == k1: nothing to do
-};
-
-// Unit u of the grid, by one warp.  The rows of inactive and flagged requests
-// are written as zeros here.
-__device__ __forceinline__ Unit unit_of(const PromptParams& p, long long u, int lane) {
-  Unit r{};
-  r.z = static_cast<int>(u % p.splits);
-  const long long v = u / p.splits;
-  r.h = static_cast<int>(v % p.Hkv);
-  // heavy blocks (long contexts, under a causal mask) first
-  r.bi = p.blocks - 1 - static_cast<int>(v / p.Hkv);
-  r.blk = block_of(p, r.bi, lane, lane == 0 && r.h == 0 && r.z == 0);
-  if (r.blk.ntok <= 0) return r;
-  if (!r.blk.ok) {
-    if (r.z == 0)
-      for (int t = 0; t < r.blk.ntok; ++t) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + ((r.blk.first + t) * static_cast<long long>(p.Hq) + r.h * p.G) * p.D);
-        for (int x = lane; x < p.G * p.D / 8; x += 32) dst[x] = make_uint4(0u, 0u, 0u, 0u);
-      }
-    return r;
-  }
-  const int splits = min(p.splits, r.blk.count);
-  if (r.z < splits) {
-    r.k0 = share_begin(r.z, splits, r.blk.count);
-    r.k1 = share_begin(r.z + 1, splits, r.blk.count);
-  }
-  return r;
+// Chunk of 16 bytes `c` of row r of the partial outputs that a CTA of a cluster
+// leaves in its shared memory (fp32 [256][D]): chunks turned by the row, so that
+// 32 rows written at the same chunk fall into different banks.
+template <int D>
+__device__ __forceinline__ uint32_t part_off(int r, int c) {
+  return static_cast<uint32_t>(r * D * 4 + ((c ^ (r & (D / 4 - 1))) << 4));
 }
 
 // The rows `rows` (bits) of this warp's 32, one after the other by the whole
@@ -130,15 +181,16 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, long long u, int 
 // rows that a value they do not see has reached (0 times infinity).  Lanes over
 // head_dim.  Out of line, so that the common path keeps its registers.
 template <typename E, int D>
-__device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, int m, uint32_t rows) {
+__device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, int m, uint32_t rows, uint32_t part,
+                                          uint32_t part_lse) {
   constexpr int PER = D / 32;
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
   const float NEG_INF = __int_as_float(0xff800000);
   while (rows) {
     const int r = warp * 32 + __ffs(rows) - 1;
     rows &= rows - 1;
-    const int token = m * (kRows / p.G) + r / p.G, i = u.blk.slot + token;
-    const long long at = ((u.blk.first + token) * static_cast<long long>(p.Hq) + u.h * p.G + r % p.G) * D + lane * PER;
+    const int token = m * (kRows / p.G) + r / p.G, i = u.slot + token;
+    const long long at = ((u.first + token) * static_cast<long long>(p.Hq) + u.h * p.G + r % p.G) * D + lane * PER;
     float q[PER], o[PER], top = NEG_INF, sum = 0.f;
 #pragma unroll
     for (int e = 0; e < PER; e += 2) {
@@ -148,10 +200,10 @@ __device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, 
       o[e] = o[e + 1] = 0.f;
     }
     for (int k = u.k0; k < u.k1; ++k) {
-      const int j0 = u.blk.tile(k) * kKeys;
+      const int j0 = u.tile(k) * kKeys;
       for (int j = j0; j < j0 + kKeys && j <= i; ++j) {
         if (j >= p.sinks && i - j >= p.window) continue;
-        const long long lp = static_cast<long long>(u.blk.row) * p.max_pages_per_seq + j / p.P;
+        const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + j / p.P;
         const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
         const bool ok = page >= 0 && page < p.num_pages;
         const long long off = ok ? page * p.page_stride + (j % p.P) * p.token_stride + u.h * p.head_stride + lane * PER : 0;
@@ -177,10 +229,16 @@ __device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, 
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     if (p.splits > 1) {
-      const long long part = ((static_cast<long long>(u.bi) * p.Hkv + u.h) * p.splits + u.z) * (2 * kRows) + m * kRows + r;
+      const int row = m * kRows + r;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) p.part_o[part * D + lane * PER + e] = o[e] * inv;
-      if (lane == 0) p.part_lse[part] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+      for (int e = 0; e < PER; ++e) {
+        const int x = lane * PER + e;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(part + part_off<D>(row, x / 4) + (x % 4) * 4), "f"(o[e] * inv) : "memory");
+      }
+      if (lane == 0)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(part_lse + row * 4),
+                     "f"(sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum))
+                     : "memory");
     } else {
 #pragma unroll
       for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(p.out + at + e) = E::pack2(o[e] * inv, o[e + 1] * inv);
@@ -199,18 +257,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   constexpr uint32_t kScores = tc_kind_f16(kRows, kKeys, !E::kF16, false);
   constexpr uint32_t kValues = tc_kind_f16(kRows, D, !E::kF16, true);
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ Unit s_units[kPromptUnits];
-  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 8];
+  __shared__ Unit s_units[kSlots];
+  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 8 + 2 * kSlots];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int per_tile = kRows / p.G;  // tokens of a row tile
+  const int shift_g = __ffs(p.G) - 1;
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
-  const long long units = static_cast<long long>(p.blocks) * p.Hkv * p.splits;
-  const int mine = static_cast<int>((units - blockIdx.x + gridDim.x - 1) / gridDim.x);  // <= kPromptUnits
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + QB * 2 * kQTile, sOut = sKV + ST * kStage;
+  // partial results of a CTA in a cluster, over the queries and stages, and beside them
+  const uint32_t sPart = base, sLse = sOut;
   const uint32_t bars = smem_addr(s_bars);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (ST + s); };
@@ -219,11 +278,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   auto s_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + m); };
   auto p_full = [&](int m, int half) { return bars + 8 * (2 * ST + 2 * QB + 2 + 2 * m + half); };
   auto o_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 6 + m); };
+  auto u_full = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + s); };
+  auto u_empty = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + kSlots + s); };
   volatile int* abort_flag = &s_abort;
-  for (int n = warp; n < mine; n += kThreads / 32) {
-    const Unit u = unit_of(p, blockIdx.x + static_cast<long long>(n) * gridDim.x, lane);
-    if (lane == 0) s_units[n] = u;
-  }
+  Rows rows{};
+  if (warp == kDrawWarp && p.B <= 32) rows = rows_of(p, lane);
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < ST; ++s) {
@@ -240,6 +299,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       mbar_init(p_full(m, 1), kRows);
       mbar_init(o_full(m), 1);
     }
+    for (int x = 0; x < kSlots; ++x) {
+      mbar_init(u_full(x), 1);
+      mbar_init(u_empty(x), 11);  // every warp but the drawing one
+    }
     fence_barrier_init();
   }
   if (warp == kProductWarp) tmem_alloc(smem_addr(&s_tmem), kTmem);
@@ -249,12 +312,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   const uint32_t tmem = s_tmem;
   auto t_scores = [&](int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
   auto t_out = [&](int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
-  // row tile m of the block sees key tile t?
-  auto sees = [&](const Block& b, int m, int t) -> bool {
-    const int last = b.slot + b.ntok - 1, f = b.slot + m * per_tile;
-    if (f > last) return false;
-    const int e = min(last, f + per_tile - 1);
-    return t <= e / kKeys && (t < b.sink_tiles || t >= max(0, f - p.window + 1) / kKeys);
+  // waits for unit number n of this CTA; false: the CTA is done (or gives up)
+  auto next_unit = [&](int n, bool& lost) -> bool {
+    lost = !mbar_wait(u_full(n % kSlots), (n / kSlots) & 1);
+    return !lost && s_units[n % kSlots].more != 0;
+  };
+  auto release_unit = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(u_empty(n % kSlots));
   };
   auto give_up = [&]() {
     if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
@@ -264,6 +329,35 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   if (warp >= kProductWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const bool leader = elect_one();
+    if (warp == kDrawWarp) {
+      // ======================= the CTA's next unit =====================================
+      // The first is the CTA's own number; the others come from the counter, which
+      // the last draw of all sets back for the next call.  A cluster has one unit a CTA.
+      const int units = p.blocks * p.Hkv * p.splits;
+      int u = blockIdx.x;
+      for (int n = 0;; ++n) {
+        if (n >= kSlots && !mbar_wait(u_empty(n % kSlots), ((n / kSlots) - 1) & 1)) {
+          give_up();
+          break;
+        }
+        Unit x{};
+        if (u < units) x = unit_of(p, rows, u, lane);
+        if (lane == 0) s_units[n % kSlots] = x;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(u_full(n % kSlots));
+        if (u >= units || *abort_flag) break;
+        if (p.splits > 1) {
+          u = units;
+        } else {
+          if (lane == 0) {
+            const int drawn = atomicAdd(p.counter, 1);
+            if (drawn == units - 1) *p.counter = 0;
+            u = gridDim.x + drawn;
+          }
+          u = __shfl_sync(0xffffffffu, u, 0);
+        }
+      }
+    } else
     if (warp == kCopyWarp || warp == kCopyWarp + 1) {
       // ======================= copies: K and the queries, and V =======================
       // tile number x of all units: K is stage 2 x of the ring, V the next one
@@ -276,19 +370,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       const int nbox = kKeys / p.box;
       int issued = kv, nq = 0;  // number in the ring, blocks of queries
       bool lost = false;
-      for (int n = 0; n < mine && !lost; ++n) {
-        const Unit& u = s_units[n];
-        const Block& blk = u.blk;
+      for (int n = 0; !lost && next_unit(n, lost); ++n) {
+        const Unit u = s_units[n % kSlots];
+        release_unit(n);
         if (u.k0 == u.k1) continue;
-        const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
+        const int last = u.slot + u.ntok - 1, low = max(0, u.slot - p.window + 1);
         for (int k = u.k0; k < u.k1 && !lost; ++k, issued += 2) {
-          const int j0 = blk.tile(k) * kKeys;
+          const int j0 = u.tile(k) * kKeys;
           // page and first token of this lane's box (at most 16 boxes a tile)
           int page = p.num_pages, tok = 0;
           if (lane < nbox) {
             const int j = j0 + lane * p.box;
             if (j <= last && (j < p.sinks || j + p.box > low)) {
-              const long long lp = static_cast<long long>(blk.row) * p.max_pages_per_seq + j / p.P;
+              const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + j / p.P;
               page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
               tok = j % p.P;
               if (page < 0 || page >= p.num_pages) {
@@ -315,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           if (k == u.k0 && kv == 0) {
             // the block's queries, once the products of the block that had
             // their place have read it (its first keys are on their way already)
-            const int b = nq % QB, ntile = blk.ntok > per_tile ? 2 : 1;
+            const int b = nq % QB, ntile = u.ntok > per_tile ? 2 : 1;
             if (nq >= QB && !mbar_wait(q_empty(b), ((nq / QB) - 1) & 1)) {
               lost = true;
               issued += 2;
@@ -326,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
               for (int m = 0; m < ntile; ++m)
                 for (int hf = 0; hf < HALVES; ++hf)
                   tma_load_3d(sQ + (2 * b + m) * kQTile + hf * kBlockBytes, &p.tmap_q, hf * 64, u.h * p.G,
-                              blk.first + m * per_tile, q_full(b));
+                              u.first + m * per_tile, q_full(b));
             }
             ++nq;
           }
@@ -356,9 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       uint32_t weights[2] = {0, 0};  // phases of the weights' barriers
       bool lost = false;
       const uint32_t k_operand = tc_operand(sKV, 16), v_operand = tc_operand(sKV, kBlockBytes);
-      for (int n = 0; n < mine && !lost; ++n) {
-        const Block blk = s_units[n].blk;
-        const int k0 = s_units[n].k0, k1 = s_units[n].k1;
+      for (int n = 0; !lost && next_unit(n, lost); ++n) {
+        const Unit blk = s_units[n % kSlots];
+        release_unit(n);
+        const int k0 = blk.k0, k1 = blk.k1;
         if (k0 == k1) continue;
         const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
         const int qb = nq % QB;
@@ -470,14 +565,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
     const int m = warp >> 2;
     const int r = tid & (kRows - 1);  // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int token = m * per_tile + r / p.G;
+    const int token = m * per_tile + (r >> shift_g);
     const float NEG_INF = __int_as_float(0xff800000);
     int tiles = 0, blocks = 0;
     bool lost = false;
-    for (int nu = 0; nu < mine && !lost; ++nu) {
-      const Unit& u = s_units[nu];
-      const Block& blk = u.blk;
-      if (u.k0 == u.k1) continue;
+    for (int nu = 0; !lost && next_unit(nu, lost); ++nu) {
+      const Unit& blk = s_units[nu % kSlots];  // (not released before the block is done)
+      if (blk.k0 == blk.k1) {
+        if (p.splits > 1 && blk.count > 0)  // (a cluster's CTA without a share has nothing to add)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + tid * 4), "f"(NEG_INF) : "memory");
+        release_unit(nu);
+        continue;
+      }
       const int last = blk.slot + blk.ntok - 1;
       const bool valid = token < blk.ntok;
       const int i = min(blk.slot + token, last);
@@ -486,9 +585,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
       float2 sum2 = make_float2(0.f, 0.f);
       int n = 0;
-      for (int k = u.k0; k < u.k1; ++k) {
+      for (int k = blk.k0; k < blk.k1; ++k) {
         const int t = blk.tile(k);
-        if (!sees(blk, m, t)) continue;
+        if (f > last || t > e / kKeys || (t >= blk.sink_tiles && t < max(0, f - p.window + 1) / kKeys)) continue;  // not seen
         if (!mbar_wait(s_full(m), tiles & 1)) {
           lost = true;
           break;
@@ -507,8 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             const uint32_t vis = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
             if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
 #pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (!((vis >> x) & 1u)) sc[c][x] = 0xff800000u;
+            for (int x = 0; x < 32; ++x) sc[c][x] = (vis & (1u << x)) ? sc[c][x] : 0xff800000u;
           }
         }
         float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
@@ -567,14 +665,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       }
       ++blocks;
       tc_fence_after();
-      const long long part0 = ((static_cast<long long>(u.bi) * p.Hkv + u.h) * p.splits + u.z) * (2 * kRows) + m * kRows;
       const float inv = sum > 0.f ? 1.f / sum : (n == 0 || top == NEG_INF ? 0.f : 1.f / sum);
       bool nan = false;
       // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
       // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
       // lines each (4500 cycles a block against 1500).
       const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
-      auto leave = [&](const uint32_t (&w)[32], auto line) {
+      auto leave = [&](const uint32_t (&w)[32], uint16_t* dst) {
 #pragma unroll
         for (int x = 0; x < 8; ++x)
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[4 * x]),
@@ -583,16 +680,22 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         __syncwarp();
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int row = 4 * x + (lane >> 3), tok = m * per_tile + ((warp & 3) * 32 + row) / p.G;
+          const int row = 4 * x + (lane >> 3), rt = (warp & 3) * 32 + row, tok = m * per_tile + (rt >> shift_g);
           uint4 v;
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                        : "r"(stage + swz128(row, lane & 7)));
-          if (tok < blk.ntok) *reinterpret_cast<uint4*>(line(row, tok) + (lane & 7) * 16) = v;
+          if (tok < blk.ntok)
+            *reinterpret_cast<uint4*>(dst + (rt >> shift_g) * tok_stride + (rt & (p.G - 1)) * D) = v;
         }
         __syncwarp();
       };
       if (p.splits > 1) {
+        // the other row tile's products may still read what the partial results overwrite
+        if (!mbar_wait(o_full(m ^ 1), 0)) {
+          lost = true;
+          break;
+        }
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -606,11 +709,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             nan |= !(v == v);
             o[x] = __float_as_uint(v);
           }
-          leave(o, [&](int row, int) {
-            return reinterpret_cast<unsigned char*>(p.part_o + (part0 + (warp & 3) * 32 + row) * D + c * 32);
-          });
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPart + part_off<D>(tid, c * 8 + x)), "r"(o[4 * x]),
+                         "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+                         : "memory");
         }
-        if (valid) p.part_lse[part0 + r] = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + tid * 4),
+                     "f"(sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum))
+                     : "memory");
+        __syncwarp();
       } else {
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
@@ -627,106 +735,114 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
               w[half * 16 + x] = E::pack2(v0, v1);
             }
           }
-          leave(w, [&](int row, int tok) {
-            return reinterpret_cast<unsigned char*>(p.out + (blk.first + tok) * tok_stride +
-                                                    (static_cast<long long>(u.h) * p.G + ((warp & 3) * 32 + row) % p.G) * D + c * 64);
-          });
+          leave(w, p.out + (blk.first + m * per_tile) * tok_stride + static_cast<long long>(blk.h) * p.G * D + c * 64 + (lane & 7) * 8);
         }
       }
       // rows that ended with a NaN, once more over what they see alone
       const uint32_t again = __ballot_sync(0xffffffffu, nan && valid);
-      if (again) attend_alone<E, D>(p, u, m, again);
+      if (again) attend_alone<E, D>(p, blk, m, again, sPart, sLse);
+      release_unit(nu);
     }
     if (lost) give_up();
   }
   tc_fence_before();
   __syncthreads();
   if (warp == kProductWarp) tmem_free(tmem, kTmem);
-}
+  if (p.splits == 1) return;
 
-// Sum of a row's partial results over the CTAs that shared its block's keys:
-// one warp a (token, head).
-template <typename E, int D>
-__global__ void __launch_bounds__(256) prompt_combine_kernel(const __grid_constant__ PromptParams p) {
-  constexpr int PER = D / 32;
-  pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.T) * p.Hq) return;
-  const int t = static_cast<int>(unit / p.Hq), hq = static_cast<int>(unit % p.Hq);
-  const int per = 2 * kRows / p.G, b = warp_last_at_most(p.B, t, lane, [&](int x) { return p.token_start[x]; });
-  if (b < 0 || t >= p.token_start[b + 1] || p.token_start[b] < 0) return;
-  const int local = t - p.token_start[b], bi = p.token_start[b] / per + b + local / per;
-  const Block blk = block_of(p, bi, lane, false);
-  if (!blk.ok || blk.row != b || blk.ntok <= 0) return;  // zeros are written already
-  const int splits = min(p.splits, blk.count);
-  const int r = (local % per) * p.G + hq % p.G;
-  const long long part = ((static_cast<long long>(bi) * p.Hkv + hq / p.G) * p.splits) * (2 * kRows) + r;
-  const float NEG_INF = __int_as_float(0xff800000);
-  // (at most 64 splits: two a lane)
-  float lse[2], top = NEG_INF;
+  // ======================= the cluster's partial results ============================
+  // (all CTAs of a cluster work on one block: they agree on whether there is one)
+  const Unit& u = s_units[0];
+  if (u.count == 0) return;
+  cluster_sync();
+  if (!*abort_flag) {
+    const int rows_valid = u.ntok << shift_g;
+    for (int r = u.z + p.splits * warp; r < rows_valid; r += p.splits * (kThreads / 32)) {
+      // lane s has the weight of CTA s's piece
+      const float NEG_INF = __int_as_float(0xff800000);
+      const float lse = lane < p.splits ? cluster_ld(cluster_map(sLse + r * 4, lane)) : NEG_INF;
+      float top = lse;
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int s = lane + 32 * x;
-    lse[x] = s < splits ? p.part_lse[part + static_cast<long long>(s) * (2 * kRows)] : NEG_INF;
-    top = fmaxf(top, lse[x]);
-  }
+      for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float w = exp2f(lse - (top == NEG_INF ? 0.f : top));
+      float sum = w;
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-  const float shift = top == NEG_INF ? 0.f : top;
-  float w[2] = {exp2f(lse[0] - shift), exp2f(lse[1] - shift)}, sum = w[0] + w[1];
+      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      constexpr int PER = D / 32;
+      float o[PER];
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  float o[PER];
-#pragma unroll
-  for (int x = 0; x < PER; ++x) o[x] = 0.f;
+      for (int x = 0; x < PER; ++x) o[x] = 0.f;
 #pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float f = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
-    const float* src = p.part_o + (part + static_cast<long long>(s) * (2 * kRows)) * D + lane * PER;
+      for (int s = 0; s < p.splits; ++s) {
+        const float f = __shfl_sync(0xffffffffu, w, s);
+        const uint32_t at = cluster_map(sPart + part_off<D>(r, lane * PER / 4) + (lane * PER % 4) * 4, s);
+        // (a piece without a visible key was not written)
 #pragma unroll
-    for (int x = 0; x < PER; x += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(src + x);
-      o[x] += f * v.x;
-      o[x + 1] += f * v.y;
+        for (int x = 0; x < PER; x += 2) {
+          const float2 v = cluster_ld2(at + x * 4);
+          o[x] += f == 0.f ? 0.f : f * v.x;
+          o[x + 1] += f == 0.f ? 0.f : f * v.y;
+        }
+      }
+      const float inv = 1.f / sum;
+      uint16_t* dst = p.out + (u.first + (r >> shift_g)) * tok_stride + (static_cast<long long>(u.h) * p.G + (r & (p.G - 1))) * D + lane * PER;
+#pragma unroll
+      for (int x = 0; x < PER; x += 2) *reinterpret_cast<uint32_t*>(dst + x) = E::pack2(o[x] * inv, o[x + 1] * inv);
     }
   }
-  const float inv = 1.f / sum;
-#pragma unroll
-  for (int x = 0; x < PER; x += 2)
-    *reinterpret_cast<uint32_t*>(p.out + unit * D + lane * PER + x) = E::pack2(o[x] * inv, o[x + 1] * inv);
+  cluster_sync();  // others may still read this CTA's shared memory
+}
+
+template <typename E, int D>
+cudaLaunchConfig_t config(const PromptParams& p, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kPromptSmem<D>;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 1 : 0;
+  return cfg;
 }
 
 template <typename E, int D>
 cudaError_t launch_t(const PromptParams& p, cudaStream_t stream) {
-  window_prompt_kernel<E, D><<<p.ctas, kThreads, kPromptSmem<D>, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || p.splits == 1) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<long long>(p.T) * p.Hq + 7) / 8));
-  cfg.blockDim = dim3(256);
-  cfg.stream = stream;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prompt_combine_kernel<E, D>, p);
+  cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
+  cfg.stream = stream;
+  return cudaLaunchKernelEx(&cfg, window_prompt_kernel<E, D>, p);
+}
+
+// Attributes of one variant, and whether clusters of 16 CTAs can run.
+template <typename E, int D>
+cudaError_t prepare_t(bool* sixteen) {
+  cudaError_t e = cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem<D>);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  int n = 0;
+  PromptParams p{};
+  p.splits = p.ctas = 16;
+  cudaLaunchAttribute attr{};
+  const cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
+  if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, window_prompt_kernel<E, D>, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    *sixteen = false;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t prepare_window_prompt() {
-  const void* k[4] = {reinterpret_cast<const void*>(&window_prompt_kernel<ElemBf16, 64>),
-                      reinterpret_cast<const void*>(&window_prompt_kernel<ElemBf16, 128>),
-                      reinterpret_cast<const void*>(&window_prompt_kernel<ElemF16, 64>),
-                      reinterpret_cast<const void*>(&window_prompt_kernel<ElemF16, 128>)};
-  for (int x = 0; x < 4; ++x) {
-    const cudaError_t e = cudaFuncSetAttribute(k[x], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               x & 1 ? kPromptSmem<128> : kPromptSmem<64>);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+cudaError_t prepare_window_prompt(int* max_splits) {
+  bool sixteen = true;
+  cudaError_t e = prepare_t<ElemBf16, 64>(&sixteen);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128>(&sixteen);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 64>(&sixteen);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 128>(&sixteen);
+  *max_splits = sixteen ? 16 : 8;
+  return e;
 }
 
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream) {

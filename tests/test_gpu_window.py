@@ -44,10 +44,10 @@ def prompt(r, q, scale=0.0, splits=0, table=True, extra=0):
     qq = torch.cat([q, torch.full((extra, r.Hq, r.D), float("nan"), dtype=q.dtype)]).cuda()
     out = torch.full((T, r.Hq, r.D), 7.0, dtype=r.pool.dtype, device="cuda")
     ws = v.alloc_prompt_workspace(T, r.B, r.Hq, r.Hkv, r.D)
-    ws.fill_(255)
     v.vh_window_prompt_attn(qq, g["k"], g["v"], g["table"] if table else None, g["starts"], g["lens"], g["active"], out,
                             ws, window=r.window, sinks=r.sinks, sm_scale=scale, num_splits=splits, err_flag=g["err"])
     torch.cuda.synchronize()
+    assert not ws.any(), "the workspace is left zero for the next call"
     out = out.cpu()
     assert (out[r.starts[-1]:] == 7.0).all(), "tokens behind the last row were written"
     return out[:r.starts[-1]], int(g["err"])
@@ -153,9 +153,17 @@ def test_prompt_heads(heads, D, dtype):
     check_prompt(R.make([150, 77, 290], [150, 3, 140], *heads, D=D, window=90, sinks=3, dtype=dtype, layout="HND", seed=D + heads[0]))
 
 
-@pytest.mark.parametrize("splits", [1, 2, 5, 64])
+@pytest.mark.parametrize("splits", [1, 2, 4, 8, 16])
 def test_prompt_splits(splits):
     check_prompt(R.make([1500, 700, 90], [9, 150, 1], Hq=8, Hkv=2, window=1100, sinks=10, seed=splits), splits=splits)
+    check_prompt(R.make([333, 40], [1, 40], Hq=8, Hkv=1, D=64, dtype=FP, sinks=0, active=[1, 0], seed=splits), splits=splits, extra=2)
+
+
+def test_prompt_many_rows():
+    # more requests than one a lane of the drawing warp
+    lens = [1 + (37 * b) % 150 for b in range(70)]
+    news = [min(n, (13 * b) % 40) for b, n in enumerate(lens)]
+    check_prompt(R.make(lens, news, Hq=4, Hkv=2, window=50, sinks=3, active=[int(b % 7 != 2) for b in range(70)], seed=9), extra=4)
 
 
 def test_prompt_large_scores_and_scale():

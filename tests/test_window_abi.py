@@ -88,7 +88,9 @@ def test_attention_checks(call, over, code):
 def test_prompt_checks():
     assert prompt(T=-1) == v.VH_EINVAL
     assert prompt(start=None) == v.VH_EINVAL
-    assert prompt(n=65) == v.VH_EINVAL
+    assert prompt(n=32) == v.VH_EINVAL
+    assert prompt(n=3) == v.VH_EINVAL
+    assert prompt(wsb=255) in (v.VH_EWORKSPACE, v.VH_ENODEV)
     assert prompt(flags=v.VH_FLAG_PDL) == v.VH_EINVAL
     assert prompt(T=0, q=None, out=None) == v.VH_OK
     assert v.lib.vh_prompt_workspace_bytes(-1, 4, 16, 8, 128) == 0
