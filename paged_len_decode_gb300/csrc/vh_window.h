@@ -109,7 +109,8 @@ cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl);
-cudaError_t prepare_window_prompt(int* max_splits);  // once per device, every variant
+// once per device, every variant; clusters[x]: clusters of 2^x CTAs that run at a time
+cudaError_t prepare_window_prompt(int (&clusters)[5]);
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace vh

@@ -33,14 +33,14 @@ constexpr int kStageTarget = 65536;  // bytes in flight of a CTA, two CTAs on an
 struct Prepared {
   std::once_flag once;
   bool ok = false;
-  int max_splits = 1;  // largest cluster of the prompt kernel
+  int clusters[5] = {};  // clusters of 2^x CTAs of the prompt kernel that run at a time
 };
 Prepared g_prepared[kMaxDevices];
 
 bool prepared(const DeviceInfo& dev) {
   Prepared& s = g_prepared[dev.index];
   std::call_once(s.once, [&]() {
-    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(&s.max_splits) == cudaSuccess;
+    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(s.clusters) == cudaSuccess;
     if (!s.ok) cudaGetLastError();
   });
   return s.ok;
@@ -208,16 +208,18 @@ bool encode_prompt_maps(vh::PromptParams& p) {
   return false;
 }
 
-// CTAs that share a block's keys: as many as leave no SM idle, and no more than
-// a block can have key tiles.
-int prompt_splits(const vh::PromptParams& p, const DeviceInfo& dev, int max_splits) {
+// CTAs that share a block's keys: as many as leave every cluster running at
+// once, and no more than a block can have key tiles.  (16 tokens over 4100 keys,
+// 8 kv heads: 53 us with one CTA a block, 33, 23 and 18 us with 2, 4 and 8, and
+// 31 us with 16, of which half the clusters wait for the others.)
+int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
   const int per = vh::kPromptRows / p.G;
   const long long blocks = (p.T + per - 1) / per + (p.B - 1) / 2;  // rows fill their last blocks by half, say
   const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
                                                 static_cast<long long>(p.window) + p.sinks + per);
-  int s = 1;
-  while (2 * s <= max_splits && blocks * p.Hkv * 2 * s <= dev.sm_count && longest >= 128LL * 2 * s) s *= 2;
-  return s;
+  int x = 0;
+  while (x < 4 && blocks * p.Hkv <= clusters[x + 1] && longest >= (128LL << (x + 1))) ++x;
+  return 1 << x;
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? VH_OK : VH_ECUDA; }
@@ -413,8 +415,9 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
   p.D = D;
   p.G = Hq / Hkv;
   p.P = page_size;
-  const int max_splits = g_prepared[dev->index].max_splits;
-  p.splits = num_splits > 0 ? std::min(num_splits, max_splits) : prompt_splits(p, *dev, max_splits);
+  const int(&clusters)[5] = g_prepared[dev->index].clusters;
+  p.splits = num_splits > 0 ? num_splits : prompt_splits(p, clusters);
+  while (p.splits > 1 && clusters[__builtin_ctz(p.splits)] < 1) p.splits /= 2;
   const long long blocks = static_cast<long long>(T) / (vh::kPromptRows / p.G) + B, units = blocks * Hkv * p.splits;
   if (units > INT32_MAX / 2 || !encode_prompt_maps(p)) return VH_EINVAL;
   p.blocks = static_cast<int>(blocks);

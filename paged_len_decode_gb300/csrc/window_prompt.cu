@@ -815,33 +815,36 @@ cudaError_t launch_t(const PromptParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, window_prompt_kernel<E, D>, p);
 }
 
-// Attributes of one variant, and whether clusters of 16 CTAs can run.
+// Attributes of one variant, and how many of its clusters of 2^x CTAs run at a time.
 template <typename E, int D>
-cudaError_t prepare_t(bool* sixteen) {
+cudaError_t prepare_t(int (&clusters)[5]) {
   cudaError_t e = cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem<D>);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  int n = 0;
-  PromptParams p{};
-  p.splits = p.ctas = 16;
-  cudaLaunchAttribute attr{};
-  const cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
-  if (e != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, window_prompt_kernel<E, D>, &cfg) != cudaSuccess || n < 1) {
+  if (cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     cudaGetLastError();
-    *sixteen = false;
+  for (int x = 1; x <= 4; ++x) {
+    PromptParams p{};
+    p.splits = p.ctas = 1 << x;
+    cudaLaunchAttribute attr{};
+    const cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, window_prompt_kernel<E, D>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    clusters[x] = n < clusters[x] ? n : clusters[x];
   }
   return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t prepare_window_prompt(int* max_splits) {
-  bool sixteen = true;
-  cudaError_t e = prepare_t<ElemBf16, 64>(&sixteen);
-  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128>(&sixteen);
-  if (e == cudaSuccess) e = prepare_t<ElemF16, 64>(&sixteen);
-  if (e == cudaSuccess) e = prepare_t<ElemF16, 128>(&sixteen);
-  *max_splits = sixteen ? 16 : 8;
+cudaError_t prepare_window_prompt(int (&clusters)[5]) {
+  for (int& c : clusters) c = 1 << 20;
+  cudaError_t e = prepare_t<ElemBf16, 64>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 64>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 128>(clusters);
   return e;
 }
 
