@@ -8,13 +8,17 @@
 // (cos and sin from the fp32 table) and norm_*(x) = w x / sqrt(mean(x^2) + eps).
 //
 // Bound by HBM for prompts (T D (Hq (2 + out) + 8 Hkv) bytes, 3 flops an
-// element) and by latency for a decode step's few tokens.  A CTA takes
-// `tokens_per_cta` consecutive tokens: warp w first looks up token w's row,
-// slot and page and gathers the token's cos/sin row into shared memory (one
-// pair at a time, since neighbouring pairs may belong to different axes), then
-// all threads rotate units of 8 pairs (16-byte loads) and copy v.  The first
-// unit of a thread is loaded before the barrier, so its latency and the
-// look-ups' overlap.
+// element) and by latency for a decode step's few tokens.  `warps` warps share
+// a token and never meet: each looks up the token's row, slot and page itself
+// and takes a share of its heads.  A lane has the same 8 pairs of every head it
+// rotates (the D/16 neighbouring lanes of a head have its D elements), so their
+// cos and sin, gathered pair by pair where neighbouring pairs belong to different
+// axes, stay in its registers for the whole token; loads are 16 bytes, and the
+// first of them and the values are under way before anything is looked up.
+// What counts is bytes in flight: 24 warps an SM with two loads a lane each
+// measured 66 us on 16384 tokens (32 / 8 heads, 403 MB: 6.1 TB/s, 89 % of the
+// copy peak), 16 warps with four 83 us, and a CTA of 4 tokens with its angles in
+// shared memory behind a barrier 82 us.
 #include "vh_ragged.cuh"
 #include "vh_window.h"
 
@@ -22,106 +26,113 @@ namespace vh {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kMaxTok = kThreads / 32;  // tokens of a CTA: one look-up warp each
+constexpr int kThreads = 64;  // (small CTAs: no two warps need each other)
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kThreads) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
+__global__ void __launch_bounds__(kThreads, 12) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
   constexpr int HALF = D / 2;
-  constexpr int UPH = HALF / 8;  // units of a head: 8 pairs each
-  __shared__ float s_cs[kMaxTok][D];
-  __shared__ long long s_slot[kMaxTok];  // offset of the slot in the cache; -1: no append
-  __shared__ int s_live[kMaxTok];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int t0 = blockIdx.x * p.tokens_per_cta;
-  const int ntok = min(p.tokens_per_cta, p.T - t0);
-  const int heads = p.Hq + p.Hkv;
-  const int units = ntok * heads * UPH;
+  constexpr int UPH = HALF / 8;  // lanes of a head
+  constexpr int HPW = 32 / UPH;  // heads that a warp rotates at a time
+  constexpr int U = 2;           // of those, in flight
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int t = unit / p.warps, part = unit - t * p.warps;
+  if (t >= p.T) return;
   const bool ilv = p.rope_interleaved != 0;
+  const int i = (lane % UPH) * 8;                   // first pair
+  const int e0 = ilv ? 2 * i : i, e1 = ilv ? 2 * i + 8 : HALF + i;  // the lane's two runs of 8 elements
+  const int heads = p.Hq + p.Hkv, step = HPW * p.warps;
+  const uint16_t* qrow = p.q + t * p.q_stride;
+  const uint16_t* krow = p.k_new + t * p.k_stride;
 
-  // unit u: token, head (q heads first, then the new k heads) and first pair;
-  // a: the 8 first elements, b: their 8 partners (interleaved: 16 in a row)
-  uint4 a = make_uint4(0, 0, 0, 0), b = a;
-  int tk = 0, h = 0, i = 0;
-  auto load = [&](int u) {
-    const bool valid = u < units;
-    const int hu = valid ? u / UPH : 0;
-    tk = hu / heads;
-    h = hu - tk * heads;
-    i = (valid ? u % UPH : 0) * 8;
-    if (!valid) return;
-    const uint16_t* src = h < p.Hq ? p.q + (t0 + tk) * p.q_stride + h * D
-                                   : p.k_new + (t0 + tk) * p.k_stride + (h - p.Hq) * D;
-    a = ldg16(src + (ilv ? 2 * i : i));
-    b = ldg16(src + (ilv ? 2 * i + 8 : HALF + i));
+  // q heads first, then the new k heads
+  uint4 a[U], b[U];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int x = 0; x < U; ++x) {
+      const int h = h0 + x * step;
+      a[x] = b[x] = make_uint4(0u, 0u, 0u, 0u);
+      if (h < heads) {
+        const uint16_t* src = h < p.Hq ? qrow + h * D : krow + (h - p.Hq) * D;
+        a[x] = ldg16(src + e0);
+        b[x] = ldg16(src + e1);
+      }
+    }
   };
-  load(tid);
+  // the values, 16 bytes a lane: four of them travel while the rest is looked up
+  constexpr int VU = 4;
+  const int nv = p.Hkv * (D / 8), v0 = part * 32 + lane, vstep = 32 * p.warps;
+  const uint16_t* vrow = p.v_new + t * p.v_stride;
+  uint4 v[VU];
+#pragma unroll
+  for (int x = 0; x < VU; ++x)
+    if (v0 + x * vstep < nv) v[x] = ldg16(vrow + (v0 + x * vstep) * 8);
+  const int first = part * HPW + lane / UPH;
+  load(first);  // (needs nothing of what is looked up next)
 
-  // ---- look-ups: warp w for token t0 + w ------------------------------------
-  if (warp < ntok) {
-    const int t = t0 + warp;
-    const int row = p.token_start
-                        ? warp_last_at_most(p.B, t, lane, [&](int r) { return p.token_start[r]; })
-                        : t;
-    bool live = false;
-    long long slot_off = -1;
-    int slot = 0;
-    if (row >= 0) {
-      const RaggedRow r = ragged_row(p.token_start, p.seq_lens, p.active, row, p.T, p.max_pages_per_seq * p.P,
-                                     p.err_flag, lane == 0);
-      slot = r.len - (r.end - t);
-      live = r.ok && t < r.end;
-    }
-    if (live) {
-      int bad = 0;
-      int pos[HALF / 32];
+  // ---- the token's row, slot, page and angles --------------------------------
+  RaggedRow r;
+  const int row = warp_row_of_token(p.token_start, p.seq_lens, p.active, t, p.B, p.T, p.max_pages_per_seq * p.P, lane,
+                                    p.err_flag, lane == 0 && part == 0, r);
+  if (row < 0 || !r.ok) return;
+  const int slot = r.len - (r.end - t);
+  int pos = slot;
+  bool bad = false;
+  if (lane < p.num_axes) {
+    if (p.positions) pos = __ldg(p.positions + static_cast<long long>(lane) * p.T + t);
+    bad = pos < 0 || pos >= p.max_pos;  // (every axis is checked, those that no pair takes too)
+  }
+  const long long lp = static_cast<long long>(row) * p.max_pages_per_seq + slot / p.P;
+  const int page = p.page_table ? __ldg(p.page_table + lp) : static_cast<int>(lp);
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) flag_error(p.err_flag, VH_ERR_POS);
+    return;
+  }
+  float c[8], s[8];
+  const uint32_t axes = static_cast<uint32_t>(p.axis[i >> 5] >> (2 * (i & 31))) & 0xFFFFu;  // of the lane's pairs
+  const bool same = axes == (axes & 3u) * 0x5555u;
+  if (__all_sync(0xffffffffu, same)) {
+    const float* row_cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, axes & 3u)) * D + i;
 #pragma unroll
-      for (int j = 0; j < HALF / 32; ++j) {
-        const int pair = lane + 32 * j;
-        const int ax = static_cast<int>(p.axis[pair >> 5] >> (2 * (pair & 31))) & 3;
-        pos[j] = p.positions ? __ldg(p.positions + static_cast<long long>(ax) * p.T + t) : slot;
-      }
-      // every axis is checked, those that no pair takes too
-      if (lane < p.num_axes) {
-        const int x = p.positions ? __ldg(p.positions + static_cast<long long>(lane) * p.T + t) : slot;
-        bad = x < 0 || x >= p.max_pos;
-      }
-      if (__any_sync(0xffffffffu, bad)) {
-        live = false;
-        if (lane == 0) flag_error(p.err_flag, VH_ERR_POS);
-      } else {
-#pragma unroll
-        for (int j = 0; j < HALF / 32; ++j) {
-          const int pair = lane + 32 * j;
-          const float* cs = p.cos_sin + static_cast<long long>(pos[j]) * D + pair;
-          s_cs[warp][pair] = __ldg(cs);
-          s_cs[warp][HALF + pair] = __ldg(cs + HALF);
-        }
-        const long long lp = static_cast<long long>(row) * p.max_pages_per_seq + slot / p.P;
-        const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-        if (page >= 0 && page < p.num_pages)
-          slot_off = page * p.page_stride + (slot % p.P) * p.token_stride;
-        else if (lane == 0)
-          flag_error(p.err_flag, VH_ERR_PAGE);
-      }
+    for (int k = 0; k < 8; k += 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(row_cs + k));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(row_cs + HALF + k));
+      c[k] = x.x; c[k + 1] = x.y; c[k + 2] = x.z; c[k + 3] = x.w;
+      s[k] = y.x; s[k + 1] = y.y; s[k + 2] = y.z; s[k + 3] = y.w;
     }
-    if (lane == 0) {
-      s_live[warp] = live;
-      s_slot[warp] = slot_off;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float* cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, (axes >> (2 * k)) & 3u)) * D + i + k;
+      c[k] = __ldg(cs);
+      s[k] = __ldg(cs + HALF);
     }
   }
-  __syncthreads();
+  const bool page_ok = page >= 0 && page < p.num_pages;
+  if (!page_ok && lane == 0) flag_error(p.err_flag, VH_ERR_PAGE);
+  const long long slot_off = static_cast<long long>(page) * p.page_stride + (slot % p.P) * p.token_stride;
+
+  if (page_ok) {
+    auto to = [&](int u) {
+      return reinterpret_cast<uint4*>(p.v_cache + slot_off + (u / (D / 8)) * p.head_stride + (u % (D / 8)) * 8);
+    };
+#pragma unroll
+    for (int x = 0; x < VU; ++x)
+      if (v0 + x * vstep < nv) *to(v0 + x * vstep) = v[x];
+    for (int u = v0 + VU * vstep; u < nv; u += vstep) *to(u) = ldg16(vrow + u * 8);
+  }
 
   // ---- rotation (every lane runs each round: the norm's sum shuffles) ---------
-  for (int base = 0; base < units; base += kThreads) {
-    if (base > 0) load(base + tid);
-    const bool valid = base + tid < units;
-    const bool is_q = h < p.Hq;
-    float x[8], y[8];
-    {
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+  for (int h0 = first; h0 - lane / UPH < heads; h0 += U * step) {
+    if (h0 != first) load(h0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = h0 + u * step;
+      const bool is_q = h < p.Hq;
+      float x[8], y[8];
+      const uint32_t aw[4] = {a[u].x, a[u].y, a[u].z, a[u].w}, bw[4] = {b[u].x, b[u].y, b[u].z, b[u].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 fa = E::to_float2(aw[k]), fb = E::to_float2(bw[k]);
@@ -137,68 +148,56 @@ __global__ void __launch_bounds__(kThreads) mrope_kv_append_kernel(const __grid_
           y[2 * k + 1] = fb.y;
         }
       }
-    }
-    const float* nw = is_q ? p.q_norm_w : p.k_norm_w;
-    if (p.q_norm_w || p.k_norm_w) {
-      // the UPH neighbouring lanes of a head hold its D elements; summed in fp32
-      float ss = 0.f;
+      if (p.q_norm_w || p.k_norm_w) {
+        // summed in fp32 over the lanes of the head
+        float ss = 0.f;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
+        for (int k = 0; k < 8; ++k) ss += x[k] * x[k] + y[k] * y[k];
 #pragma unroll
-      for (int off = 1; off < UPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-      if (nw) {
-        const float r = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+        for (int off = 1; off < UPH; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+        const float* nw = is_q ? p.q_norm_w : p.k_norm_w;
+        if (nw) {
+          const float rs = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          x[k] = __ldg(nw + (ilv ? 2 * (i + k) : i + k)) * (x[k] * r);
-          y[k] = __ldg(nw + (ilv ? 2 * (i + k) + 1 : HALF + i + k)) * (y[k] * r);
+          for (int k = 0; k < 8; ++k) {
+            x[k] = __ldg(nw + (ilv ? 2 * (i + k) : i + k)) * (x[k] * rs);
+            y[k] = __ldg(nw + (ilv ? 2 * (i + k) + 1 : HALF + i + k)) * (y[k] * rs);
+          }
         }
       }
-    }
-    if (!valid || !s_live[tk]) continue;
-    float rx[8], ry[8];
+      if (h >= heads || !(is_q || page_ok)) continue;
+      float o0[8], o1[8];  // the two runs of 8 elements
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float c = s_cs[tk][i + k], s = s_cs[tk][HALF + i + k];
-      rx[k] = x[k] * c - y[k] * s;
-      ry[k] = y[k] * c + x[k] * s;
-    }
-    // first 8 elements and partners in memory order: two runs of 8
-    float o0[8], o1[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      o0[k] = ilv ? ((k & 1) ? ry[k / 2] : rx[k / 2]) : rx[k];
-      o1[k] = ilv ? ((k & 1) ? ry[4 + k / 2] : rx[4 + k / 2]) : ry[k];
-    }
-    const int e0 = ilv ? 2 * i : i, e1 = ilv ? 2 * i + 8 : HALF + i;
-    if (is_q && !p.q16) {
-      float* dst = static_cast<float*>(p.q_rot) + (static_cast<long long>(t0 + tk) * p.Hq + h) * D;
-      *reinterpret_cast<float4*>(dst + e0) = make_float4(o0[0], o0[1], o0[2], o0[3]);
-      *reinterpret_cast<float4*>(dst + e0 + 4) = make_float4(o0[4], o0[5], o0[6], o0[7]);
-      *reinterpret_cast<float4*>(dst + e1) = make_float4(o1[0], o1[1], o1[2], o1[3]);
-      *reinterpret_cast<float4*>(dst + e1 + 4) = make_float4(o1[4], o1[5], o1[6], o1[7]);
-    } else {
-      uint16_t* dst;
-      if (is_q) {
-        dst = static_cast<uint16_t*>(p.q_rot) + (static_cast<long long>(t0 + tk) * p.Hq + h) * D;
-      } else {
-        if (s_slot[tk] < 0) continue;
-        dst = p.k_cache + s_slot[tk] + (h - p.Hq) * p.head_stride;
+      for (int k = 0; k < 8; ++k) {
+        const float rx = x[k] * c[k] - y[k] * s[k], ry = y[k] * c[k] + x[k] * s[k];
+        if (ilv) {
+          if (k < 4) {
+            o0[2 * k] = rx;
+            o0[2 * k + 1] = ry;
+          } else {
+            o1[2 * k - 8] = rx;
+            o1[2 * k - 7] = ry;
+          }
+        } else {
+          o0[k] = rx;
+          o1[k] = ry;
+        }
       }
-      *reinterpret_cast<uint4*>(dst + e0) =
-          make_uint4(E::pack2(o0[0], o0[1]), E::pack2(o0[2], o0[3]), E::pack2(o0[4], o0[5]), E::pack2(o0[6], o0[7]));
-      *reinterpret_cast<uint4*>(dst + e1) =
-          make_uint4(E::pack2(o1[0], o1[1]), E::pack2(o1[2], o1[3]), E::pack2(o1[4], o1[5]), E::pack2(o1[6], o1[7]));
+      if (is_q && !p.q16) {
+        float* dst = static_cast<float*>(p.q_rot) + (static_cast<long long>(t) * p.Hq + h) * D;
+        *reinterpret_cast<float4*>(dst + e0) = make_float4(o0[0], o0[1], o0[2], o0[3]);
+        *reinterpret_cast<float4*>(dst + e0 + 4) = make_float4(o0[4], o0[5], o0[6], o0[7]);
+        *reinterpret_cast<float4*>(dst + e1) = make_float4(o1[0], o1[1], o1[2], o1[3]);
+        *reinterpret_cast<float4*>(dst + e1 + 4) = make_float4(o1[4], o1[5], o1[6], o1[7]);
+      } else {
+        uint16_t* dst = is_q ? static_cast<uint16_t*>(p.q_rot) + (static_cast<long long>(t) * p.Hq + h) * D
+                             : p.k_cache + slot_off + (h - p.Hq) * p.head_stride;
+        *reinterpret_cast<uint4*>(dst + e0) =
+            make_uint4(E::pack2(o0[0], o0[1]), E::pack2(o0[2], o0[3]), E::pack2(o0[4], o0[5]), E::pack2(o0[6], o0[7]));
+        *reinterpret_cast<uint4*>(dst + e1) =
+            make_uint4(E::pack2(o1[0], o1[1]), E::pack2(o1[2], o1[3]), E::pack2(o1[4], o1[5]), E::pack2(o1[6], o1[7]));
+      }
     }
-  }
-
-  // ---- values: 16 bytes a thread, bit for bit ---------------------------------
-  const int vec = p.Hkv * (D / 8);
-  for (int u = tid; u < ntok * vec; u += kThreads) {
-    const int vt = u / vec, r = u - vt * vec;
-    if (!s_live[vt] || s_slot[vt] < 0) continue;
-    const uint4 w = ldg16(p.v_new + (t0 + vt) * p.v_stride + r * 8);
-    *reinterpret_cast<uint4*>(p.v_cache + s_slot[vt] + (r / (D / 8)) * p.head_stride + (r % (D / 8)) * 8) = w;
   }
 }
 
@@ -206,10 +205,11 @@ __global__ void __launch_bounds__(kThreads) mrope_kv_append_kernel(const __grid_
 
 cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
   MropeParams p = pp;
-  // One token a CTA while the tokens do not fill the GPU (latency counts), more
-  // after that: the look-ups are shared by fewer barriers.
-  p.tokens_per_cta = p.T <= 2048 ? 1 : 4;
-  const int grid = (p.T + p.tokens_per_cta - 1) / p.tokens_per_cta;
+  // A token's heads over several warps while the tokens do not fill the GPU: 64
+  // tokens (16 / 8 heads) take 4.4 us with 8 warps each and 6.3 with 1, 800 6.3 with
+  // up to 4 and 8.4 with 8, 2000 10.4 with 1, 11.8 with 2 and 16.6 with 8.
+  p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
+  const int grid = static_cast<int>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32));
   if (p.D == 128) {
     if (p.f16) mrope_kv_append_kernel<ElemF16, 128><<<grid, kThreads, 0, stream>>>(p);
     else mrope_kv_append_kernel<ElemBf16, 128><<<grid, kThreads, 0, stream>>>(p);

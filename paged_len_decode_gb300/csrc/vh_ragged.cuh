@@ -46,4 +46,33 @@ __device__ __forceinline__ RaggedRow ragged_row(const int32_t* token_start, cons
   return r;
 }
 
+// The row of token t, by one warp; -1 if it belongs to none.  Up to 32 rows are
+// read at once, one a lane, so that a look-up costs one round trip to memory;
+// with more rows the row is searched first.
+__device__ __forceinline__ int warp_row_of_token(const int32_t* token_start, const int32_t* seq_lens,
+                                                 const int32_t* active, int t, int B, int T, int max_len, int lane,
+                                                 int32_t* err_flag, bool report, RaggedRow& r) {
+  if (token_start && B <= 32) {
+    RaggedRow mine{};
+    bool here = false;
+    if (lane < B) {
+      mine = ragged_row(token_start, seq_lens, active, lane, T, max_len, nullptr, false);
+      here = mine.start <= t && t < mine.end;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, here);
+    if (hit == 0) return -1;
+    const int row = 31 - __clz(hit);
+    r.start = __shfl_sync(0xffffffffu, mine.start, row);
+    r.end = __shfl_sync(0xffffffffu, mine.end, row);
+    r.len = __shfl_sync(0xffffffffu, mine.len, row);
+    r.ok = __shfl_sync(0xffffffffu, mine.ok ? 1 : 0, row) != 0;
+    if (!r.ok && report && active[row]) flag_error(err_flag, VH_ERR_SEQLEN);
+    return row;
+  }
+  const int row = token_start ? warp_last_at_most(B, t, lane, [&](int b) { return __ldg(token_start + b); }) : t;
+  if (row < 0) return -1;
+  r = ragged_row(token_start, seq_lens, active, row, T, max_len, err_flag, report);
+  return t < r.end ? row : -1;
+}
+
 }  // namespace vh

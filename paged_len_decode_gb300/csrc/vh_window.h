@@ -39,7 +39,7 @@ struct MropeParams {
   int rope_interleaved, f16;
   int32_t* err_flag;
   int T, B, Hq, Hkv, D, P;
-  int tokens_per_cta;
+  int warps;                   // that share a token
 };
 
 struct WindowDecodeParams {
