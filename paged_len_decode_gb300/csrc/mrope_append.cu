@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(kThreads, 12) mrope_kv_append_kernel(const __g
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int t = unit / p.warps, part = unit - t * p.warps;
+  pdl_begin();
   if (t >= p.T) return;
   const bool ilv = p.rope_interleaved != 0;
   const int i = (lane % UPH) * 8;                   // first pair
@@ -209,15 +210,10 @@ cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
   // tokens (16 / 8 heads) take 4.4 us with 8 warps each and 6.3 with 1, 800 6.3 with
   // up to 4 and 8.4 with 8, 2000 10.4 with 1, 11.8 with 2 and 16.6 with 8.
   p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
-  const int grid = static_cast<int>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32));
-  if (p.D == 128) {
-    if (p.f16) mrope_kv_append_kernel<ElemF16, 128><<<grid, kThreads, 0, stream>>>(p);
-    else mrope_kv_append_kernel<ElemBf16, 128><<<grid, kThreads, 0, stream>>>(p);
-  } else {
-    if (p.f16) mrope_kv_append_kernel<ElemF16, 64><<<grid, kThreads, 0, stream>>>(p);
-    else mrope_kv_append_kernel<ElemBf16, 64><<<grid, kThreads, 0, stream>>>(p);
-  }
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32)));
+  return launch_dependent(p.D == 128 ? (p.f16 ? mrope_kv_append_kernel<ElemF16, 128> : mrope_kv_append_kernel<ElemBf16, 128>)
+                                     : (p.f16 ? mrope_kv_append_kernel<ElemF16, 64> : mrope_kv_append_kernel<ElemBf16, 64>),
+                          p, grid, kThreads, 0, stream);
 }
 
 }  // namespace vh

@@ -6,6 +6,17 @@
 
 namespace vh {
 
+// These kernels are always launched as programmatic dependents: their CTAs may
+// take their places while the previous kernel on the stream still runs, but
+// touch no memory before this wait has returned, when that kernel and all
+// before it are complete.  Only then may the next kernel do the same, so one
+// that reads ahead of its own wait (VH_FLAG_PDL) meets finished work as it would
+// behind an ordinary launch.
+__device__ __forceinline__ void pdl_begin() {
+  pdl_wait();
+  pdl_launch_dependents();
+}
+
 // Largest b in [0, B) with key(b) <= x, for a non-decreasing key; -1 if there
 // is none.  One warp: every round probes 32 places at once, so 1000 rows take
 // two rounds of loads (a thread alone would take ten).

@@ -61,6 +61,7 @@ struct WindowDecodeParams {
   float* part_lse;             // [groups][N][2][Hc*G], base 2
   int32_t* err_flag;
   int f16;
+  int early;                   // VH_FLAG_PDL: lengths, flags and page ids are read before the dependency wait
   int B, Hq, Hkv, D, G, P;
   int Hc, groups, N, stages, min_tiles;
   int stage_bytes;             // K then V of one tile: [D/64][Hc][16 tokens][128 B swizzled] each
@@ -105,10 +106,30 @@ struct PromptParams {
   int* counter;                // the next unit to be drawn (splits == 1); zero between calls
 };
 
+// The launch of kernels that begin with pdl_begin (vh_ragged.cuh).
+template <typename P>
+inline cudaError_t launch_dependent(void (*kernel)(P), const P& p, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                                    int cluster = 1) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
-cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl);
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream);
 // once per device, every variant; clusters[x]: clusters of 2^x CTAs that run at a time
 cudaError_t prepare_window_prompt(int (&clusters)[5]);
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);

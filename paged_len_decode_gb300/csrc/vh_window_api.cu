@@ -360,7 +360,8 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   p.err_flag = err_flag;
   const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D));
   p.scale_log2 = scale * 1.4426950408889634f;
-  return status_of(vh::launch_window_decode(p, static_cast<cudaStream_t>(stream), (flags & VH_FLAG_PDL) != 0));
+  p.early = (flags & VH_FLAG_PDL) != 0;
+  return status_of(vh::launch_window_decode(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {

@@ -25,7 +25,7 @@
 //  * Merge: partial (o, lse) go to the workspace; a counter per row tells the
 //    last CTA to arrive, which adds the pieces in their order in the row, so
 //    the result does not depend on who is last.
-#include "vh_common.cuh"
+#include "vh_ragged.cuh"
 #include "vh_window.h"
 
 namespace vh {
@@ -34,6 +34,7 @@ namespace {
 
 constexpr int kMaxHeads = 8;                 // kv heads (consumer warps) of a CTA
 constexpr int kThreadsMax = 32 * (kMaxHeads + 1);
+constexpr int kWarpRows = 128;               // rows that the producer warp sums up alone
 enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscPart = 34, kMiscInts = 48 };  // part: 4 ints each
 
 __device__ __forceinline__ int share_begin(int c, int n, int total) {
@@ -120,36 +121,68 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   const int max_len = p.max_pages_per_seq * p.P;
   const bool p8 = p.P == 8;
   const float NEG_INF = __int_as_float(0xff800000);
-  pdl_launch_dependents();
+  if (p.early) pdl_launch_dependents();
+  else pdl_begin();
 
-  // ---- work list (lengths, flags and page ids are read before the wait) -------
-  if (tid == 0) {
-    *abort_flag = 0;
-    misc[kMiscLost] = 0;
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full0 + 8 * s, 1);
-      mbar_init(empty0 + 8 * s, Hc);
-    }
-    mbar_init(qfull, 1);
-    mbar_init(qempty, Hc);
-    fence_barrier_init();
-    cum[0] = 0;
-  }
-  for (int b = tid; b < p.B; b += blockDim.x) {
+  // ---- work list (with VH_FLAG_PDL, before the wait) -------------------------------
+  // Up to kWarpRows rows are counted and summed by the producer warp, which goes
+  // on to its first copies while the consumers wait for the sums; more rows by
+  // all threads.
+  auto count_row = [&](int b) -> int {
     const int act = p.active[b], L = p.seq_lens[b];
     const bool ok = act && L >= 1 && L <= max_len;
     if (act && !ok && c == 0 && gy == 0) flag_error(p.err_flag, VH_ERR_SEQLEN);
-    cum[1 + b] = ok ? tiles_of(L, p.window, p.sinks).count : 0;
     lens[b] = L;
+    return ok ? tiles_of(L, p.window, p.sinks).count : 0;
+  };
+  if (warp == Hc) {
+    if (lane == 0) {
+      *abort_flag = 0;
+      misc[kMiscLost] = 0;
+      for (int s = 0; s < S; ++s) {
+        mbar_init(full0 + 8 * s, 1);
+        mbar_init(empty0 + 8 * s, Hc);
+      }
+      mbar_init(qfull, 1);
+      mbar_init(qempty, Hc);
+      fence_barrier_init();
+      cum[0] = 0;
+    }
+    if (p.B <= kWarpRows) {
+      int n[kWarpRows / 32], run = 0;
+#pragma unroll
+      for (int x = 0; x < kWarpRows / 32; ++x) n[x] = x * 32 + lane < p.B ? count_row(x * 32 + lane) : 0;
+#pragma unroll
+      for (int x = 0; x < kWarpRows / 32; ++x) {
+        if (x * 32 >= p.B) break;
+        int v = n[x];
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, v, off);
+          if (lane >= off) v += y;
+        }
+        v += run;
+        if (x * 32 + lane < p.B) cum[1 + x * 32 + lane] = v;
+        run = __shfl_sync(0xffffffffu, v, 31);
+      }
+      __syncwarp();
+      asm volatile("bar.arrive 2, %0;" ::"r"(static_cast<int>(blockDim.x)) : "memory");
+    }
+  } else if (p.B <= kWarpRows) {
+    named_sync(2, blockDim.x);
   }
-  __syncthreads();
-  scan_rows(cum, p.B, misc + kMiscTot);
+  if (p.B > kWarpRows) {
+    for (int b = tid; b < p.B; b += blockDim.x) cum[1 + b] = count_row(b);
+    __syncthreads();
+    scan_rows(cum, p.B, misc + kMiscTot);
+  }
   const int T = cum[p.B];
   const int n_eff = min(p.N, (T + p.min_tiles - 1) / p.min_tiles);  // 0 if there is no work
   const bool works = c < n_eff;
   const int t0 = works ? share_begin(c, n_eff, T) : 0, t1 = works ? share_begin(c + 1, n_eff, T) : 0;
   const int b0 = works ? row_of(cum, 0, p.B, t0) : 0;
   const int tpp = (p.P + kTile - 1) / kTile;  // tiles of a page
+  const int tpp_shift = (tpp & (tpp - 1)) == 0 ? __ffs(tpp) - 1 : -1;
 
   // ---- padding rows, dealt out to the CTAs, are written as zeros ---------------
   auto zero_rows = [&]() {
@@ -181,19 +214,19 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         if (d.mask & 0x00FFu) d.page = page_at(2 * tk);
         if (d.mask & 0xFF00u) d.page2 = page_at(2 * tk + 1);
       } else {
-        d.page = page_at(tk / tpp);
-        d.tok = (tk % tpp) * kTile;
+        const int j = tpp_shift >= 0 ? tk >> tpp_shift : tk / tpp;
+        d.page = page_at(j);
+        d.tok = (tk - j * tpp) * kTile;
       }
       return d;
     };
     Tile cur{}, nxt{};
     if (works) {
       cur = describe(t0 + lane);
-      nxt = describe(t0 + 32 + lane);
       if (lane == 0) prefetch_tensormap(&p.tmap_k);
       if (lane == 1) prefetch_tensormap(&p.tmap_v);
     }
-    pdl_wait();
+    if (p.early) pdl_wait();
     zero_rows();
     if (!works) return;
     // Boxes of this lane.  Whole tiles: lanes 0 .. 2 HALVES - 1 take (K or V,
@@ -209,10 +242,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
     bool aborted = false;
     for (int t = t0; t < t1; ++t, ++issued) {
       const int w = (t - t0) & 31;
-      if (w == 0 && t > t0) {
-        cur = nxt;
-        nxt = describe(t + 32 + lane);
-      }
+      if (w == 0 && t > t0) cur = nxt;
       const int row = __shfl_sync(0xffffffffu, cur.row, w), tok = __shfl_sync(0xffffffffu, cur.tok, w);
       const uint32_t mask = __shfl_sync(0xffffffffu, cur.mask, w);
       int page = __shfl_sync(0xffffffffu, cur.page, w), page2 = __shfl_sync(0xffffffffu, cur.page2, w);
@@ -258,6 +288,8 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         stage = 0;
         ++round;
       }
+      // the next 32 tiles, well ahead, but not before the first copies are under way
+      if (w == 7) nxt = describe(t - w + 32 + lane);
     }
     if (aborted) {
       if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
@@ -270,7 +302,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   }
 
   // ========================= consumer warps ======================================
-  pdl_wait();
+  if (p.early) pdl_wait();
   zero_rows();
   if (!works) return;
   const int w = warp, h = h0 + w;
@@ -466,21 +498,19 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   named_sync(1, 32 * Hc);
   // (only consumers set this one, before the barrier: they all see the same)
   if (*reinterpret_cast<volatile int*>(misc + kMiscLost) || npart == 0) return;
-  if (tid == 0) {
-    for (int k = 0; k < npart; ++k) {
-      const int rb = part_row[k];
-      const int first = share_of(cum[rb], n_eff, T), last = share_of(cum[rb + 1] - 1, n_eff, T);
-      // acquire-release at GPU scope: publishes this CTA's pieces (ordered before
-      // it by the barrier) and lets the last one see all others
-      int* counter = p.counters + static_cast<long long>(gy) * p.B + rb;
-      const bool mine = atom_add_acq_rel_gpu(counter, 1) == last - first;
-      if (mine) *counter = 0;  // ready for the next call
-      int* v = misc + kMiscPart + 4 * k;
-      v[0] = mine ? 1 : 0;
-      v[1] = first;
-      v[2] = last - first + 1;
-      v[3] = share_begin(first, n_eff, T) == cum[rb] ? 0 : 1;  // the first piece's slot
-    }
+  if (tid < npart) {  // (a thread a piece: their counters answer at the same time)
+    const int rb = tid == 0 ? part_row[0] : part_row[1];
+    const int first = share_of(cum[rb], n_eff, T), last = share_of(cum[rb + 1] - 1, n_eff, T);
+    // acquire-release at GPU scope: publishes this CTA's pieces (ordered before
+    // it by the barrier) and lets the last one see all others
+    int* counter = p.counters + static_cast<long long>(gy) * p.B + rb;
+    const bool mine = atom_add_acq_rel_gpu(counter, 1) == last - first;
+    if (mine) *counter = 0;  // ready for the next call
+    int* v = misc + kMiscPart + 4 * tid;
+    v[0] = mine ? 1 : 0;
+    v[1] = first;
+    v[2] = last - first + 1;
+    v[3] = share_begin(first, n_eff, T) == cum[rb] ? 0 : 1;  // the first piece's slot
   }
   named_sync(1, 32 * Hc);
 
@@ -564,29 +594,29 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   }
 }
 
+using Kernel = void (*)(WindowDecodeParams);
+
 template <typename E>
-const void* select_t(int D, int G) {
+Kernel select_t(int D, int G) {
   if (D == 128) {
     switch (G) {
-      case 1: return reinterpret_cast<const void*>(&window_decode_kernel<128, 1, E>);
-      case 2: return reinterpret_cast<const void*>(&window_decode_kernel<128, 2, E>);
-      case 4: return reinterpret_cast<const void*>(&window_decode_kernel<128, 4, E>);
-      case 8: return reinterpret_cast<const void*>(&window_decode_kernel<128, 8, E>);
+      case 1: return &window_decode_kernel<128, 1, E>;
+      case 2: return &window_decode_kernel<128, 2, E>;
+      case 4: return &window_decode_kernel<128, 4, E>;
+      case 8: return &window_decode_kernel<128, 8, E>;
     }
   } else if (D == 64) {
     switch (G) {
-      case 1: return reinterpret_cast<const void*>(&window_decode_kernel<64, 1, E>);
-      case 2: return reinterpret_cast<const void*>(&window_decode_kernel<64, 2, E>);
-      case 4: return reinterpret_cast<const void*>(&window_decode_kernel<64, 4, E>);
-      case 8: return reinterpret_cast<const void*>(&window_decode_kernel<64, 8, E>);
+      case 1: return &window_decode_kernel<64, 1, E>;
+      case 2: return &window_decode_kernel<64, 2, E>;
+      case 4: return &window_decode_kernel<64, 4, E>;
+      case 8: return &window_decode_kernel<64, 8, E>;
     }
   }
   return nullptr;
 }
 
-const void* select_kernel(int D, int G, bool f16) {
-  return f16 ? select_t<ElemF16>(D, G) : select_t<ElemBf16>(D, G);
-}
+Kernel select_kernel(int D, int G, bool f16) { return f16 ? select_t<ElemF16>(D, G) : select_t<ElemBf16>(D, G); }
 
 }  // namespace
 
@@ -606,19 +636,9 @@ cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per
                                                        32 * (p.Hc + 1), p.smem_bytes);
 }
 
-cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream, bool pdl) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.N, p.groups);
-  cfg.blockDim = dim3(32 * (p.Hc + 1));
-  cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_bytes);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = pdl ? 1 : 0;
-  void* args[] = {const_cast<WindowDecodeParams*>(&p)};
-  return cudaLaunchKernelExC(&cfg, select_kernel(p.D, p.G, p.f16 != 0), args);
+cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream) {
+  return launch_dependent(select_kernel(p.D, p.G, p.f16 != 0), p, dim3(p.N, p.groups), 32 * (p.Hc + 1),
+                          static_cast<size_t>(p.smem_bytes), stream);
 }
 
 }  // namespace vh

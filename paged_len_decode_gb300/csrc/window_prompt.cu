@@ -281,8 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   auto u_full = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + s); };
   auto u_empty = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + kSlots + s); };
   volatile int* abort_flag = &s_abort;
-  Rows rows{};
-  if (warp == kDrawWarp && p.B <= 32) rows = rows_of(p, lane);
   if (tid == 0) {
     s_abort = 0;
     for (int s = 0; s < ST; ++s) {
@@ -309,6 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_begin();
   const uint32_t tmem = s_tmem;
   auto t_scores = [&](int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
   auto t_out = [&](int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
@@ -333,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       // ======================= the CTA's next unit =====================================
       // The first is the CTA's own number; the others come from the counter, which
       // the last draw of all sets back for the next call.  A cluster has one unit a CTA.
+      Rows rows{};
+      if (p.B <= 32) rows = rows_of(p, lane);
       const int units = p.blocks * p.Hkv * p.splits;
       int u = blockIdx.x;
       for (int n = 0;; ++n) {
@@ -807,14 +808,6 @@ cudaLaunchConfig_t config(const PromptParams& p, cudaLaunchAttribute* attr) {
   return cfg;
 }
 
-template <typename E, int D>
-cudaError_t launch_t(const PromptParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr{};
-  cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
-  cfg.stream = stream;
-  return cudaLaunchKernelEx(&cfg, window_prompt_kernel<E, D>, p);
-}
-
 // Attributes of one variant, and how many of its clusters of 2^x CTAs run at a time.
 template <typename E, int D>
 cudaError_t prepare_t(int (&clusters)[5]) {
@@ -849,8 +842,9 @@ cudaError_t prepare_window_prompt(int (&clusters)[5]) {
 }
 
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream) {
-  if (p.D == 128) return p.f16 ? launch_t<ElemF16, 128>(p, stream) : launch_t<ElemBf16, 128>(p, stream);
-  return p.f16 ? launch_t<ElemF16, 64>(p, stream) : launch_t<ElemBf16, 64>(p, stream);
+  return launch_dependent(p.D == 128 ? (p.f16 ? window_prompt_kernel<ElemF16, 128> : window_prompt_kernel<ElemBf16, 128>)
+                                     : (p.f16 ? window_prompt_kernel<ElemF16, 64> : window_prompt_kernel<ElemBf16, 64>),
+                          p, dim3(p.ctas), kThreads, p.D == 128 ? kPromptSmem<128> : kPromptSmem<64>, stream, p.splits);
 }
 
 }  // namespace vh
