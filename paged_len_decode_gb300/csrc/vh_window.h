@@ -71,7 +71,6 @@ struct WindowDecodeParams {
 // The prompt kernel's ring of K and V stages and its shared memory: the
 // queries of both row tiles, the stages, 32 KB through which outputs leave, and
 // up to 1024 bytes to align them.
-constexpr int kPromptRows = 256;  // (token, head) rows of a block
 template <int D>
 constexpr int kPromptStages = D == 128 ? 4 : 6;
 template <int D>
@@ -100,9 +99,13 @@ struct PromptParams {
   int32_t* err_flag;
   int f16;
   int T, B, Hq, Hkv, D, G, P;
-  int blocks;                  // T / (256 / G) + B: an upper bound (rows fill their last block partly)
+  int pair;                    // blocks of 128 (token, head) rows, by both warpgroups; else of 256
+  int shift_block;             // log2 of a block's tokens
+  int blocks;                  // T >> shift_block, + B: an upper bound (rows fill their last block partly)
   int splits;                  // CTAs that share the keys of a block (a cluster): 1, 2, 4, 8 or 16
   int ctas;
+  int shift_g, shift_splits, shift_page;  // log2 of G, splits and P (-1: not a power of two)
+  uint32_t hkv_inverse;        // ceil(2^32 / Hkv), 0 for Hkv == 1: v / Hkv of v < 2^32 / Hkv is the high word of v times it
   int* counter;                // the next unit to be drawn (splits == 1); zero between calls
 };
 

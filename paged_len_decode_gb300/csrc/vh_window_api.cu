@@ -208,15 +208,27 @@ bool encode_prompt_maps(vh::PromptParams& p) {
   return false;
 }
 
+// Blocks that T tokens of B rows make, with 2^shift tokens in a block (rows fill
+// their last blocks by half, say; the kernel finds the number itself).
+long long likely_blocks(int T, int B, int shift) {
+  return ((static_cast<long long>(T) + (1 << shift) - 1) >> shift) + (B - 1) / 2;
+}
+
+// Small blocks (128 rows, both warpgroups on them) where they fit the SMs once: a
+// prompt of 1000 tokens (16 / 8 heads, 128 such blocks, window 256) takes 12 us
+// with them and 19 us with blocks of 256 rows, one of 2000 tokens (256) 18 and 15.
+bool small_blocks(int T, int B, int G, int Hkv, const DeviceInfo& dev) {
+  return likely_blocks(T, B, 7 - __builtin_ctz(G)) * Hkv <= dev.sm_count;
+}
+
 // CTAs that share a block's keys: as many as leave every cluster running at
 // once, and no more than a block can have key tiles.  (16 tokens over 4100 keys,
-// 8 kv heads: 53 us with one CTA a block, 33, 23 and 18 us with 2, 4 and 8, and
-// 31 us with 16, of which half the clusters wait for the others.)
+// 8 kv heads: 33 us with one CTA a block, 23, 17 and 15 us with 2, 4 and 8, and
+// 27 us with 16, of which half the clusters wait for the others.)
 int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
-  const int per = vh::kPromptRows / p.G;
-  const long long blocks = (p.T + per - 1) / per + (p.B - 1) / 2;  // rows fill their last blocks by half, say
   const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
-                                                static_cast<long long>(p.window) + p.sinks + per);
+                                                static_cast<long long>(p.window) + p.sinks + (1 << p.shift_block));
+  const long long blocks = likely_blocks(p.T, p.B, p.shift_block);
   int x = 0;
   while (x < 4 && blocks * p.Hkv <= clusters[x + 1] && longest >= (128LL << (x + 1))) ++x;
   return 1 << x;
@@ -417,10 +429,16 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
   p.G = Hq / Hkv;
   p.P = page_size;
   const int(&clusters)[5] = g_prepared[dev->index].clusters;
+  p.shift_g = __builtin_ctz(p.G);
+  p.pair = small_blocks(T, B, p.G, Hkv, *dev);
+  p.shift_block = (p.pair ? 7 : 8) - p.shift_g;
   p.splits = num_splits > 0 ? num_splits : prompt_splits(p, clusters);
   while (p.splits > 1 && clusters[__builtin_ctz(p.splits)] < 1) p.splits /= 2;
-  const long long blocks = static_cast<long long>(T) / (vh::kPromptRows / p.G) + B, units = blocks * Hkv * p.splits;
-  if (units > INT32_MAX / 2 || !encode_prompt_maps(p)) return VH_EINVAL;
+  const long long blocks = (static_cast<long long>(T) >> p.shift_block) + B, units = blocks * Hkv * p.splits;
+  if (units > INT32_MAX / 2 || blocks * Hkv > (1LL << 32) / Hkv - 1 || !encode_prompt_maps(p)) return VH_EINVAL;
+  p.shift_splits = __builtin_ctz(p.splits);
+  p.shift_page = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(page_size) : -1;
+  p.hkv_inverse = Hkv == 1 ? 0u : static_cast<uint32_t>(((1ULL << 32) + Hkv - 1) / Hkv);
   p.blocks = static_cast<int>(blocks);
   // CTAs draw units one after the other; a cluster's CTAs have one each
   p.ctas = static_cast<int>(p.splits > 1 ? units : std::min<long long>(units, dev->sm_count));

@@ -12,7 +12,9 @@
 //    less and K and V are read once for the whole group.  The rows form two
 //    tiles of 128, whose products and softmax alternate: while one tile's
 //    scores are turned into weights, the tensor cores work for the other.  A
-//    block holds tokens of one request.
+//    block holds tokens of one request.  Where such blocks would be few or
+//    mostly empty, they have 128 rows (PAIR): the two tiles are then the same
+//    rows, over alternate key tiles, and their accumulators are added at the end.
 //  * Keys.  Tiles of 128 slots: those that hold sinks, then those from the
 //    first query's window to the last query.  Each is copied box by box through
 //    the page table; boxes that nobody sees, and bad page ids, become a page
@@ -56,6 +58,11 @@ constexpr int kSlots = 2;        // blocks drawn: this one and the next
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
+template <int M>
+struct Place {
+  static constexpr int value = M;
+};
+
 // One CTA's work: queries of one request and kv head, and a share of their key tiles.
 struct Unit {
   int row, first, ntok;         // request, first token, tokens
@@ -88,12 +95,12 @@ struct Rows {
 
 __device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
   Rows x{};
-  const int per = 2 * kRows / p.G;
+  const int per = 1 << p.shift_block;
   int weight = -1;
   if (lane < p.B) {
     x.r = ragged_row(p.token_start, p.seq_lens, p.active, lane, p.T, p.max_pages_per_seq * p.P, p.err_flag, blockIdx.x == 0);
     const int n = x.r.start >= 0 ? min(x.r.end, p.T) - x.r.start : 0;
-    x.blocks = n > 0 ? (n + per - 1) / per : 0;
+    x.blocks = n > 0 ? (n + per - 1) >> p.shift_block : 0;
     if (x.r.ok && n > 0) {
       int a, b;
       list_tiles(p, x.r.len - min(n, per), min(n, per), a, b, weight);
@@ -116,11 +123,11 @@ __device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
 __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows, int u, int lane) {
   Unit r{};
   r.more = 1;
-  const int per = 2 * kRows / p.G;
-  r.z = u % p.splits;
-  const int v = u / p.splits;
-  r.h = v % p.Hkv;
-  const int i = v / p.Hkv;
+  const int per = 1 << p.shift_block;
+  r.z = u & (p.splits - 1);
+  const int v = u >> p.shift_splits;
+  const int i = static_cast<int>(__umulhi(static_cast<uint32_t>(v), p.hkv_inverse)) - (p.hkv_inverse == 0 ? -v : 0);  // v / Hkv
+  r.h = v - i * p.Hkv;
   RaggedRow g{};
   int n;  // number of the block in its request
   if (p.B <= 32) {
@@ -135,11 +142,11 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows,
     n = __shfl_sync(0xffffffffu, rows.blocks, r.row) - 1 - (i - __shfl_sync(0xffffffffu, rows.before, r.row));
   } else {
     const int bi = p.blocks - 1 - i;
-    r.row = warp_last_at_most(p.B, bi, lane, [&](int b) { return p.token_start[b] / per + b; });
+    r.row = warp_last_at_most(p.B, bi, lane, [&](int b) { return (p.token_start[b] >> p.shift_block) + b; });
     if (r.row < 0) return r;
     g = ragged_row(p.token_start, p.seq_lens, p.active, r.row, p.T, p.max_pages_per_seq * p.P, p.err_flag,
                    lane == 0 && r.h == 0 && r.z == 0);
-    n = bi - (g.start / per + r.row);
+    n = bi - ((g.start >> p.shift_block) + r.row);
   }
   r.first = g.start + n * per;
   r.ntok = min(per, min(g.end, p.T) - r.first);
@@ -246,7 +253,7 @@ __device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, 
   }
 }
 
-template <typename E, int D>
+template <typename E, int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid_constant__ PromptParams p) {
   constexpr int HALVES = D / 64;
   constexpr int KS = D / 16;                   // k-steps of the score product
@@ -258,18 +265,17 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   constexpr uint32_t kValues = tc_kind_f16(kRows, D, !E::kF16, true);
   extern __shared__ __align__(128) unsigned char smem_raw[];
   __shared__ Unit s_units[kSlots];
-  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 8 + 2 * kSlots];
+  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 11 + 2 * kSlots];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const int per_tile = kRows / p.G;  // tokens of a row tile
-  const int shift_g = __ffs(p.G) - 1;
+  const int shift_g = p.shift_g, per_tile = kRows >> shift_g;  // tokens of a row tile
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
 
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + QB * 2 * kQTile, sOut = sKV + ST * kStage;
   // partial results of a CTA in a cluster, over the queries and stages, and beside them
-  const uint32_t sPart = base, sLse = sOut;
+  const uint32_t sPart = base, sLse = sOut + 7 * 4096 + 1024;  // (behind what the last warp stages)
   const uint32_t bars = smem_addr(s_bars);
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 8 * (ST + s); };
@@ -278,8 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   auto s_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + m); };
   auto p_full = [&](int m, int half) { return bars + 8 * (2 * ST + 2 * QB + 2 + 2 * m + half); };
   auto o_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 6 + m); };
-  auto u_full = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + s); };
-  auto u_empty = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 8 + kSlots + s); };
+  auto o_seen = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 8 + m); };
+  const uint32_t met = bars + 8 * (2 * ST + 2 * QB + 10);  // both softmax warpgroups
+  auto u_full = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 11 + s); };
+  auto u_empty = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 11 + kSlots + s); };
   volatile int* abort_flag = &s_abort;
   if (tid == 0) {
     s_abort = 0;
@@ -296,7 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       mbar_init(p_full(m, 0), kRows);
       mbar_init(p_full(m, 1), kRows);
       mbar_init(o_full(m), 1);
+      mbar_init(o_seen(m), 4);
     }
+    mbar_init(met, 2 * kRows);
     for (int x = 0; x < kSlots; ++x) {
       mbar_init(u_full(x), 1);
       mbar_init(u_empty(x), 11);  // every warp but the drawing one
@@ -308,9 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   __syncthreads();
   tc_fence_after();
   pdl_begin();
-  const uint32_t tmem = s_tmem;
-  auto t_scores = [&](int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
-  auto t_out = [&](int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
+  auto t_scores = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
+  auto t_out = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
   // waits for unit number n of this CTA; false: the CTA is done (or gives up)
   auto next_unit = [&](int n, bool& lost) -> bool {
     lost = !mbar_wait(u_full(n % kSlots), (n / kSlots) & 1);
@@ -383,9 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           if (lane < nbox) {
             const int j = j0 + lane * p.box;
             if (j <= last && (j < p.sinks || j + p.box > low)) {
-              const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + j / p.P;
+              const int of_row = p.shift_page >= 0 ? j >> p.shift_page : j / p.P;
+              const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + of_row;
               page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-              tok = j % p.P;
+              tok = j - of_row * p.P;
               if (page < 0 || page >= p.num_pages) {
                 flag_error(p.err_flag, VH_ERR_PAGE);
                 page = p.num_pages;
@@ -410,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           if (k == u.k0 && kv == 0) {
             // the block's queries, once the products of the block that had
             // their place have read it (its first keys are on their way already)
-            const int b = nq % QB, ntile = u.ntok > per_tile ? 2 : 1;
+            const int b = nq % QB, ntile = !PAIR && u.ntok > per_tile ? 2 : 1;
             if (nq >= QB && !mbar_wait(q_empty(b), ((nq / QB) - 1) & 1)) {
               lost = true;
               issued += 2;
@@ -439,6 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       // The tensor cores wait whenever this warp does more between two products
       // than they have queued, so all that a tile needs is known before: its
       // place in the ring, and which row tiles see it.
+      const uint32_t tmem = s_tmem;
       uint32_t ki = 0, kp = 0, vi = 1, vp = 0;  // ring place and phase of the next K and V
       auto next = [&](uint32_t& i, uint32_t& ph) {
         i += 2;
@@ -471,85 +482,137 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
         auto scores = [&](int m) {
           if (leader) {
-            const uint32_t qa = q_operand + m * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
+            const uint32_t qa = q_operand + (PAIR ? 0 : m) * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
               const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
-              tc_mma(t_scores(m), qa + off, kb + off, kScores, s > 0);
+              tc_mma(t_scores(tmem, m), qa + off, kb + off, kScores, s > 0);
             }
             tc_commit(s_full(m));
           }
+        };
+        bool add[2] = {false, false};
+        // the block's last products of row tile m are issued; its softmax has seen the end
+        // of the block before (else it could miss this one)
+        auto finish = [&](int m) {
+          lost = lost || (nq > 1 && !mbar_wait(o_seen(m), (nq - 2) & 1));
+          if (leader && !lost) tc_commit(o_full(m));
+        };
+        // values of key tile k: slots that nobody sees may hold anything where an end of
+        // what the block sees lies inside the tile, so they become zeros
+        auto clean = [&](int k) {
+          if (k + 1 != blk.count && k + 1 != blk.sink_tiles && k != blk.sink_tiles) return;
+          const uint32_t vb = sKV + vi * kStage;
+          const int j0 = blk.tile(k) * kKeys;
+          for (int r = lane / 8; r < kKeys; r += 4) {
+            const int j = j0 + r;
+            if (j <= last && (j < p.sinks || j >= low)) continue;
+#pragma unroll
+            for (int hf = 0; hf < HALVES; ++hf)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        };
+        // the weights arrive in two halves of 64 keys
+        auto values = [&](auto place) {
+          constexpr int m = decltype(place)::value;  // (a constant, so that nothing is indexed at run time)
+          const uint32_t va = v_operand + vi * (kStage >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            lost = lost || !mbar_wait(p_full(m, half), weights[m]);
+            tc_fence_after();
+            if (leader && !lost) {
+#pragma unroll
+              for (int s = 4 * half; s < 4 * half + 4; ++s)
+                tc_mma_ta(t_out(tmem, m), t_scores(tmem, m) + s * 8, va + s * (2048 >> 4), kValues, add[m] || s > 0);
+            }
+          }
+          weights[m] ^= 1u;
+          add[m] = true;
         };
         if (!mbar_wait(q_full(qb), (nq / QB) & 1) || !mbar_wait(full(ki), kp)) {
           lost = true;
           break;
         }
         ++nq;
-        bool see[2] = {sees_k(0, k0), sees_k(1, k0)}, add[2] = {false, false};
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-          if (see[m]) scores(m);
-        if (leader) {
-          tc_commit(empty(ki));
-          if (k0 + 1 == k1) tc_commit(q_empty(qb));
-        }
-        next(ki, kp);
-        for (int k = k0; k < k1; ++k) {
-          const bool more = k + 1 < k1;
-          const bool see_next[2] = {more && sees_k(0, k + 1), more && sees_k(1, k + 1)};
-          if (!mbar_wait(full(vi), vp)) {
-            lost = true;
-            break;
+        tc_fence_after();
+        if constexpr (PAIR) {
+          scores(0);
+          if (leader) tc_commit(empty(ki));
+          next(ki, kp);
+          if (k0 + 1 < k1) {
+            lost = !mbar_wait(full(ki), kp);
+            if (lost) break;
+            scores(1);
+            if (leader) tc_commit(empty(ki));
+            next(ki, kp);
           }
-          if (k + 1 == blk.count || k + 1 == blk.sink_tiles || k == blk.sink_tiles) {
-            // an end of what the block sees may lie inside this tile: slots that
-            // nobody sees may hold anything, so their values become zeros
-            const uint32_t vb = sKV + vi * kStage;
-            const int j0 = blk.tile(k) * kKeys;
-            for (int r = lane / 8; r < kKeys; r += 4) {
-              const int j = j0 + r;
-              if (j <= last && (j < p.sinks || j >= low)) continue;
-#pragma unroll
-              for (int hf = 0; hf < HALVES; ++hf)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
-                             "r"(0u)
-                             : "memory");
+          if (leader && k0 + 2 >= k1) tc_commit(q_empty(qb));
+          // key tile k by row tile place m: its values, then the scores of the tile after next
+          auto step = [&](auto place, int k) {
+            constexpr int m = decltype(place)::value;
+            lost = !mbar_wait(full(vi), vp);
+            if (lost) return;
+            clean(k);
+            values(place);
+            if (lost) return;
+            if (leader) tc_commit(empty(vi));
+            next(vi, vp);
+            if (k + 2 >= k1) return;
+            lost = !mbar_wait(full(ki), kp);
+            if (lost) return;
+            scores(m);
+            if (leader) {
+              tc_commit(empty(ki));
+              if (k + 3 == k1) tc_commit(q_empty(qb));
             }
-            fence_proxy_async_smem();
-            __syncwarp();
+            next(ki, kp);
+          };
+          for (int k = k0; k < k1 && !lost; k += 2) {
+            step(Place<0>{}, k);
+            if (!lost && k + 1 < k1) step(Place<1>{}, k + 1);
           }
-          const uint32_t va = v_operand + vi * (kStage >> 4);
+          finish(0);
+          finish(1);
+        } else {
+          bool see[2] = {sees_k(0, k0), sees_k(1, k0)};
 #pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            if (see[m]) {
-              // the weights arrive in two halves of 64 keys
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                lost = lost || !mbar_wait(p_full(m, half), weights[m]);
-                tc_fence_after();
-                if (leader && !lost) {
-#pragma unroll
-                  for (int s = 4 * half; s < 4 * half + 4; ++s)
-                    tc_mma_ta(t_out(m), t_scores(m) + s * 8, va + s * (2048 >> 4), kValues, add[m] || s > 0);
-                }
-              }
-              weights[m] ^= 1u;
-              add[m] = true;
-            }
-            if (m == 0 && more) lost = lost || !mbar_wait(full(ki), kp);
-            if (see_next[m] && !lost) scores(m);
-            if (!more && leader && !lost) tc_commit(o_full(m));
-          }
-          if (lost) break;
+          for (int m = 0; m < 2; ++m)
+            if (see[m]) scores(m);
           if (leader) {
-            tc_commit(empty(vi));
-            if (more) tc_commit(empty(ki));
-            if (k + 2 == k1) tc_commit(q_empty(qb));  // the block's last scores are issued
+            tc_commit(empty(ki));
+            if (k0 + 1 == k1) tc_commit(q_empty(qb));
           }
-          next(vi, vp);
-          if (more) next(ki, kp);
-          see[0] = see_next[0];
-          see[1] = see_next[1];
+          next(ki, kp);
+          for (int k = k0; k < k1; ++k) {
+            const bool more = k + 1 < k1;
+            const bool see_next[2] = {more && sees_k(0, k + 1), more && sees_k(1, k + 1)};
+            if (!mbar_wait(full(vi), vp)) {
+              lost = true;
+              break;
+            }
+            clean(k);
+            if (see[0]) values(Place<0>{});
+            if (more) lost = lost || !mbar_wait(full(ki), kp);
+            if (see_next[0] && !lost) scores(0);
+            if (!more) finish(0);
+            if (see[1]) values(Place<1>{});
+            if (see_next[1] && !lost) scores(1);
+            if (!more) finish(1);
+            if (lost) break;
+            if (leader) {
+              tc_commit(empty(vi));
+              if (more) tc_commit(empty(ki));
+              if (k + 2 == k1) tc_commit(q_empty(qb));  // the block's last scores are issued
+            }
+            next(vi, vp);
+            if (more) next(ki, kp);
+            see[0] = see_next[0];
+            see[1] = see_next[1];
+          }
         }
       }
       if (lost) {
@@ -563,13 +626,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   } else {
     // ======================= softmax of row tile m =================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // (read anew: kept from the kernel's beginning they would be spilled here)
+    int tid;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+    const int lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t tmem = s_tmem;
     const int m = warp >> 2;
     const int r = tid & (kRows - 1);  // row of the tile = lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int token = m * per_tile + (r >> shift_g);
     const float NEG_INF = __int_as_float(0xff800000);
     int tiles = 0, blocks = 0;
+    uint32_t meets = 0;
     bool lost = false;
+    auto meet = [&]() {  // of both warpgroups; sets `lost` if the other does not come
+      mbar_arrive(met);
+      lost = lost || !mbar_wait(met, meets & 1);
+      ++meets;
+    };
     for (int nu = 0; !lost && next_unit(nu, lost); ++nu) {
       const Unit& blk = s_units[nu % kSlots];  // (not released before the block is done)
       if (blk.k0 == blk.k1) {
@@ -578,17 +651,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         release_unit(nu);
         continue;
       }
+      const int mq = PAIR ? 0 : m, token = mq * per_tile + (r >> shift_g);
       const int last = blk.slot + blk.ntok - 1;
-      const bool valid = token < blk.ntok;
       const int i = min(blk.slot + token, last);
-      const int f = blk.slot + m * per_tile;                 // first and last query of the tile
+      const int f = blk.slot + mq * per_tile;                // first and last query of the tile
       const int e = min(last, f + per_tile - 1);
       float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
       float2 sum2 = make_float2(0.f, 0.f);
       int n = 0;
       for (int k = blk.k0; k < blk.k1; ++k) {
         const int t = blk.tile(k);
-        if (f > last || t > e / kKeys || (t >= blk.sink_tiles && t < max(0, f - p.window + 1) / kKeys)) continue;  // not seen
+        if (PAIR ? ((k - blk.k0) & 1) != m
+                 : f > last || t > e / kKeys || (t >= blk.sink_tiles && t < max(0, f - p.window + 1) / kKeys))
+          continue;  // not this warpgroup's, or not seen
         if (!mbar_wait(s_full(m), tiles & 1)) {
           lost = true;
           break;
@@ -596,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         tc_fence_after();
         uint32_t sc[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(m) + lanes + c * 32, sc[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(tmem, m) + lanes + c * 32, sc[c]);
         tmem_wait_ld();
         const int j0 = t * kKeys;
         if (j0 + kKeys - 1 > f || (j0 <= e - p.window && j0 + kKeys > p.sinks)) {
@@ -626,11 +701,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
 #pragma unroll 1
           for (int c = 0; c < D; c += 8) {
             uint32_t o[8];
-            tmem_ld8(t_out(m) + lanes + c, o);
+            tmem_ld8(t_out(tmem, m) + lanes + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-            tmem_st8(t_out(m) + lanes + c, o);
+            tmem_st8(t_out(tmem, m) + lanes + c, o);
           }
           sum2.x *= by;
           sum2.y *= by;
@@ -651,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             w[x] = E::pack2(v.x, v.y);
           }
           sum2 = fadd2(sum2, fadd2(add[0], add[1]));
-          tmem_st32(t_scores(m) + lanes + half * 32, w);
+          tmem_st32(t_scores(tmem, m) + lanes + half * 32, w);
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(p_full(m, half));
@@ -659,96 +734,140 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         ++n;
         ++tiles;
       }
-      const float sum = sum2.x + sum2.y;
-      if (lost || !mbar_wait(o_full(m), blocks & 1)) {
+      float sum = sum2.x + sum2.y;
+      if (lost || !mbar_wait(o_full(m), blocks & 1) || ((PAIR || p.splits > 1) && !mbar_wait(o_full(m ^ 1), blocks & 1))) {
         lost = true;
         break;
       }
+      if (lane == 0) mbar_arrive(o_seen(m));
       ++blocks;
       tc_fence_after();
-      const float inv = sum > 0.f ? 1.f / sum : (n == 0 || top == NEG_INF ? 0.f : 1.f / sum);
-      bool nan = false;
-      // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
-      // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
-      // lines each (4500 cycles a block against 1500).
+      // The row's output is w0 O_0 + w1 O_1 (the accumulators of both warpgroups, who
+      // tell each other their sums) for a pair, which shares the columns between the
+      // warpgroups, and O_m / sum otherwise.  A warpgroup that saw no key of a row
+      // has sum 0, and what its accumulator holds does not count.
       const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
-      auto leave = [&](const uint32_t (&w)[32], uint16_t* dst) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[4 * x]),
-                       "r"(w[4 * x + 1]), "r"(w[4 * x + 2]), "r"(w[4 * x + 3])
-                       : "memory");
-        __syncwarp();
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int row = 4 * x + (lane >> 3), rt = (warp & 3) * 32 + row, tok = m * per_tile + (rt >> shift_g);
-          uint4 v;
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                       : "r"(stage + swz128(row, lane & 7)));
-          if (tok < blk.ntok)
-            *reinterpret_cast<uint4*>(dst + (rt >> shift_g) * tok_stride + (rt & (p.G - 1)) * D) = v;
+      float w0 = sum > 0.f || sum != sum ? 1.f / sum : 0.f, w1 = 0.f;
+      float lse = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+      if constexpr (PAIR) {
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
+        meet();
+        float top1, sum1;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(top1), "=f"(sum1) : "r"(sOut + static_cast<uint32_t>(warp ^ 4) * 4096 + lane * 8));
+        meet();  // the staging space is used again below
+        if (lost) break;
+        if (m == 1) {  // in the same order on both sides
+          const float t = top, u = sum;
+          top = top1;
+          sum = sum1;
+          top1 = t;
+          sum1 = u;
         }
-        __syncwarp();
+        const float both = fmaxf(top, top1), shift = both == NEG_INF ? 0.f : both;
+        const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
+        const float all = a * sum + b * sum1;
+        lse = all > 0.f ? both + log2f(all) : (all == 0.f ? NEG_INF : all);
+        const float inv = all > 0.f || all != all ? 1.f / all : 0.f;
+        w0 = a * inv;
+        w1 = b * inv;
+      }
+      // 64 columns at a time: c0 is the first
+      float2 probe = make_float2(0.f, 0.f);  // becomes NaN with any output that is NaN or infinite
+      auto load = [&](int c0, uint32_t (&o)[64]) {
+        const uint32_t src = t_out(tmem, mq);
+        uint32_t x[32], y[32];
+        tmem_ld32(src + lanes + c0, x);
+        tmem_ld32(src + lanes + c0 + 32, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const uint32_t v = i < 32 ? x[i] : y[i - 32];
+          o[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(v) * w0);
+        }
+        if constexpr (PAIR) {
+          tmem_ld32(t_out(tmem, 1) + lanes + c0, x);
+          tmem_ld32(t_out(tmem, 1) + lanes + c0 + 32, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            const uint32_t v = i < 32 ? x[i] : y[i - 32];
+            o[i] = w1 == 0.f ? o[i] : __float_as_uint(fmaf(__uint_as_float(v), w1, __uint_as_float(o[i])));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 2)
+          probe = ffma2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), make_float2(0.f, 0.f), probe);
       };
+      const int c_begin = PAIR ? 64 * m : 0, c_end = PAIR ? min(D, 64 * m + 64) : D;
+      const int part_row = mq * kRows + r;
       if (p.splits > 1) {
-        // the other row tile's products may still read what the partial results overwrite
-        if (!mbar_wait(o_full(m ^ 1), 0)) {
-          lost = true;
-          break;
-        }
+        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+          uint32_t o[64];
+          load(c0, o);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32(t_out(m) + lanes + c * 32, o);
-            tmem_wait_ld();
-          }
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const float v = n > 0 ? __uint_as_float(o[x]) * inv : 0.f;
-            nan |= !(v == v);
-            o[x] = __float_as_uint(v);
-          }
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPart + part_off<D>(tid, c * 8 + x)), "r"(o[4 * x]),
-                         "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+          for (int x = 0; x < 16; ++x)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPart + part_off<D>(part_row, c0 / 4 + x)),
+                         "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
                          : "memory");
         }
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + tid * 4),
-                     "f"(sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum))
-                     : "memory");
-        __syncwarp();
+        if (!PAIR || m == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + part_row * 4), "f"(lse) : "memory");
       } else {
+        // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
+        // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
+        // lines each.
+        uint16_t* dst = p.out + (blk.first + mq * per_tile) * tok_stride + static_cast<long long>(blk.h) * p.G * D + (lane & 7) * 8;
+        const int row0 = (warp & 3) * 32 + (lane >> 3);  // this lane's rows: row0 + 4 x
+        dst += (row0 >> shift_g) * tok_stride + (row0 & (p.G - 1)) * D;
+        const int left = ((blk.ntok - mq * per_tile) << shift_g) - row0;
+        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+          uint32_t o[64];
+          load(c0, o);
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t w[32];
+          for (int x = 0; x < 8; ++x) {
+            uint32_t w[4];
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t o[32];
-            tmem_ld32(t_out(m) + lanes + c * 64 + half * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float v0 = __uint_as_float(o[2 * x]) * inv, v1 = __uint_as_float(o[2 * x + 1]) * inv;
-              nan |= !(v0 == v0) || !(v1 == v1);
-              w[half * 16 + x] = E::pack2(v0, v1);
-            }
+            for (int y = 0; y < 4; ++y)
+              w[y] = E::pack2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
-          leave(w, p.out + (blk.first + m * per_tile) * tok_stride + static_cast<long long>(blk.h) * p.G * D + c * 64 + (lane & 7) * 8);
+          __syncwarp();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            uint4 v;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(stage + swz128(4 * x + (lane >> 3), lane & 7)));
+            // (row0 has no bits that 4 x has: the two offsets add up)
+            if (4 * x < left)
+              *reinterpret_cast<uint4*>(dst + ((4 * x) >> shift_g) * tok_stride + ((4 * x) & (p.G - 1)) * D + c0) = v;
+          }
+          __syncwarp();
         }
       }
-      // rows that ended with a NaN, once more over what they see alone
-      const uint32_t again = __ballot_sync(0xffffffffu, nan && valid);
-      if (again) attend_alone<E, D>(p, blk, m, again, sPart, sLse);
+      // Rows that ended with a NaN (or an infinity), once more over what they see alone.
+      const float probed = probe.x + probe.y;
+      uint32_t again = __ballot_sync(0xffffffffu, probed != probed && token < blk.ntok);
+      if constexpr (PAIR) {
+        // warpgroup 0 takes them for both halves of the columns, once both have read
+        // the accumulators and written what they have
+        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage), "r"(again) : "memory");
+        meet();
+        uint32_t other;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(other) : "r"(sOut + static_cast<uint32_t>(warp ^ 4) * 4096));
+        again = m == 0 ? again | other : 0u;
+        meet();
+        if (lost) break;
+      }
+      if (again) attend_alone<E, D>(p, blk, mq, again, sPart, sLse);
       release_unit(nu);
     }
     if (lost) give_up();
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == kProductWarp) tmem_free(tmem, kTmem);
+  if (warp == kProductWarp) tmem_free(s_tmem, kTmem);
   if (p.splits == 1) return;
 
   // ======================= the cluster's partial results ============================
@@ -809,11 +928,11 @@ cudaLaunchConfig_t config(const PromptParams& p, cudaLaunchAttribute* attr) {
 }
 
 // Attributes of one variant, and how many of its clusters of 2^x CTAs run at a time.
-template <typename E, int D>
+template <typename E, int D, bool PAIR>
 cudaError_t prepare_t(int (&clusters)[5]) {
-  cudaError_t e = cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem<D>);
+  cudaError_t e = cudaFuncSetAttribute(window_prompt_kernel<E, D, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPromptSmem<D>);
   if (e != cudaSuccess) return e;
-  if (cudaFuncSetAttribute(window_prompt_kernel<E, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+  if (cudaFuncSetAttribute(window_prompt_kernel<E, D, PAIR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
     cudaGetLastError();
   for (int x = 1; x <= 4; ++x) {
     PromptParams p{};
@@ -821,7 +940,7 @@ cudaError_t prepare_t(int (&clusters)[5]) {
     cudaLaunchAttribute attr{};
     const cudaLaunchConfig_t cfg = config<E, D>(p, &attr);
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, window_prompt_kernel<E, D>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, window_prompt_kernel<E, D, PAIR>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
     }
@@ -834,17 +953,25 @@ cudaError_t prepare_t(int (&clusters)[5]) {
 
 cudaError_t prepare_window_prompt(int (&clusters)[5]) {
   for (int& c : clusters) c = 1 << 20;
-  cudaError_t e = prepare_t<ElemBf16, 64>(clusters);
-  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128>(clusters);
-  if (e == cudaSuccess) e = prepare_t<ElemF16, 64>(clusters);
-  if (e == cudaSuccess) e = prepare_t<ElemF16, 128>(clusters);
+  cudaError_t e = prepare_t<ElemBf16, 64, false>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 64, true>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, false>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, true>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 64, false>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 64, true>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 128, false>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemF16, 128, true>(clusters);
   return e;
 }
 
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream) {
-  return launch_dependent(p.D == 128 ? (p.f16 ? window_prompt_kernel<ElemF16, 128> : window_prompt_kernel<ElemBf16, 128>)
-                                     : (p.f16 ? window_prompt_kernel<ElemF16, 64> : window_prompt_kernel<ElemBf16, 64>),
-                          p, dim3(p.ctas), kThreads, p.D == 128 ? kPromptSmem<128> : kPromptSmem<64>, stream, p.splits);
+  using Kernel = void (*)(PromptParams);
+  const Kernel kernels[8] = {window_prompt_kernel<ElemBf16, 64, false>,  window_prompt_kernel<ElemBf16, 64, true>,
+                             window_prompt_kernel<ElemF16, 64, false>,   window_prompt_kernel<ElemF16, 64, true>,
+                             window_prompt_kernel<ElemBf16, 128, false>, window_prompt_kernel<ElemBf16, 128, true>,
+                             window_prompt_kernel<ElemF16, 128, false>,  window_prompt_kernel<ElemF16, 128, true>};
+  return launch_dependent(kernels[(p.D == 128 ? 4 : 0) + (p.f16 ? 2 : 0) + (p.pair ? 1 : 0)], p, dim3(p.ctas), kThreads,
+                          p.D == 128 ? kPromptSmem<128> : kPromptSmem<64>, stream, p.splits);
 }
 
 }  // namespace vh

@@ -159,6 +159,14 @@ def test_prompt_splits(splits):
     check_prompt(R.make([333, 40], [1, 40], Hq=8, Hkv=1, D=64, dtype=FP, sinks=0, active=[1, 0], seed=splits), splits=splits, extra=2)
 
 
+@pytest.mark.parametrize("heads", [(8, 1), (2, 2), (8, 8)])
+def test_prompt_large_blocks(heads):
+    # more blocks than SMs: blocks of 256 (token, head) rows, drawn one after the other
+    T = 152 * 128 // heads[0] + 700
+    r = R.make([T // 2 + 3, T // 2, 5], [T // 2 + 3, T // 2 - 9, 5], *heads, D=64, window=70, sinks=3, dtype=FP, seed=heads[0])
+    check_prompt(r, extra=1)
+
+
 def test_prompt_many_rows():
     # more requests than one a lane of the drawing warp
     lens = [1 + (37 * b) % 150 for b in range(70)]
