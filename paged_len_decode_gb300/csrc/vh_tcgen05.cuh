@@ -23,9 +23,14 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Arrival on `bar` once every product this thread has issued is complete.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Arrival on `bar` once every product this thread has issued is complete (by
+// the lane whose `leader` is set; see tc_mma).
+__device__ __forceinline__ void tc_commit(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %0, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%1];\n\t}" ::"r"(leader),
+      "r"(bar)
+      : "memory");
 }
 
 // 32 columns of the warp's 32 lanes: lane l of the warp holds row l.
@@ -87,20 +92,25 @@ __host__ __device__ constexpr uint32_t tc_kind_f16(int M, int N, bool bf16, bool
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// d (+)= a b, one k-step of 16; issued by one thread.
-__device__ __forceinline__ void tc_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
+// d (+)= a b, one k-step of 16; issued by the one lane whose `leader` is set.  The
+// whole warp calls it, without a branch: descriptors then stay in uniform
+// registers, where a branch to one lane makes the compiler move each of them
+// there from that lane's registers, product by product.
+__device__ __forceinline__ void tc_mma(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 q, %6, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh), "r"(leader)
       : "memory");
 }
 // the same with a in tensor memory
-__device__ __forceinline__ void tc_mma_ta(uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
+__device__ __forceinline__ void tc_mma_ta(uint32_t leader, uint32_t d, uint32_t a, uint32_t b, uint32_t kind, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %4, 0;\n\tmov.b64 y, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 q, %6, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "mov.b64 y, {%2, %5};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kind), "r"(static_cast<uint32_t>(add)), "n"(kOperandHigh), "r"(leader)
       : "memory");
 }
 

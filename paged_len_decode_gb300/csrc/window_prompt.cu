@@ -58,11 +58,6 @@ constexpr int kSlots = 2;        // blocks drawn: this one and the next
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
-template <int M>
-struct Place {
-  static constexpr int value = M;
-};
-
 // One CTA's work: queries of one request and kv head, and a share of their key tiles.
 struct Unit {
   int row, first, ntok;         // request, first token, tokens
@@ -447,9 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
     } else if (warp == kProductWarp) {
       // ======================= products =============================================
       // The tensor cores wait whenever this warp does more between two products
-      // than they have queued, so all that a tile needs is known before: its
-      // place in the ring, and which row tiles see it.
-      const uint32_t tmem = s_tmem;
+      // than they have queued.  So all that a tile needs is known before, and the
+      // warp stays together: a wait that ran out is noted and acted on once a tile
+      // (what is multiplied until then is garbage in this CTA's own memory).
+      const uint32_t issue = leader ? 1u : 0u;
+      const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
       uint32_t ki = 0, kp = 0, vi = 1, vp = 0;  // ring place and phase of the next K and V
       auto next = [&](uint32_t& i, uint32_t& ph) {
         i += 2;
@@ -459,13 +456,25 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         }
       };
       int nq = 0;
-      uint32_t weights[2] = {0, 0};  // phases of the weights' barriers
+      uint32_t weights0 = 0, weights1 = 0;  // phases of the weights' barriers
+      bool ran_out = false;
+      auto wait = [&](uint32_t bar, uint32_t parity) { ran_out |= !mbar_wait(bar, parity); };
       bool lost = false;
       const uint32_t k_operand = tc_operand(sKV, 16), v_operand = tc_operand(sKV, kBlockBytes);
-      for (int n = 0; !lost && next_unit(n, lost); ++n) {
-        const Unit blk = s_units[n % kSlots];
+      for (int n = 0;; ++n) {
+        wait(u_full(n % kSlots), (n / kSlots) & 1);
+        lost = __any_sync(0xffffffffu, ran_out);
+        auto field = [&](const int& x) { return __shfl_sync(0xffffffffu, x, 0); };  // (uniform, and known to be)
+        const Unit& from = s_units[n % kSlots];
+        if (lost || field(from.more) == 0) break;
+        Unit blk;
+        blk.slot = field(from.slot);
+        blk.ntok = field(from.ntok);
+        blk.sink_tiles = field(from.sink_tiles);
+        blk.from = field(from.from);
+        blk.count = field(from.count);
+        const int k0 = field(from.k0), k1 = field(from.k1);
         release_unit(n);
-        const int k0 = blk.k0, k1 = blk.k1;
         if (k0 == k1) continue;
         const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
         const int qb = nq % QB;
@@ -481,22 +490,20 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
         const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
         auto scores = [&](int m) {
-          if (leader) {
-            const uint32_t qa = q_operand + (PAIR ? 0 : m) * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
+          const uint32_t qa = q_operand + (PAIR ? 0 : m) * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-              const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
-              tc_mma(t_scores(tmem, m), qa + off, kb + off, kScores, s > 0);
-            }
-            tc_commit(s_full(m));
+          for (int s = 0; s < KS; ++s) {
+            const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
+            tc_mma(issue, tmem + m * kKeys, qa + off, kb + off, kScores, s > 0);
           }
+          tc_commit(issue, s_full(m));
         };
-        bool add[2] = {false, false};
+        bool add0 = false, add1 = false;
         // the block's last products of row tile m are issued; its softmax has seen the end
         // of the block before (else it could miss this one)
         auto finish = [&](int m) {
-          lost = lost || (nq > 1 && !mbar_wait(o_seen(m), (nq - 2) & 1));
-          if (leader && !lost) tc_commit(o_full(m));
+          if (nq > 1) wait(o_seen(m), (nq - 2) & 1);
+          tc_commit(issue, o_full(m));
         };
         // values of key tile k: slots that nobody sees may hold anything where an end of
         // what the block sees lies inside the tile, so they become zeros
@@ -517,101 +524,84 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           __syncwarp();
         };
         // the weights arrive in two halves of 64 keys
-        auto values = [&](auto place) {
-          constexpr int m = decltype(place)::value;  // (a constant, so that nothing is indexed at run time)
-          const uint32_t va = v_operand + vi * (kStage >> 4);
+        auto values = [&](int m, uint32_t& weights, bool& add) {
+          const uint32_t va = v_operand + vi * (kStage >> 4), scores_at = tmem + m * kKeys, out_at = tmem + 2 * kKeys + m * D;
+          wait(p_full(m, 0), weights);
+          tc_fence_after();
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            lost = lost || !mbar_wait(p_full(m, half), weights[m]);
-            tc_fence_after();
-            if (leader && !lost) {
+          for (int s = 0; s < 4; ++s)
+            tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, add || s > 0);
+          wait(p_full(m, 1), weights);
+          tc_fence_after();
 #pragma unroll
-              for (int s = 4 * half; s < 4 * half + 4; ++s)
-                tc_mma_ta(t_out(tmem, m), t_scores(tmem, m) + s * 8, va + s * (2048 >> 4), kValues, add[m] || s > 0);
-            }
-          }
-          weights[m] ^= 1u;
-          add[m] = true;
+          for (int s = 4; s < 8; ++s) tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, true);
+          weights ^= 1u;
+          add = true;
         };
-        if (!mbar_wait(q_full(qb), (nq / QB) & 1) || !mbar_wait(full(ki), kp)) {
-          lost = true;
-          break;
-        }
+        wait(q_full(qb), (nq / QB) & 1);
+        wait(full(ki), kp);
         ++nq;
         tc_fence_after();
         if constexpr (PAIR) {
           scores(0);
-          if (leader) tc_commit(empty(ki));
+          tc_commit(issue, empty(ki));
           next(ki, kp);
           if (k0 + 1 < k1) {
-            lost = !mbar_wait(full(ki), kp);
-            if (lost) break;
+            wait(full(ki), kp);
             scores(1);
-            if (leader) tc_commit(empty(ki));
+            tc_commit(issue, empty(ki));
             next(ki, kp);
           }
-          if (leader && k0 + 2 >= k1) tc_commit(q_empty(qb));
+          if (k0 + 2 >= k1) tc_commit(issue, q_empty(qb));
           // key tile k by row tile place m: its values, then the scores of the tile after next
-          auto step = [&](auto place, int k) {
-            constexpr int m = decltype(place)::value;
-            lost = !mbar_wait(full(vi), vp);
-            if (lost) return;
+          auto step = [&](int m, int k, uint32_t& weights, bool& add) {
+            wait(full(vi), vp);
             clean(k);
-            values(place);
-            if (lost) return;
-            if (leader) tc_commit(empty(vi));
+            values(m, weights, add);
+            tc_commit(issue, empty(vi));
             next(vi, vp);
-            if (k + 2 >= k1) return;
-            lost = !mbar_wait(full(ki), kp);
-            if (lost) return;
-            scores(m);
-            if (leader) {
-              tc_commit(empty(ki));
-              if (k + 3 == k1) tc_commit(q_empty(qb));
+            if (k + 2 < k1) {
+              wait(full(ki), kp);
+              scores(m);
+              tc_commit(issue, empty(ki));
+              if (k + 3 == k1) tc_commit(issue, q_empty(qb));
+              next(ki, kp);
             }
-            next(ki, kp);
           };
-          for (int k = k0; k < k1 && !lost; k += 2) {
-            step(Place<0>{}, k);
-            if (!lost && k + 1 < k1) step(Place<1>{}, k + 1);
+          for (int k = k0; k < k1; k += 2) {
+            step(0, k, weights0, add0);
+            if (k + 1 < k1) step(1, k + 1, weights1, add1);
+            if (__any_sync(0xffffffffu, ran_out)) break;
           }
           finish(0);
           finish(1);
         } else {
-          bool see[2] = {sees_k(0, k0), sees_k(1, k0)};
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            if (see[m]) scores(m);
-          if (leader) {
-            tc_commit(empty(ki));
-            if (k0 + 1 == k1) tc_commit(q_empty(qb));
-          }
+          bool see0 = sees_k(0, k0), see1 = sees_k(1, k0);
+          if (see0) scores(0);
+          if (see1) scores(1);
+          tc_commit(issue, empty(ki));
+          if (k0 + 1 == k1) tc_commit(issue, q_empty(qb));
           next(ki, kp);
           for (int k = k0; k < k1; ++k) {
             const bool more = k + 1 < k1;
-            const bool see_next[2] = {more && sees_k(0, k + 1), more && sees_k(1, k + 1)};
-            if (!mbar_wait(full(vi), vp)) {
-              lost = true;
-              break;
-            }
+            const bool next0 = more && sees_k(0, k + 1), next1 = more && sees_k(1, k + 1);
+            wait(full(vi), vp);
             clean(k);
-            if (see[0]) values(Place<0>{});
-            if (more) lost = lost || !mbar_wait(full(ki), kp);
-            if (see_next[0] && !lost) scores(0);
+            if (see0) values(0, weights0, add0);
+            if (more) wait(full(ki), kp);
+            if (next0) scores(0);
             if (!more) finish(0);
-            if (see[1]) values(Place<1>{});
-            if (see_next[1] && !lost) scores(1);
+            if (see1) values(1, weights1, add1);
+            if (next1) scores(1);
             if (!more) finish(1);
-            if (lost) break;
-            if (leader) {
-              tc_commit(empty(vi));
-              if (more) tc_commit(empty(ki));
-              if (k + 2 == k1) tc_commit(q_empty(qb));  // the block's last scores are issued
-            }
+            tc_commit(issue, empty(vi));
+            if (more) tc_commit(issue, empty(ki));
+            if (k + 2 == k1) tc_commit(issue, q_empty(qb));  // the block's last scores are issued
             next(vi, vp);
             if (more) next(ki, kp);
-            see[0] = see_next[0];
-            see[1] = see_next[1];
+            see0 = next0;
+            see1 = next1;
+            if (__any_sync(0xffffffffu, ran_out)) break;
           }
         }
       }
@@ -619,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         give_up();
         // products in flight end before the tensor memory is freed (row tile 0's output
         // barrier serves for that; its softmax has given up or will)
-        if (leader) tc_commit(o_full(0));
+        tc_commit(issue, o_full(0));
         for (int x = 0; x < 2; ++x) (void)mbar_wait(o_full(0), x);
       }
     }
