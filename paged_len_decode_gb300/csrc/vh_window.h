@@ -63,7 +63,7 @@ struct WindowDecodeParams {
   int f16;
   int early;                   // VH_FLAG_PDL: lengths, flags and page ids are read before the dependency wait
   int B, Hq, Hkv, D, G, P;
-  int Hc, groups, N, stages, min_tiles;
+  int Hc, groups, N, stages;
   int stage_bytes;             // K then V of one tile: [D/64][Hc][16 tokens][128 B swizzled] each
   int q_off, cum_off, len_off, bar_off, smem_bytes;
 };

@@ -334,7 +334,6 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   int auto_n = 0;
   if (!plan_decode(p, *dev, &auto_n)) return VH_EINVAL;
   p.N = num_ctas > 0 ? num_ctas : auto_n;
-  p.min_tiles = 1;
   const vh::WsLayout w = vh::ws_layout(B, Hq, Hkv, D, p.N);
   if (workspace_bytes < w.total) return VH_EWORKSPACE;
   // the tensor maps are those of the other attention calls

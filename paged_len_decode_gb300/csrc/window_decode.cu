@@ -35,7 +35,7 @@ namespace {
 constexpr int kMaxHeads = 8;                 // kv heads (consumer warps) of a CTA
 constexpr int kThreadsMax = 32 * (kMaxHeads + 1);
 constexpr int kWarpRows = 128;               // rows that the producer warp sums up alone
-enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscPart = 34, kMiscInts = 48 };  // part: 4 ints each
+enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscMost = 34, kMiscPart = 36, kMiscInts = 48 };  // part: 4 ints each
 
 __device__ __forceinline__ int share_begin(int c, int n, int total) {
   return c * (total / n) + min(c, total % n);
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
     if (lane == 0) {
       *abort_flag = 0;
       misc[kMiscLost] = 0;
+      misc[kMiscMost] = 0;
       for (int s = 0; s < S; ++s) {
         mbar_init(full0 + 8 * s, 1);
         mbar_init(empty0 + 8 * s, Hc);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
       fence_barrier_init();
       cum[0] = 0;
     }
+    __syncwarp();
     if (p.B <= kWarpRows) {
       int n[kWarpRows / 32], run = 0;
 #pragma unroll
@@ -165,6 +167,11 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         if (x * 32 + lane < p.B) cum[1 + x * 32 + lane] = v;
         run = __shfl_sync(0xffffffffu, v, 31);
       }
+      int most = 0;
+#pragma unroll
+      for (int x = 0; x < kWarpRows / 32; ++x) most = max(most, n[x]);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) misc[kMiscMost] = most;
       __syncwarp();
       asm volatile("bar.arrive 2, %0;" ::"r"(static_cast<int>(blockDim.x)) : "memory");
     }
@@ -172,12 +179,24 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
     named_sync(2, blockDim.x);
   }
   if (p.B > kWarpRows) {
-    for (int b = tid; b < p.B; b += blockDim.x) cum[1 + b] = count_row(b);
+    __syncthreads();
+    int most = 0;
+    for (int b = tid; b < p.B; b += blockDim.x) {
+      const int n = count_row(b);
+      cum[1 + b] = n;
+      most = max(most, n);
+    }
+    atomicMax(misc + kMiscMost, most);
     __syncthreads();
     scan_rows(cum, p.B, misc + kMiscTot);
   }
   const int T = cum[p.B];
-  const int n_eff = min(p.N, (T + p.min_tiles - 1) / p.min_tiles);  // 0 if there is no work
+  // A CTA takes at least q tiles: its share streams in about 0.5 us a tile, and the
+  // longest row's pieces, R / q of them, are then added at about G / 40 us each, so
+  // q = sqrt(R G / 20) is the least of both.  (One row of 8000 tokens, 8 q heads of
+  // one kv head: 179 us with q = 1 and 152 or more pieces, 23 us with q = 14.)
+  const int q = max(1, static_cast<int>(sqrtf(static_cast<float>(misc[kMiscMost]) * (0.05f * G)) + 0.5f));
+  const int n_eff = min(p.N, (T + q - 1) / q);  // 0 if there is no work
   const bool works = c < n_eff;
   const int t0 = works ? share_begin(c, n_eff, T) : 0, t1 = works ? share_begin(c + 1, n_eff, T) : 0;
   const int b0 = works ? row_of(cum, 0, p.B, t0) : 0;
@@ -552,7 +571,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[n][i] *= sc;
       }
-      constexpr int U = G >= 8 ? 1 : (G == 4 ? 2 : 4);  // pieces loaded at a time
+      constexpr int U = 16 / G;  // pieces loaded at a time: 16 loads in flight
       for (int j = 0; j < nj; j += U) {
         float x[U][G][PER];
 #pragma unroll
