@@ -147,6 +147,15 @@ bool plan_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev, int* auto_n) 
   return true;
 }
 
+// CTAs that the kernel can use at most: with every row as long as the window, the
+// sinks and its pages allow, it takes this many (see the kernel's rule for q).
+int useful_ctas(const vh::WindowDecodeParams& p, int max_pages_per_seq) {
+  const long long all = (static_cast<long long>(max_pages_per_seq) * p.P + 15) / 16;
+  const long long row = std::min(all, (p.sinks + 15LL) / 16 + (p.window + 15LL) / 16 + 1);
+  const long long q = std::max(1L, static_cast<long>(std::sqrt(static_cast<float>(row) * (0.05f * p.G)) + 0.5f) - 1);
+  return static_cast<int>(std::min<long long>(65535, (p.B * row + q - 1) / q));
+}
+
 // Scalars that every call of this file checks alike.
 bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int64_t token_stride, int64_t head_stride,
                  int num_pages, const int32_t* page_table, int max_pages_per_seq) {
@@ -333,7 +342,9 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   p.P = page_size;
   int auto_n = 0;
   if (!plan_decode(p, *dev, &auto_n)) return VH_EINVAL;
-  p.N = num_ctas > 0 ? num_ctas : auto_n;
+  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
+  p.sinks = std::min(sinks, vh::kNoWindow);
+  p.N = num_ctas > 0 ? num_ctas : std::min(auto_n, useful_ctas(p, max_pages_per_seq));
   const vh::WsLayout w = vh::ws_layout(B, Hq, Hkv, D, p.N);
   if (workspace_bytes < w.total) return VH_EWORKSPACE;
   // the tensor maps are those of the other attention calls
@@ -361,8 +372,6 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   p.max_pages_per_seq = max_pages_per_seq;
   p.seq_lens = seq_lens;
   p.active = active;
-  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
-  p.sinks = std::min(sinks, vh::kNoWindow);
   p.out = out;
   unsigned char* ws = static_cast<unsigned char*>(workspace);
   p.counters = reinterpret_cast<int*>(ws + w.counters);

@@ -191,15 +191,29 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
     scan_rows(cum, p.B, misc + kMiscTot);
   }
   const int T = cum[p.B];
-  // A CTA takes at least q tiles: its share streams in about 0.5 us a tile, and the
-  // longest row's pieces, R / q of them, are then added at about G / 40 us each, so
-  // q = sqrt(R G / 20) is the least of both.  (One row of 8000 tokens, 8 q heads of
-  // one kv head: 179 us with q = 1 and 152 or more pieces, 23 us with q = 14.)
-  const int q = max(1, static_cast<int>(sqrtf(static_cast<float>(misc[kMiscMost]) * (0.05f * G)) + 0.5f));
-  const int n_eff = min(p.N, (T + q - 1) / q);  // 0 if there is no work
-  const bool works = c < n_eff;
-  const int t0 = works ? share_begin(c, n_eff, T) : 0, t1 = works ? share_begin(c + 1, n_eff, T) : 0;
-  const int b0 = works ? row_of(cum, 0, p.B, t0) : 0;
+  // Shares: either T / n tiles each, of which a CTA takes at least q (a share streams
+  // in about 0.5 us a tile, and the longest row's pieces, R / q of them, are then added
+  // at about G / 40 us each, so q = sqrt(R G / 20) is the least of both; one row of 8000
+  // tokens, 8 q heads of one kv head: 179 us with q = 1, 23 us with q = 14), or whole
+  // rows, which need no merge: that takes 2.5 us (4.8 us against 7.3 for a few rows of
+  // a tile or two), as long as 6 tiles.
+  const int most = misc[kMiscMost];
+  const int q = max(1, static_cast<int>(sqrtf(static_cast<float>(most) * (0.05f * G)) + 0.5f));
+  const int rows_each = (p.B + p.N - 1) / p.N;
+  const bool by_row = most * rows_each <= max(q, T / p.N) + 6;
+  const int n_eff = by_row ? 0 : min(p.N, (T + q - 1) / q);  // CTAs that share the tiles
+  int t0 = 0, t1 = 0, b0 = 0;
+  if (by_row) {
+    b0 = min(c * rows_each, p.B);
+    t0 = cum[b0];
+    t1 = cum[min(b0 + rows_each, p.B)];
+  } else if (c < n_eff) {
+    const int each = T / n_eff, rest = T - each * n_eff;  // the first `rest` CTAs take one tile more
+    t0 = c * each + min(c, rest);
+    t1 = t0 + each + (c < rest ? 1 : 0);
+  }
+  const bool works = t1 > t0;
+  if (works) b0 = row_of(cum, b0, p.B, t0);
   const int tpp = (p.P + kTile - 1) / kTile;  // tiles of a page
   const int tpp_shift = (tpp & (tpp - 1)) == 0 ? __ffs(tpp) - 1 : -1;
 
