@@ -67,7 +67,7 @@ bool layout_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev) {
     p.groups = p.Hkv / hc;
     p.stage_bytes = 2 * 16 * hc * p.D * 2;
     const size_t rows = align_up(4 * (static_cast<size_t>(p.B) + 1), 16) + align_up(4 * static_cast<size_t>(p.B), 16);
-    const size_t fixed = 1024 + static_cast<size_t>(hc) * p.G * p.D * 4 + rows + 8 * (2 * kMaxStages + 2) + 48 * 4 + 128;
+    const size_t fixed = 1024 + static_cast<size_t>(hc) * p.G * p.D * 4 + rows + 8 * (2 * kMaxStages + 2 + kMaxHc) + 48 * 4 + 128;
     const size_t budget = static_cast<size_t>(dev.smem_optin);
     if (fixed + 2 * static_cast<size_t>(p.stage_bytes) > budget) continue;
     p.stages = static_cast<int>(std::min<size_t>((budget - fixed) / p.stage_bytes,
@@ -80,7 +80,7 @@ bool layout_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev) {
     p.len_off = static_cast<int>(off);
     off += align_up(4 * static_cast<size_t>(p.B), 16);
     p.bar_off = static_cast<int>(off);
-    off += 8 * (2 * static_cast<size_t>(p.stages) + 2) + 48 * 4;
+    off += 8 * (2 * static_cast<size_t>(p.stages) + 2 + kMaxHc) + 48 * 4;
     p.smem_bytes = static_cast<int>(align_up(off, 128) + 1024);  // + up to 1024 to align the base
     return true;
   }

@@ -114,10 +114,11 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   int* cum = reinterpret_cast<int*>(smem + p.cum_off);
   int* lens = reinterpret_cast<int*>(smem + p.len_off);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.bar_off);
-  int* misc = reinterpret_cast<int*>(bars + 2 * S + 2);
+  int* misc = reinterpret_cast<int*>(bars + 2 * S + 2 + kMaxHeads);
   volatile int* abort_flag = misc + kMiscAbort;
   const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + S);
   const uint32_t qfull = smem_addr(bars + 2 * S), qempty = smem_addr(bars + 2 * S + 1);
+  const uint32_t merged0 = smem_addr(bars + 2 * S + 2);  // pieces have come, by consumer warp
   const int max_len = p.max_pages_per_seq * p.P;
   const bool p8 = p.P == 8;
   const float NEG_INF = __int_as_float(0xff800000);
@@ -146,6 +147,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
       }
       mbar_init(qfull, 1);
       mbar_init(qempty, Hc);
+      for (int x = 0; x < Hc; ++x) mbar_init(merged0 + 8 * x, 1);
       fence_barrier_init();
       cum[0] = 0;
     }
@@ -548,6 +550,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
   named_sync(1, 32 * Hc);
 
   // ---- the last CTA of a row adds its pieces: warp w those of kv head w -------------
+  uint32_t merges = 0;
   for (int k = 0; k < npart; ++k) {
     const int* v = misc + kMiscPart + 4 * k;
     if (!v[0]) continue;
@@ -563,10 +566,10 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
 #pragma unroll
       for (int i = 0; i < PER; ++i) o[n][i] = 0.f;
     }
-    for (int j0 = 0; j0 < np; j0 += 32) {
-      // 32 pieces a round: lane j has piece j0 + j's weight for every head
-      const int nj = min(32, np - j0);
-      float wt[G];
+    // Weights of the pieces j0 .. j0 + nj - 1, lane j that of piece j0 + j, and the
+    // sums so far in the new maximum's terms.
+    float wt[G];
+    auto weigh = [&](int j0, int nj) {
 #pragma unroll
       for (int n = 0; n < G; ++n) {
         const float lse = lane < nj ? __ldcg(p.part_lse + piece(j0 + lane) + n) : NEG_INF;
@@ -585,36 +588,83 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
 #pragma unroll
         for (int i = 0; i < PER; ++i) o[n][i] *= sc;
       }
-      constexpr int U = 16 / G;  // pieces loaded at a time: 16 loads in flight
-      for (int j = 0; j < nj; j += U) {
-        float x[U][G][PER];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
+    };
+    constexpr int PIECE = G * D * 4;
+    const uint32_t share = static_cast<uint32_t>(S * p.stage_bytes / Hc) & ~127u;
+    const int each = min(32, static_cast<int>(share / PIECE));
+    if (each * G >= 64) {
+      // One or two heads a CTA: the warp's share of the stages (all tiles have been
+      // consumed) holds many pieces, so they come by bulk copies, one trip to memory for
+      // up to 32 of them (12 rows of 6000 tokens, 4 q heads of one kv head: 27 -> 22 us;
+      // with 4 kv heads a CTA it would be 4 or 8, and 24 -> 29 us for G = 8).
+      const uint32_t room = smem_addr(smem) + static_cast<uint32_t>(w) * share;
+      for (int j0 = 0; j0 < np; j0 += each) {
+        const int nj = min(each, np - j0);
+        // what was read and written there by loads and stores comes before the copies, and
+        // what other CTAs wrote (seen by the counter's acquire) too
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(merged0 + 8 * w, static_cast<uint32_t>(nj * PIECE));
+        __syncwarp();
+        if (lane < nj) bulk_g2s(room + lane * PIECE, p.part_o + piece(j0 + lane) * D, PIECE, merged0 + 8 * w);
+        weigh(j0, nj);
+        const bool came = mbar_wait(merged0 + 8 * w, merges & 1u) || mbar_wait(merged0 + 8 * w, merges & 1u);
+        ++merges;
+        if (!came) {
+          if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
+          return;
+        }
+        for (int j = 0; j < nj; ++j) {
+          const uint32_t at = room + static_cast<uint32_t>(j * PIECE + lane * PER * 4);
 #pragma unroll
           for (int n = 0; n < G; ++n) {
-            const float* src = p.part_o + (piece(j0 + min(j + u, nj - 1)) + n) * D + lane * PER;
-            if constexpr (PER == 4) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-              x[u][n][0] = f.x;
-              x[u][n][1] = f.y;
-              x[u][n][2] = f.z;
-              x[u][n][3] = f.w;
-            } else {
-              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-              x[u][n][0] = f.x;
-              x[u][n][1] = f.y;
+            const float f = __shfl_sync(0xffffffffu, wt[n], j);
+#pragma unroll
+            for (int i = 0; i < PER; i += 2) {
+              float2 x;
+              asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x.x), "=f"(x.y) : "r"(at + n * D * 4 + i * 4));
+              o[n][i] += f * x.x;
+              o[n][i + 1] += f * x.y;
             }
           }
+        }
+        __syncwarp();
+      }
+    } else {
+      for (int j0 = 0; j0 < np; j0 += 32) {
+        const int nj = min(32, np - j0);
+        weigh(j0, nj);
+        constexpr int U = 16 / G;  // pieces loaded at a time: 16 loads in flight
+        for (int j = 0; j < nj; j += U) {
+          float x[U][G][PER];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-          for (int n = 0; n < G; ++n) {
-            const float f = __shfl_sync(0xffffffffu, wt[n], min(j + u, 31));
-            if (j + u < nj) {
-#pragma unroll
-              for (int i = 0; i < PER; ++i) o[n][i] += f * x[u][n][i];
+            for (int n = 0; n < G; ++n) {
+              const float* src = p.part_o + (piece(j0 + min(j + u, nj - 1)) + n) * D + lane * PER;
+              if constexpr (PER == 4) {
+                const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
+                x[u][n][0] = f.x;
+                x[u][n][1] = f.y;
+                x[u][n][2] = f.z;
+                x[u][n][3] = f.w;
+              } else {
+                const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
+                x[u][n][0] = f.x;
+                x[u][n][1] = f.y;
+              }
             }
-          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int n = 0; n < G; ++n) {
+              const float f = __shfl_sync(0xffffffffu, wt[n], min(j + u, 31));
+              if (j + u < nj) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) o[n][i] += f * x[u][n][i];
+              }
+            }
+        }
       }
     }
 #pragma unroll
