@@ -231,15 +231,16 @@ bool small_blocks(int T, int B, int G, int Hkv, const DeviceInfo& dev) {
 }
 
 // CTAs that share a block's keys: as many as leave every cluster running at
-// once, and no more than a block can have key tiles.  (16 tokens over 4100 keys,
+// once, and two key tiles each at least.  (16 tokens over 4100 keys,
 // 8 kv heads: 33 us with one CTA a block, 23, 17 and 15 us with 2, 4 and 8, and
-// 27 us with 16, of which half the clusters wait for the others.)
+// 27 us with 16, of which half the clusters wait for the others; over 300 keys 9.5
+// us with one and 10.8 with 2.)
 int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
   const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
                                                 static_cast<long long>(p.window) + p.sinks + (1 << p.shift_block));
   const long long blocks = likely_blocks(p.T, p.B, p.shift_block);
   int x = 0;
-  while (x < 4 && blocks * p.Hkv <= clusters[x + 1] && longest >= (128LL << (x + 1))) ++x;
+  while (x < 4 && blocks * p.Hkv <= clusters[x + 1] && (longest + 127) / 128 >= (2LL << (x + 1))) ++x;
   return 1 << x;
 }
 

@@ -156,6 +156,10 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows,
   }
   r.slot = g.len - (g.end - r.first);
   list_tiles(p, r.slot, r.ntok, r.sink_tiles, r.from, r.count);
+  if (p.splits == 1) {
+    r.k1 = r.count;
+    return r;
+  }
   const int splits = min(p.splits, r.count);
   if (r.z < splits) {
     r.k0 = share_begin(r.z, splits, r.count);
@@ -263,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   __shared__ uint64_t s_bars[2 * ST + 2 * QB + 11 + 2 * kSlots];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_again[8];  // rows of a softmax warp that ended with a NaN (PAIR)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int shift_g = p.shift_g, per_tile = kRows >> shift_g;  // tokens of a row tile
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
@@ -842,13 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       if constexpr (PAIR) {
         // warpgroup 0 takes them for both halves of the columns, once both have read
         // the accumulators and written what they have
-        if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(stage), "r"(again) : "memory");
-        meet();
-        uint32_t other;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(other) : "r"(sOut + static_cast<uint32_t>(warp ^ 4) * 4096));
-        again = m == 0 ? again | other : 0u;
+        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&s_again[warp]) = again;
         meet();
         if (lost) break;
+        again |= *reinterpret_cast<volatile uint32_t*>(&s_again[warp ^ 4]);
+        if (m == 1) again = 0u;
       }
       if (again) attend_alone<E, D>(p, blk, mq, again, sPart, sLse);
       release_unit(nu);
