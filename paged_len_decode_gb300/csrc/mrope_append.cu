@@ -15,10 +15,12 @@
 // cos and sin, gathered pair by pair where neighbouring pairs belong to different
 // axes, stay in its registers for the whole token; loads are 16 bytes, and the
 // first of them and the values are under way before anything is looked up.
-// What counts is bytes in flight: 24 warps an SM with two loads a lane each
-// measured 66 us on 16384 tokens (32 / 8 heads, 403 MB: 6.1 TB/s, 89 % of the
-// copy peak), 16 warps with four 83 us, and a CTA of 4 tokens with its angles in
-// shared memory behind a barrier 82 us.
+// What counts is bytes in flight and the length of the chain of look-ups: 20 warps
+// an SM with three heads' loads a lane each measured 64 us on 16384 tokens (32 / 8
+// heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.3 us on 2413 with the norm;
+// 24 warps with two 63.6 and 10.1 us, 16 warps with four 83, and a CTA of 4 tokens
+// with its angles in shared memory behind a barrier 82 us.  Angles gathered beside
+// the row's look-up instead of after it, and weights by 16 bytes: 12.2 -> 10.1 us.
 #include "vh_ragged.cuh"
 #include "vh_window.h"
 
@@ -31,11 +33,11 @@ constexpr int kThreads = 64;  // (small CTAs: no two warps need each other)
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(kThreads, 12) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
+__global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
   constexpr int HALF = D / 2;
   constexpr int UPH = HALF / 8;  // lanes of a head
   constexpr int HPW = 32 / UPH;  // heads that a warp rotates at a time
-  constexpr int U = 2;           // of those, in flight
+  constexpr int U = 3;           // of those, in flight
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int t = unit / p.warps, part = unit - t * p.warps;
@@ -73,43 +75,51 @@ __global__ void __launch_bounds__(kThreads, 12) mrope_kv_append_kernel(const __g
   const int first = part * HPW + lane / UPH;
   load(first);  // (needs nothing of what is looked up next)
 
-  // ---- the token's row, slot, page and angles --------------------------------
+  // ---- the token's angles, row, slot and page ---------------------------------
+  // Given positions depend on nothing but t, so the angles are gathered while the
+  // row is looked up (a position out of range reads row 0 and is dealt with below).
+  float c[8], s[8];
+  const uint32_t axes = static_cast<uint32_t>(p.axis[i >> 5] >> (2 * (i & 31))) & 0xFFFFu;  // of the lane's pairs
+  auto gather = [&](int pos) {  // pos: lane a's is the position on axis a
+    if (__all_sync(0xffffffffu, axes == (axes & 3u) * 0x5555u)) {
+      const float* row_cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, axes & 3u)) * D + i;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row_cs + k));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row_cs + HALF + k));
+        c[k] = x.x; c[k + 1] = x.y; c[k + 2] = x.z; c[k + 3] = x.w;
+        s[k] = y.x; s[k + 1] = y.y; s[k + 2] = y.z; s[k + 3] = y.w;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float* cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, (axes >> (2 * k)) & 3u)) * D + i + k;
+        c[k] = __ldg(cs);
+        s[k] = __ldg(cs + HALF);
+      }
+    }
+  };
+  auto outside = [&](int pos) { return lane < p.num_axes && (pos < 0 || pos >= p.max_pos); };
+  bool bad = false;
+  if (p.positions) {
+    const int pos = lane < p.num_axes ? __ldg(p.positions + static_cast<long long>(lane) * p.T + t) : 0;
+    bad = outside(pos);  // (every axis is checked, those that no pair takes too)
+    gather(bad ? 0 : pos);
+  }
   RaggedRow r;
   const int row = warp_row_of_token(p.token_start, p.seq_lens, p.active, t, p.B, p.T, p.max_pages_per_seq * p.P, lane,
                                     p.err_flag, lane == 0 && part == 0, r);
   if (row < 0 || !r.ok) return;
   const int slot = r.len - (r.end - t);
-  int pos = slot;
-  bool bad = false;
-  if (lane < p.num_axes) {
-    if (p.positions) pos = __ldg(p.positions + static_cast<long long>(lane) * p.T + t);
-    bad = pos < 0 || pos >= p.max_pos;  // (every axis is checked, those that no pair takes too)
+  if (!p.positions) {
+    bad = outside(slot);
+    gather(slot < p.max_pos ? slot : 0);
   }
   const long long lp = static_cast<long long>(row) * p.max_pages_per_seq + slot / p.P;
   const int page = p.page_table ? __ldg(p.page_table + lp) : static_cast<int>(lp);
   if (__any_sync(0xffffffffu, bad)) {
     if (lane == 0) flag_error(p.err_flag, VH_ERR_POS);
     return;
-  }
-  float c[8], s[8];
-  const uint32_t axes = static_cast<uint32_t>(p.axis[i >> 5] >> (2 * (i & 31))) & 0xFFFFu;  // of the lane's pairs
-  const bool same = axes == (axes & 3u) * 0x5555u;
-  if (__all_sync(0xffffffffu, same)) {
-    const float* row_cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, axes & 3u)) * D + i;
-#pragma unroll
-    for (int k = 0; k < 8; k += 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(row_cs + k));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(row_cs + HALF + k));
-      c[k] = x.x; c[k + 1] = x.y; c[k + 2] = x.z; c[k + 3] = x.w;
-      s[k] = y.x; s[k + 1] = y.y; s[k + 2] = y.z; s[k + 3] = y.w;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float* cs = p.cos_sin + static_cast<long long>(__shfl_sync(0xffffffffu, pos, (axes >> (2 * k)) & 3u)) * D + i + k;
-      c[k] = __ldg(cs);
-      s[k] = __ldg(cs + HALF);
-    }
   }
   const bool page_ok = page >= 0 && page < p.num_pages;
   if (!page_ok && lane == 0) flag_error(p.err_flag, VH_ERR_PAGE);
@@ -159,10 +169,17 @@ __global__ void __launch_bounds__(kThreads, 12) mrope_kv_append_kernel(const __g
         const float* nw = is_q ? p.q_norm_w : p.k_norm_w;
         if (nw) {
           const float rs = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+          // the weights of the lane's two runs of 8 elements
+          float wt[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v4 = __ldg(reinterpret_cast<const float4*>(nw + (k < 2 ? e0 + 4 * k : e1 + 4 * k - 8)));
+            wt[4 * k] = v4.x; wt[4 * k + 1] = v4.y; wt[4 * k + 2] = v4.z; wt[4 * k + 3] = v4.w;
+          }
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            x[k] = __ldg(nw + (ilv ? 2 * (i + k) : i + k)) * (x[k] * rs);
-            y[k] = __ldg(nw + (ilv ? 2 * (i + k) + 1 : HALF + i + k)) * (y[k] * rs);
+            x[k] = (ilv ? wt[2 * k] : wt[k]) * (x[k] * rs);
+            y[k] = (ilv ? wt[2 * k + 1] : wt[8 + k]) * (y[k] * rs);
           }
         }
       }
