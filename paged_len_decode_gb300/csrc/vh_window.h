@@ -82,7 +82,7 @@ struct PromptParams {
   // queries as a 3-D tensor (head_dim, q head, token), boxes of 64 x G x 128/G;
   // K and V as 4-D tensors (see vh_kernels.h), boxes of 64 x `box` tokens x 1 head
   CUtensorMap tmap_q, tmap_k, tmap_v;
-  int tm_tok_dim, box;
+  int tm_tok_dim, box, shift_box;
   const uint16_t* q;           // [T][Hq][D]
   const uint16_t* k_cache;
   const uint16_t* v_cache;

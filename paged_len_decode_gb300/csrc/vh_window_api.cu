@@ -199,6 +199,7 @@ bool encode_prompt_maps(vh::PromptParams& p) {
   if (p.max_pages_per_seq > 1)
     while (p.P % box != 0) box /= 2;
   p.box = box;
+  p.shift_box = __builtin_ctz(box);
   auto dim = [](long long x) { return static_cast<cuuint64_t>(x); };
   {
     const cuuint64_t dims[3] = {dim(p.D), dim(p.Hq), dim(p.T)}, strides[2] = {dim(2LL * p.D), dim(2LL * p.D * p.Hq)};

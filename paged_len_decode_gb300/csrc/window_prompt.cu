@@ -15,10 +15,11 @@
 //    block holds tokens of one request.  Where such blocks would be few or
 //    mostly empty, they have 128 rows (PAIR): the two tiles are then the same
 //    rows, over alternate key tiles, and their accumulators are added at the end.
-//  * Keys.  Tiles of 128 slots: those that hold sinks, then those from the
-//    first query's window to the last query.  Each is copied box by box through
-//    the page table; boxes that nobody sees, and bad page ids, become a page
-//    past the tensor, which the copy engine fills with zeros without reading.
+//  * Keys.  A list of boxes, runs of slots within a page: those that hold sinks,
+//    then those from the first query's window to the last query.  128 / box of
+//    them make a key tile, so that four sinks cost a box and not a tile.  They are
+//    copied through the page table; boxes past the list and bad page ids become a
+//    page past the tensor, which the copy engine fills with zeros without reading.
 //    A tile that one of the two row tiles does not see is skipped for it.
 //  * Warps: two warpgroups for the softmax of a row tile each (a thread owns a
 //    row, so its maximum and sum need no exchange), one warp that issues the
@@ -63,20 +64,36 @@ struct Unit {
   int row, first, ntok;         // request, first token, tokens
   int slot;                     // slot of the first token
   int h, z;                     // kv head, share of the keys
-  int sink_tiles, from, count;  // key tiles: 0 .. sink_tiles - 1, then `from` on; `count` in all
+  int sink_boxes, from, boxes;  // boxes 0 .. sink_boxes - 1 of the row, then `from` on; `boxes` in all
+  int count;                    // key tiles
   int k0, k1;                   // this CTA's of them; k0 == k1: nothing to do
   int more;                     // 0: no unit, the CTA is done
-  __device__ int tile(int k) const { return k < sink_tiles ? k : k - sink_tiles + from; }
 };
+
+// The slots of key tile k: column c holds slot base + c, from column `jump` on base + c + gap.
+struct Columns {
+  int base, jump, gap;
+  __device__ int slot(int c) const { return base + c + (c >= jump ? gap : 0); }
+};
+
+__device__ __forceinline__ Columns columns_of(int sink_boxes, int from, int k, int shift_box) {
+  const int b = k << (7 - shift_box), gap = from - sink_boxes;  // first box; boxes left out
+  Columns x;
+  const bool sinks = b < sink_boxes;
+  x.base = (sinks ? b : b + gap) << shift_box;
+  x.jump = sinks ? (sink_boxes - b) << shift_box : kKeys;
+  x.gap = gap << shift_box;
+  return x;
+}
 
 __device__ __forceinline__ int share_begin(int c, int n, int total) { return c * (total / n) + min(c, total % n); }
 
-// The key tiles of `ntok` queries from `slot` on.
-__device__ __forceinline__ void list_tiles(const PromptParams& p, int slot, int ntok, int& sink_tiles, int& from, int& count) {
+// The boxes of `ntok` queries from `slot` on.
+__device__ __forceinline__ void list_boxes(const PromptParams& p, int slot, int ntok, int& sink_boxes, int& from, int& boxes) {
   const int last = slot + ntok - 1;
-  sink_tiles = (min(p.sinks, last + 1) + kKeys - 1) / kKeys;
-  from = max(sink_tiles, max(0, slot - p.window + 1) / kKeys);
-  count = sink_tiles + last / kKeys + 1 - from;
+  sink_boxes = (min(p.sinks, last + 1) + p.box - 1) >> p.shift_box;
+  from = max(sink_boxes, max(0, slot - p.window + 1) >> p.shift_box);
+  boxes = sink_boxes + (last >> p.shift_box) + 1 - from;
 }
 
 // What the drawing warp knows of up to 32 requests, one a lane: with these, a
@@ -98,7 +115,7 @@ __device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
     x.blocks = n > 0 ? (n + per - 1) >> p.shift_block : 0;
     if (x.r.ok && n > 0) {
       int a, b;
-      list_tiles(p, x.r.len - min(n, per), min(n, per), a, b, weight);
+      list_boxes(p, x.r.len - min(n, per), min(n, per), a, b, weight);
     }
   }
   int rank = 0;
@@ -155,7 +172,8 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows,
     return r;
   }
   r.slot = g.len - (g.end - r.first);
-  list_tiles(p, r.slot, r.ntok, r.sink_tiles, r.from, r.count);
+  list_boxes(p, r.slot, r.ntok, r.sink_boxes, r.from, r.boxes);
+  r.count = (r.boxes + (kKeys >> p.shift_box) - 1) >> (7 - p.shift_box);
   if (p.splits == 1) {
     r.k1 = r.count;
     return r;
@@ -169,9 +187,9 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows,
 }
 
 // Keys c of 32 that are visible, as bits: c < above, and c >= low or c < sink.
+__device__ __forceinline__ uint32_t below32(int x) { return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u); }
 __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
-  auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : (x >= 32 ? 0xffffffffu : (1u << x) - 1u); };
-  return below(above) & (~below(low) | below(sink));
+  return below32(above) & (~below32(low) | below32(sink));
 }
 
 // Chunk of 16 bytes `c` of row r of the partial outputs that a CTA of a cluster
@@ -206,8 +224,10 @@ __device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, 
       o[e] = o[e + 1] = 0.f;
     }
     for (int k = u.k0; k < u.k1; ++k) {
-      const int j0 = u.tile(k) * kKeys;
-      for (int j = j0; j < j0 + kKeys && j <= i; ++j) {
+      const Columns cols = columns_of(u.sink_boxes, u.from, k, p.shift_box);
+      for (int x = 0; x < kKeys; ++x) {
+        const int j = cols.slot(x);
+        if (j > i) break;
         if (j >= p.sinks && i - j >= p.window) continue;
         const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + j / p.P;
         const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
@@ -384,22 +404,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         const Unit u = s_units[n % kSlots];
         release_unit(n);
         if (u.k0 == u.k1) continue;
-        const int last = u.slot + u.ntok - 1, low = max(0, u.slot - p.window + 1);
         for (int k = u.k0; k < u.k1 && !lost; ++k, issued += 2) {
-          const int j0 = u.tile(k) * kKeys;
           // page and first token of this lane's box (at most 16 boxes a tile)
           int page = p.num_pages, tok = 0;
-          if (lane < nbox) {
-            const int j = j0 + lane * p.box;
-            if (j <= last && (j < p.sinks || j + p.box > low)) {
-              const int of_row = p.shift_page >= 0 ? j >> p.shift_page : j / p.P;
-              const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + of_row;
-              page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-              tok = j - of_row * p.P;
-              if (page < 0 || page >= p.num_pages) {
-                flag_error(p.err_flag, VH_ERR_PAGE);
-                page = p.num_pages;
-              }
+          const int box = (k << (7 - p.shift_box)) + lane;
+          if (lane < nbox && box < u.boxes) {
+            const int j = (box < u.sink_boxes ? box : box - u.sink_boxes + u.from) << p.shift_box;
+            const int of_row = p.shift_page >= 0 ? j >> p.shift_page : j / p.P;
+            const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + of_row;
+            page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
+            tok = j - of_row * p.P;
+            if (page < 0 || page >= p.num_pages) {
+              flag_error(p.err_flag, VH_ERR_PAGE);
+              page = p.num_pages;
             }
           }
           const int s = issued % ST;
@@ -475,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         Unit blk;
         blk.slot = field(from.slot);
         blk.ntok = field(from.ntok);
-        blk.sink_tiles = field(from.sink_tiles);
+        blk.sink_boxes = field(from.sink_boxes);
         blk.from = field(from.from);
         blk.count = field(from.count);
         const int k0 = field(from.k0), k1 = field(from.k1);
@@ -483,14 +500,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         if (k0 == k1) continue;
         const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
         const int qb = nq % QB;
-        // the key tiles of the list that row tile m sees: below s_end, and from w_begin to w_end
+        // the key tiles that row tile m sees: below s_end, and from w_begin to w_end
         int s_end[2], w_begin[2], w_end[2];
+        const int shift = 7 - p.shift_box;  // log2 of the boxes of a tile
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int f = blk.slot + m * per_tile, e = min(last, f + per_tile - 1);
-          s_end[m] = f > last ? 0 : min(blk.sink_tiles, e / kKeys + 1);
-          w_begin[m] = blk.sink_tiles + max(0, max(0, f - p.window + 1) / kKeys - blk.from);
-          w_end[m] = f > last ? 0 : blk.sink_tiles + e / kKeys + 1 - blk.from;
+          const int to = blk.sink_boxes + (e >> p.shift_box) - blk.from;  // last box, if it is one of the window's
+          s_end[m] = f > last ? 0 : min((blk.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
+          w_begin[m] = (blk.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - blk.from)) >> shift;
+          w_end[m] = f > last || to < blk.sink_boxes ? 0 : (to >> shift) + 1;
         }
         auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
         const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
@@ -512,12 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         };
         // values of key tile k: slots that nobody sees may hold anything where an end of
         // what the block sees lies inside the tile, so they become zeros
+        const int last_sinks = blk.sink_boxes > 0 ? (blk.sink_boxes - 1) >> shift : -1, first_window = blk.sink_boxes >> shift;
         auto clean = [&](int k) {
-          if (k + 1 != blk.count && k + 1 != blk.sink_tiles && k != blk.sink_tiles) return;
+          if (k + 1 != blk.count && k != last_sinks && k != first_window) return;
           const uint32_t vb = sKV + vi * kStage;
-          const int j0 = blk.tile(k) * kKeys;
+          const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
           for (int r = lane / 8; r < kKeys; r += 4) {
-            const int j = j0 + r;
+            const int j = cols.slot(r);
             if (j <= last && (j < p.sinks || j >= low)) continue;
 #pragma unroll
             for (int hf = 0; hf < HALVES; ++hf)
@@ -651,14 +671,33 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       const int i = min(blk.slot + token, last);
       const int f = blk.slot + mq * per_tile;                // first and last query of the tile
       const int e = min(last, f + per_tile - 1);
+      // the key tiles that the row tile sees (as the products' warp has it)
+      const int shift_tile = 7 - p.shift_box, to = blk.sink_boxes + (e >> p.shift_box) - blk.from;
+      const int s_end = f > last ? 0 : min((blk.sink_boxes + (1 << shift_tile) - 1) >> shift_tile, (e >> 7) + 1);
+      const int w_begin = (blk.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - blk.from)) >> shift_tile;
+      const int w_end = f > last || to < blk.sink_boxes ? 0 : (to >> shift_tile) + 1;
       float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
       float2 sum2 = make_float2(0.f, 0.f);
       int n = 0;
       for (int k = blk.k0; k < blk.k1; ++k) {
-        const int t = blk.tile(k);
-        if (PAIR ? ((k - blk.k0) & 1) != m
-                 : f > last || t > e / kKeys || (t >= blk.sink_tiles && t < max(0, f - p.window + 1) / kKeys))
-          continue;  // not this warpgroup's, or not seen
+        if (PAIR ? ((k - blk.k0) & 1) != m : !(k < s_end || (k >= w_begin && k < w_end))) continue;  // not this row tile's
+        // which keys this row sees, found while the scores are on their way
+        const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
+        const bool edge = (k << shift_tile) < blk.sink_boxes || cols.base + kKeys - 1 > f || cols.base <= e - p.window;
+        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (edge) {
+          // sinks, or an edge of the causal mask or of the window
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int jc = cols.base + c * 32;
+            vis[c] = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
+            if (cols.jump < kKeys) {
+              const int jg = jc + cols.gap;  // the word's first slot behind the jump
+              const uint32_t lead = below32(cols.jump - c * 32);
+              vis[c] = (vis[c] & lead) | (visible32(i + 1 - jg, i - p.window + 1 - jg, p.sinks - jg) & ~lead);
+            }
+          }
+        }
         if (!mbar_wait(s_full(m), tiles & 1)) {
           lost = true;
           break;
@@ -668,16 +707,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(tmem, m) + lanes + c * 32, sc[c]);
         tmem_wait_ld();
-        const int j0 = t * kKeys;
-        if (j0 + kKeys - 1 > f || (j0 <= e - p.window && j0 + kKeys > p.sinks)) {
-          // an edge of the causal mask, of the window or of the sinks
+        if (edge) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int jc = j0 + c * 32;
-            const uint32_t vis = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
-            if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
+            if (__all_sync(0xffffffffu, vis[c] == 0xffffffffu)) continue;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) sc[c][x] = (vis & (1u << x)) ? sc[c][x] : 0xff800000u;
+            for (int x = 0; x < 32; ++x) sc[c][x] = (vis[c] & (1u << x)) ? sc[c][x] : 0xff800000u;
           }
         }
         float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
