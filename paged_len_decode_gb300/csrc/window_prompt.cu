@@ -249,8 +249,16 @@ __device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, 
         const float by = exp2f(top - shift), w = exp2f(s - shift);
         top = now;
         sum = sum * by + w;
+        bool gone = true;
 #pragma unroll
-        for (int e = 0; e < PER; ++e) o[e] = o[e] * by + w * v[e];
+        for (int e = 0; e < PER; ++e) {
+          o[e] = o[e] * by + w * v[e];
+          gone = gone && o[e] != o[e];
+        }
+        if ((x & 15) == 15 && __all_sync(0xffffffffu, gone)) {  // all NaN, whatever follows
+          k = u.k1;
+          break;
+        }
       }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;

@@ -159,3 +159,21 @@ def test_bad_positions_pages_and_rows_are_flagged():
         assert call(lens=lens)[:2] == (v.VH_ERR_SEQLEN, [True, True, False, False, True, True])
     err, wrote, _ = call(starts=[0, 2, 4, 9])  # tokens past the arrays
     assert err == v.VH_ERR_SEQLEN and wrote == [True, True, True, True, False, False]
+
+
+def test_no_tokens():
+    """An empty batch of tokens is accepted by the append and the prompt attention, and writes nothing."""
+    v = vh()
+    r = R.make([5, 7], [0, 0], Hq=4, Hkv=2, D=64, seed=2)
+    pool = r.pool.cuda()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.zeros(0, 8, 64, dtype=BF, device="cuda")
+    q_rot = torch.zeros(0, 4, 64, dtype=BF, device="cuda")
+    k, val = r.view(pool, 0), r.view(pool, 1)
+    rows = (r.table.cuda(), i32(r.lens), i32(r.active))
+    v.vh_mrope_kv_append(x[:, :4], x[:, 4:6], x[:, 6:], v.vh_rope_table(torch.empty(8, 64, device="cuda")), k, val, *rows, q_rot,
+                         token_start=i32(r.starts))
+    ws = v.alloc_prompt_workspace(0, 2, 4, 2, 64)
+    v.vh_window_prompt_attn(q_rot, k, val, rows[0], i32(r.starts), *rows[1:], torch.zeros_like(q_rot), ws)
+    torch.cuda.synchronize()
+    assert torch.equal(pool.cpu().view(torch.int16), r.pool.view(torch.int16))

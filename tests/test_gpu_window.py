@@ -90,6 +90,44 @@ def test_decode_split_rows(num_ctas):
     check_decode(R.make([900, 3, 411, 1], [1] * 4, window=700, sinks=20, seed=num_ctas), num_ctas=num_ctas)
 
 
+@pytest.mark.parametrize("B", [128, 129, 700])
+def test_decode_many_rows(B):
+    # more rows than the producer warp sums up alone, and more than CTAs
+    lens = [1 + (29 * b) % 75 for b in range(B)]
+    lens[B // 2] = 1500
+    check_decode(R.make(lens, [1] * B, Hq=2, Hkv=1, D=64, window=40, sinks=3, active=[int(b % 9 != 4) for b in range(B)], seed=B))
+    check_decode(R.make(lens, [1] * B, Hq=2, Hkv=1, D=64, seed=B))
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose elements lie more than 2^32 into the pool: the same bits as in a small pool."""
+    v = vh()
+    P, HKV, D, lens = 16, 8, 128, [70, 33]
+    far = (1 << 32) // (2 * P * HKV * D) + 3
+    small = R.make(lens, [1, 1], P=P, seed=4)
+    big = torch.empty(far + small.pool.shape[0], 2, P, HKV, D, dtype=BF, device="cuda")
+    big[far:] = small.pool.cuda()
+    table = torch.where(small.table > 0, small.table + far, small.table).cuda()
+    x = torch.randn(2, 32, D).to(BF).cuda()
+    cs = v.vh_rope_table(torch.empty(128, D, device="cuda"))
+    got = []
+    for pool, t in ((small.pool.cuda(), small.table.cuda()), (big, table)):
+        k, val = pool[:, 0], pool[:, 1]
+        q32 = torch.empty(2, 16, D, device="cuda")
+        q16 = torch.empty(2, 16, D, dtype=BF, device="cuda")
+        rows = (t, i32(lens), i32([1, 1]))
+        o1, o2 = torch.zeros(2, 16, D, dtype=BF, device="cuda"), torch.zeros(2, 16, D, dtype=BF, device="cuda")
+        for q in (q32, q16):
+            v.vh_mrope_kv_append(x[:, :16], x[:, 16:24], x[:, 24:], cs, k, val, *rows, q)
+        v.vh_window_decode_attn(q32, k, val, *rows, o1, v.alloc_workspace(2, 16, HKV, D, P))
+        v.vh_window_prompt_attn(q16, k, val, t, i32([0, 1, 2]), *rows[1:], o2, v.alloc_prompt_workspace(2, 2, 16, HKV, D))
+        torch.cuda.synchronize()
+        n = small.pool.shape[0]
+        got.append((o1, o2, pool[-n:].clone().view(torch.int16)))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.isfinite(got[0][0].float()).all() and torch.isfinite(got[0][1].float()).all()
+
+
 def test_decode_many_pieces_and_repeated_calls():
     r = R.make([6000, 17], [1, 1], Hq=8, Hkv=1, window=5500, sinks=40, seed=3)
     check_decode(r)
