@@ -406,6 +406,10 @@ int vh_paged_decode_attn_noalloc(const float* q_rot, const vh_bf16* k_cache, con
  * that fell behind the window may have been given back, and their entries
  * may hold anything.  Keys or values that one query does not see never
  * change its result, whatever they hold (NaN and infinities too).
+ *
+ * The kernels are launched as programmatic dependents of the previous kernel
+ * on the stream and wait for it before they touch memory (but for what
+ * VH_FLAG_PDL allows), so they keep the stream's order as any launch does.
  */
 
 /* RoPE with one to four axes of positions (time, height, width, ...) and KV

@@ -18,8 +18,9 @@
 // What counts is bytes in flight and the length of the chain of look-ups: 20 warps
 // an SM with three heads' loads a lane each measured 64 us on 16384 tokens (32 / 8
 // heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.3 us on 2413 with the norm;
-// 24 warps with two 63.6 and 10.1 us, 16 warps with four 83, and a CTA of 4 tokens
-// with its angles in shared memory behind a barrier 82 us.  Angles gathered beside
+// 24 warps with two 63.6 and 10.1 us.  In an earlier form four heads took 68 us
+// where two took 66, and a CTA of 4 tokens with its angles in shared memory
+// behind a barrier 82 us.  Angles gathered beside
 // the row's look-up instead of after it, and weights by 16 bytes: 12.2 -> 10.1 us.
 #include "vh_ragged.cuh"
 #include "vh_window.h"

@@ -194,3 +194,28 @@ def test_captured_steps_with_other_lengths_and_a_shared_workspace():
                 torch.cuda.synchronize()
                 check(m, c, o, True)
     assert int(err) == 0
+
+
+def test_readme_example_runs_as_written():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    first, second = re.findall(r"```python\n(.*?)```", text, re.S)[:2]
+    torch.manual_seed(6)
+    e = {}
+    exec(first, e)
+    prompt, single = second.split("seq_lens += 1", 1)
+    exec(prompt, e)
+    torch.cuda.synchronize()
+    starts = e["token_start"].tolist()
+    news = [b - a for a, b in zip(starts, starts[1:])]
+
+    def reference(q, lens, n):
+        r = R.Ragged(e["Hq"], e["Hkv"], e["D"], e["P"], e["pool"].cpu(), "NHD", e["page_table"].cpu(), lens, n, [1] * len(lens),
+                     e["window"], e["sinks"])
+        return R.attention(r, q.cpu())
+
+    assert R.close(e["prompt_out"], reference(e["q_rot"], news, news), torch.bfloat16, e["D"], False) is None
+    exec("seq_lens += 1" + single, e)
+    torch.cuda.synchronize()
+    assert R.close(e["out"], reference(e["q_rot32"], [n + 1 for n in news], [1] * 8), torch.bfloat16, e["D"], True) is None
