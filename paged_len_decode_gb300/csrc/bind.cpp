@@ -31,14 +31,17 @@ template <typename... A>
 // Positional and keyword arguments of one function, by position.
 struct Signature {
   const char* function;
-  std::initializer_list<const char*> names;
   int required;
+  const char* names[32];  // (string literals; an initializer_list's own array would not outlive the constructor)
   PyObject* interned[32];
   int n = 0;
-  Signature(const char* f, std::initializer_list<const char*> ns, int req) : function(f), names(ns), required(req) {
-    for (const char* s : names) interned[n++] = PyUnicode_InternFromString(s);
+  Signature(const char* f, std::initializer_list<const char*> ns, int req) : function(f), required(req) {
+    for (const char* s : ns) {
+      names[n] = s;
+      interned[n++] = PyUnicode_InternFromString(s);
+    }
   }
-  const char* name(int i) const { return names.begin()[i]; }
+  const char* name(int i) const { return names[i]; }
   void parse(PyObject* const* args, Py_ssize_t nargs, PyObject* kw, PyObject** to) const {
     if (nargs > n) raise(PyExc_TypeError, "%s takes at most %d arguments", function, n);
     for (int i = 0; i < n; ++i) to[i] = i < nargs ? args[i] : nullptr;

@@ -140,3 +140,23 @@ def test_binding_refuses(op, wrong, text):
     call, args = binding_args(op)
     with pytest.raises(ValueError, match=text):
         call(**dict(args, **wrong))
+
+
+@pytest.mark.parametrize("call, first, count", [(v.vh_mrope_kv_append, "q", 19), (v.vh_window_decode_attn, "q_rot", 15),
+                                                (v.vh_window_prompt_attn, "q", 15)])
+def test_arguments_are_named_in_errors_call_after_call(call, first, count):
+    for _ in range(3):
+        with pytest.raises(TypeError, match=f"needs the argument '{first}'"):
+            call()
+        with pytest.raises(TypeError, match=f"got two values for '{first}'"):
+            call(1, **{first: 1})
+        with pytest.raises(TypeError, match="unexpected argument 'nothing'"):
+            call(nothing=1)
+        with pytest.raises(TypeError, match=f"at most {count} arguments"):
+            call(*range(count + 1))
+    for _ in range(2):
+        with pytest.raises(TypeError, match="q_norm_w must be a torch.Tensor"):
+            x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+            pool = torch.zeros(1, 16, 2, 64, dtype=torch.bfloat16)
+            one = torch.ones(1, dtype=torch.int32)
+            v.vh_mrope_kv_append(x, x, x, torch.zeros(4, 64), pool, pool, one[:, None], one, one, x, q_norm_w=1)
