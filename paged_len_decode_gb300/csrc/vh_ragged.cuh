@@ -83,7 +83,7 @@ __device__ __forceinline__ int warp_row_of_token(const int32_t* token_start, con
   const int row = token_start ? warp_last_at_most(B, t, lane, [&](int b) { return __ldg(token_start + b); }) : t;
   if (row < 0) return -1;
   r = ragged_row(token_start, seq_lens, active, row, T, max_len, err_flag, report);
-  return t < r.end ? row : -1;
+  return r.start <= t && t < r.end ? row : -1;  // (offsets out of order may find a row that starts behind t)
 }
 
 }  // namespace vh

@@ -177,3 +177,30 @@ def test_no_tokens():
     v.vh_window_prompt_attn(q_rot, k, val, rows[0], i32(r.starts), *rows[1:], torch.zeros_like(q_rot), ws)
     torch.cuda.synchronize()
     assert torch.equal(pool.cpu().view(torch.int16), r.pool.view(torch.int16))
+
+
+def test_offsets_out_of_order_write_no_foreign_slots():
+    """With more than 32 rows a token's row is searched; offsets out of order (not allowed, but data) may lead the
+    search to a row that starts behind the token.  Nothing may be written then but slots of the rows' own new tokens."""
+    v = vh()
+    B, T, P, Hq, Hkv, D = 40, 200, 16, 4, 2, 64
+    g = torch.Generator().manual_seed(9)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    x = torch.randn(T, Hq + 2 * Hkv, D, generator=g).to(BF).cuda()
+    cs = v.vh_rope_table(torch.empty(256, D, device="cuda"))
+    per = 16  # pages a row: up to 256 tokens
+    table = torch.arange(B * per, dtype=torch.int32).view(B, per).cuda()
+    for _ in range(8):
+        starts = torch.randint(0, T + 1, (B + 1,), generator=g).tolist()
+        lens = [max(0, e - a) for a, e in zip(starts, starts[1:])]
+        pool = torch.full((B * per + 2, 2, P, Hkv, D), 5.0, dtype=BF, device="cuda")
+        inner = pool[1:-1]  # a page on either side that no table entry names
+        q_rot = torch.full((T, Hq, D), 7.0, device="cuda")
+        v.vh_mrope_kv_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], cs, inner[:, 0], inner[:, 1], table, i32(lens),
+                             i32([1] * B), q_rot, token_start=i32(starts))
+        torch.cuda.synchronize()
+        wrote = (pool != 5.0).flatten(3).any(3)[:, 0].cpu()
+        assert not wrote[0].any() and not wrote[-1].any()
+        by_row = wrote[1:-1].reshape(B, per * P)
+        for b in range(B):
+            assert not by_row[b, lens[b]:].any()
