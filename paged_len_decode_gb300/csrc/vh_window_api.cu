@@ -3,6 +3,7 @@
 // of scalars and alignment, launch plans, launches on the caller's stream.
 // Nothing here synchronises, allocates or reads device memory.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -29,21 +30,26 @@ constexpr int kMaxHc = 8;
 constexpr int kMaxStages = 8;
 constexpr int kStageTarget = 65536;  // bytes in flight of a CTA, two CTAs on an SM
 
-// Kernel attributes of this file's kernels, set on the first call on a device.
+// Kernel attributes of this file's kernels, set on the first call on a device
+// (a call that could not set them leaves it to the next one).
 struct Prepared {
-  std::once_flag once;
-  bool ok = false;
+  std::mutex mu;
+  std::atomic<bool> ok{false};
   int clusters[5] = {};  // clusters of 2^x CTAs of the prompt kernel that run at a time
 };
 Prepared g_prepared[kMaxDevices];
 
 bool prepared(const DeviceInfo& dev) {
   Prepared& s = g_prepared[dev.index];
-  std::call_once(s.once, [&]() {
-    s.ok = vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(s.clusters) == cudaSuccess;
-    if (!s.ok) cudaGetLastError();
-  });
-  return s.ok;
+  if (s.ok.load(std::memory_order_acquire)) return true;
+  std::lock_guard<std::mutex> lk(s.mu);
+  if (s.ok.load(std::memory_order_relaxed)) return true;
+  if (vh::prepare_window_decode(dev.smem_optin) != cudaSuccess || vh::prepare_window_prompt(s.clusters) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  s.ok.store(true, std::memory_order_release);
+  return true;
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -120,7 +126,7 @@ bool plan_decode(vh::WindowDecodeParams& p, const DeviceInfo& dev, int* auto_n) 
     if (c.ok) {
       if (vh::window_decode_occupancy(q, &per_sm) != cudaSuccess || per_sm < 1) {
         cudaGetLastError();
-        per_sm = 1;
+        return false;  // not remembered: the next call asks again
       }
       c = DecodePlan{true,      q.Hc,      q.groups,  q.stages,   q.stage_bytes, q.q_off,
                      q.cum_off, q.len_off, q.bar_off, q.smem_bytes, 0};
@@ -322,7 +328,7 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
                           int max_pages_per_seq, const int32_t* seq_lens, const int32_t* active, int window, int sinks,
                           vh_e16* out, float sm_scale, int num_ctas, void* workspace, size_t workspace_bytes,
                           int32_t* err_flag, unsigned flags, int B, int Hq, int Hkv, int D, int page_size,
-                          void* stream) {
+                          void* stream) try {
   if (!q_rot || !k_cache || !v_cache || !seq_lens || !active || !out ||
       (flags & ~(VH_FLAG_FP16 | VH_FLAG_PDL)) != 0 || window < 0 || sinks < 0 || num_ctas < 0 || num_ctas > 65535 ||
       !(sm_scale == sm_scale) ||
@@ -384,6 +390,8 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   p.scale_log2 = scale * 1.4426950408889634f;
   p.early = (flags & VH_FLAG_PDL) != 0;
   return status_of(vh::launch_window_decode(p, static_cast<cudaStream_t>(stream)));
+} catch (...) {  // (a plan that the host has no memory for; no exception leaves a C function)
+  return VH_ECUDA;
 }
 
 size_t vh_prompt_workspace_bytes(int T, int B, int Hq, int Hkv, int D) {
