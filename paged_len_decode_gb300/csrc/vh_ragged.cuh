@@ -1,5 +1,5 @@
 // vh_ragged.cuh -- device helpers of ragged batches: the row of a token or of
-// a block of tokens, and the checks of a row's extent.
+// a block of tokens, the checks of a row's extent, and weights in merges.
 #pragma once
 
 #include "vh_common.cuh"
@@ -35,6 +35,10 @@ __device__ __forceinline__ int warp_last_at_most(int B, int x, int lane, Key key
   }
   return lo - 1;
 }
+
+// A piece's weight in a merge: not 0 however small beside the others, so that its
+// infinities stay (a NaN stays a NaN).
+__device__ __forceinline__ float at_least_tiny(float w) { return w < 1.2e-38f ? 1.2e-38f : w; }
 
 // A row of a ragged batch.
 struct RaggedRow {

@@ -37,8 +37,18 @@
 //  * What is not seen: scores get -inf; rows of V that no query of the block
 //    sees (page tails, freed pages) are zeroed in shared memory.  A value that
 //    some rows of a tile see and others do not meets weight 0 there, which is
-//    harmless unless it is infinite or NaN; a row that ends with a NaN is
-//    therefore computed again over its visible keys alone, one warp a row.
+//    harmless unless it is infinite or NaN; so does one whose weight is too small
+//    for the element type.  A block with an output that is no number, although its
+//    row's sum is one, therefore runs once more, by the same pipeline, with such
+//    values as zeros, and then once for each kind of them (+inf, -inf, NaN) that was
+//    met, with the values of that kind as ones and the others as zeros and weight 1
+//    for every visible key: outputs that come out above zero are set to what they
+//    must be.  A block takes about its usual time each of these times, whatever the
+//    cache holds, so no wait of the pipeline grows longer.  In a cluster, where
+//    partial outputs lie in memory that the runs need, the kinds are noted beside
+//    them and set in a last run.  All of this is kept apart from the common path: a
+//    function call, or code for it between the products, costs that 2 to 8 us of 43
+//    (24 ragged prompts of up to 800 tokens, head_dim 64), though never executed.
 //  * Few blocks (short chunks over long contexts): the key tiles of a block are
 //    shared by a cluster of up to 16 CTAs, which leave their partial results in
 //    shared memory and add them over distributed shared memory, each a share of
@@ -59,6 +69,13 @@ constexpr int kSlots = 2;        // blocks drawn: this one and the next
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
+// What a block is run for: its outputs; and where some of them are no numbers, its
+// outputs with values that are no numbers left out, and then which of them such
+// values reach: +inf, -inf, NaN, and infinities under a score of -inf (0 times
+// infinity is NaN).  What a run has met is noted in bits of its slot: bit 0, outputs
+// that are no numbers; bit m - 1, something for mode m.
+enum { kPlain, kWithout, kPlusInf, kMinusInf, kNaN, kNoWeight, kSettle };
+
 // One CTA's work: queries of one request and kv head, and a share of their key tiles.
 struct Unit {
   int row, first, ntok;         // request, first token, tokens
@@ -67,6 +84,9 @@ struct Unit {
   int sink_boxes, from, boxes;  // boxes 0 .. sink_boxes - 1 of the row, then `from` on; `boxes` in all
   int count;                    // key tiles
   int k0, k1;                   // this CTA's of them; k0 == k1: nothing to do
+  int mode;                     // kPlain, or once more
+  int settle;                   // the last of a cluster's runs: what was noted is set
+  int soft;                     // k1, or k0 where the unit runs once more (or has nothing to do)
   int more;                     // 0: no unit, the CTA is done
 };
 
@@ -94,6 +114,21 @@ __device__ __forceinline__ void list_boxes(const PromptParams& p, int slot, int 
   sink_boxes = (min(p.sinks, last + 1) + p.box - 1) >> p.shift_box;
   from = max(sink_boxes, max(0, slot - p.window + 1) >> p.shift_box);
   boxes = sink_boxes + (last >> p.shift_box) + 1 - from;
+}
+
+// The key tiles that row tile m of a block sees: below s_end, and from w_begin to w_end.
+struct Tiles {
+  int s_end, w_begin, w_end;
+  __device__ bool has(int k) const { return k < s_end || (k >= w_begin && k < w_end); }
+};
+__device__ __forceinline__ Tiles tiles_of(const PromptParams& p, const Unit& u, int m) {
+  const int per_tile = kRows >> p.shift_g, last = u.slot + u.ntok - 1, f = u.slot + m * per_tile, e = min(last, f + per_tile - 1);
+  const int shift = 7 - p.shift_box, to = u.sink_boxes + (e >> p.shift_box) - u.from;
+  Tiles t;
+  t.s_end = f > last ? 0 : min((u.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
+  t.w_begin = (u.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - u.from)) >> shift;
+  t.w_end = f > last || to < u.sink_boxes ? 0 : (to >> shift) + 1;
+  return t;
 }
 
 // What the drawing warp knows of up to 32 requests, one a lane: with these, a
@@ -192,6 +227,18 @@ __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
   return below32(above) & (~below32(low) | below32(sink));
 }
 
+// The keys of columns c .. c + 31 that the query in slot i sees.
+__device__ __forceinline__ uint32_t visible_of(const Columns& cols, int c, int i, int window, int sinks) {
+  const int jc = cols.base + c;
+  uint32_t vis = visible32(i + 1 - jc, i - window + 1 - jc, sinks - jc);
+  if (cols.jump < kKeys) {
+    const int jg = jc + cols.gap;  // the word's first slot behind the jump
+    const uint32_t lead = below32(cols.jump - c);
+    vis = (vis & lead) | (visible32(i + 1 - jg, i - window + 1 - jg, sinks - jg) & ~lead);
+  }
+  return vis;
+}
+
 // Chunk of 16 bytes `c` of row r of the partial outputs that a CTA of a cluster
 // leaves in its shared memory (fp32 [256][D]): chunks turned by the row, so that
 // 32 rows written at the same chunk fall into different banks.
@@ -200,84 +247,556 @@ __device__ __forceinline__ uint32_t part_off(int r, int c) {
   return static_cast<uint32_t>(r * D * 4 + ((c ^ (r & (D / 4 - 1))) << 4));
 }
 
-// The rows `rows` (bits) of this warp's 32, one after the other by the whole
-// warp, over the keys that they see among the unit's tiles, one at a time: for
-// rows that a value they do not see has reached (0 times infinity).  Lanes over
-// head_dim.  Out of line, so that the common path keeps its registers.
-template <typename E, int D>
-__device__ __noinline__ void attend_alone(const PromptParams& p, const Unit& u, int m, uint32_t rows, uint32_t part,
-                                          uint32_t part_lse) {
-  constexpr int PER = D / 32;
-  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3;
-  const float NEG_INF = __int_as_float(0xff800000);
-  while (rows) {
-    const int r = warp * 32 + __ffs(rows) - 1;
-    rows &= rows - 1;
-    const int token = m * (kRows / p.G) + r / p.G, i = u.slot + token;
-    const long long at = ((u.first + token) * static_cast<long long>(p.Hq) + u.h * p.G + r % p.G) * D + lane * PER;
-    float q[PER], o[PER], top = NEG_INF, sum = 0.f;
+// The two elements of a word of V, as `mode` takes them; `met`: kinds of values found.
+template <typename E>
+__device__ __forceinline__ uint32_t filtered(uint32_t w, int mode, uint32_t& met) {
+  constexpr uint32_t kInf = E::kF16 ? 0x7C00u : 0x7F80u, kOne = E::kF16 ? 0x3C00u : 0x3F80u;
+  uint32_t out = 0u;
 #pragma unroll
-    for (int e = 0; e < PER; e += 2) {
-      const float2 w = E::to_float2(*reinterpret_cast<const uint32_t*>(p.q + at + e));
-      q[e] = w.x;
-      q[e + 1] = w.y;
-      o[e] = o[e + 1] = 0.f;
-    }
-    for (int k = u.k0; k < u.k1; ++k) {
-      const Columns cols = columns_of(u.sink_boxes, u.from, k, p.shift_box);
-      for (int x = 0; x < kKeys; ++x) {
-        const int j = cols.slot(x);
-        if (j > i) break;
-        if (j >= p.sinks && i - j >= p.window) continue;
-        const long long lp = static_cast<long long>(u.row) * p.max_pages_per_seq + j / p.P;
-        const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
-        const bool ok = page >= 0 && page < p.num_pages;
-        const long long off = ok ? page * p.page_stride + (j % p.P) * p.token_stride + u.h * p.head_stride + lane * PER : 0;
-        float s = 0.f, v[PER];
-#pragma unroll
-        for (int e = 0; e < PER; e += 2) {
-          const float2 kk = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.k_cache + off + e)) : make_float2(0.f, 0.f);
-          const float2 vv = ok ? E::to_float2(*reinterpret_cast<const uint32_t*>(p.v_cache + off + e)) : make_float2(0.f, 0.f);
-          s += q[e] * kk.x + q[e + 1] * kk.y;
-          v[e] = vv.x;
-          v[e + 1] = vv.y;
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= p.scale_log2;
-        const float now = fmaxf(top, s), shift = now == NEG_INF ? 0.f : now;
-        const float by = exp2f(top - shift), w = exp2f(s - shift);
-        top = now;
-        sum = sum * by + w;
-        bool gone = true;
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-          o[e] = o[e] * by + w * v[e];
-          gone = gone && o[e] != o[e];
-        }
-        if ((x & 15) == 15 && __all_sync(0xffffffffu, gone)) {  // all NaN, whatever follows
-          k = u.k1;
-          break;
-        }
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    if (p.splits > 1) {
-      const int row = m * kRows + r;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) {
-        const int x = lane * PER + e;
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(part + part_off<D>(row, x / 4) + (x % 4) * 4), "f"(o[e] * inv) : "memory");
-      }
-      if (lane == 0)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(part_lse + row * 4),
-                     "f"(sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum))
-                     : "memory");
-    } else {
-#pragma unroll
-      for (int e = 0; e < PER; e += 2) *reinterpret_cast<uint32_t*>(p.out + at + e) = E::pack2(o[e] * inv, o[e + 1] * inv);
+  for (int x = 0; x < 32; x += 16) {
+    const uint32_t h = (w >> x) & 0xFFFFu, size = h & 0x7FFFu;
+    const int kind = size < kInf ? kPlain : (size > kInf ? kNaN : (h == kInf ? kPlusInf : kMinusInf));
+    if (mode == kWithout) {
+      if (kind == kPlain) out |= h << x;
+      else met |= 1u << (kind - 1);
+    } else if (kind == mode || (mode == kNoWeight && (kind == kPlusInf || kind == kMinusInf))) {
+      out |= kOne << x;
     }
   }
+  return out;
+}
+
+// A stage of V (`bytes` of shared memory, a multiple of 2048), by one warp.
+template <typename E>
+__device__ __forceinline__ uint32_t filter_values(uint32_t addr, int bytes, int mode, int lane) {
+  constexpr uint32_t kInf = E::kF16 ? 0x7C007C00u : 0x7F807F80u, kStep = E::kF16 ? 0x04000400u : 0x00800080u;
+  uint32_t met = 0u;
+  for (int x = lane * 16; x < bytes; x += 4 * 512) {
+    uint32_t odd[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[4];
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr + x + i * 512));
+      // bits 15 and 31: an exponent of all ones
+      odd[i] = (((w[0] & kInf) + kStep) | ((w[1] & kInf) + kStep) | ((w[2] & kInf) + kStep) | ((w[3] & kInf) + kStep)) & 0x80008000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (odd[i] == 0u && mode == kWithout) continue;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if (odd[i] != 0u) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr + x + i * 512));
+#pragma unroll
+        for (int y = 0; y < 4; ++y) w[y] = filtered<E>(w[y], mode, met);
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr + x + i * 512), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+  return met;
+}
+
+// An output `old` that a value of mode's kind reaches.
+__device__ __forceinline__ float reached(float old, int mode) {
+  const float inf = __int_as_float(0x7f800000), nan = __int_as_float(0x7fffffff);
+  if (old != old) return old;
+  return mode == kPlusInf ? inf : (mode == kMinusInf && old != inf ? -inf : nan);
+}
+
+// A softmax warp's part of a run that only asks which keys its rows see: weight 1 for every
+// visible one (kNoWeight: for those whose score is -inf); then every output whose
+// accumulator is above 0 is set, or in a cluster noted (the warp's words of a bit a
+// column for +inf, -inf and NaN, in its part of `staging`).  bars: s_full of both row tiles,
+// then p_full, o_full and o_seen.  Returns the key tiles done, or -1 if a wait ran out.
+template <typename E, int D, bool PAIR>
+__device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit& u, int tiles, int blocks, uint32_t tmem,
+                                           uint32_t bars, uint32_t staging) {
+  const int m = threadIdx.x >> 7, warp = threadIdx.x >> 5;
+  const uint32_t noted = staging + static_cast<uint32_t>(warp) * 4096 + 2048;
+  tmem += static_cast<uint32_t>((warp & 3) * 32) << 16;
+  constexpr uint32_t kOne = E::kF16 ? 0x3C00u : 0x3F80u;
+  const int lane = threadIdx.x & 31, r = threadIdx.x & (kRows - 1), mode = u.mode;
+  const int before = tiles, per_tile = kRows >> p.shift_g, mq = PAIR ? 0 : m, token = mq * per_tile + (r >> p.shift_g);
+  const int last = u.slot + u.ntok - 1, i = min(u.slot + token, last);
+  const uint32_t scores = tmem + static_cast<uint32_t>(m * kKeys);
+  const Tiles sees = tiles_of(p, u, mq);
+#pragma unroll 1
+  for (int k = u.k0; k < u.k1; ++k) {
+    if (PAIR ? ((k - u.k0) & 1) != m : !sees.has(k)) continue;
+    const Columns cols = columns_of(u.sink_boxes, u.from, k, p.shift_box);
+    if (!mbar_wait(bars + 8 * m, tiles & 1)) return -1;
+    tc_fence_after();
+    uint32_t vis[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      vis[c] = visible_of(cols, 32 * c, i, p.window, p.sinks);
+      if (mode == kNoWeight) {
+        uint32_t x[32], low = 0u;
+        tmem_ld32(scores + 32 * c, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 32; ++y) low |= (x[y] == 0xff800000u ? 1u : 0u) << y;
+        vis[c] &= low;
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t w[32];
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        const uint32_t b = vis[2 * half + (x >> 4)] >> (2 * (x & 15));
+        w[x] = ((b & 1u) ? kOne : 0u) | ((b & 2u) ? kOne << 16 : 0u);
+      }
+      tmem_st32(scores + half * 32, w);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(bars + 8 * (2 + 2 * m + half));
+    }
+    ++tiles;
+  }
+  if (!mbar_wait(bars + 8 * (6 + m), blocks & 1) || ((PAIR || p.splits > 1) && !mbar_wait(bars + 8 * (6 + (m ^ 1)), blocks & 1))) return -1;
+  if (lane == 0) mbar_arrive(bars + 8 * (8 + m));
+  tc_fence_after();
+  __syncwarp();  // (the outputs of the runs before were stored by other lanes)
+  // accumulators that hold this run's sums: the row tile's, and for a pair both where there are two tiles
+  const bool first = PAIR || tiles > before, second = PAIR && u.k1 - u.k0 > 1;
+  const int c_end = PAIR ? min(D, 64 * m + 64) : D;
+  uint32_t bits = 0u;
+#pragma unroll 1
+  for (int c = PAIR ? 64 * m : 0; c < c_end; c += 8) {
+    uint32_t x[8], hit = 0u;
+    if (first) {
+      tmem_ld8(tmem + static_cast<uint32_t>(2 * kKeys + mq * D + c), x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int y = 0; y < 8; ++y) hit |= (x[y] != 0u ? 1u : 0u) << y;
+    }
+    if (second) {
+      tmem_ld8(tmem + static_cast<uint32_t>(2 * kKeys + D + c), x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int y = 0; y < 8; ++y) hit |= (x[y] != 0u ? 1u : 0u) << y;
+    }
+    if (p.splits > 1) {
+      bits |= hit << (c & 31);
+      if ((c & 31) == 24) {
+        const uint32_t at = noted + static_cast<uint32_t>((min(mode, static_cast<int>(kNaN)) - kPlusInf) * 4 + c / 32) * 128 + lane * 4;
+        uint32_t old;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(old) : "r"(at));
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(old | bits) : "memory");
+        bits = 0u;
+      }
+    } else if (hit != 0u && token < u.ntok) {
+      uint16_t* at = p.out + ((u.first + token) * static_cast<long long>(p.Hq) + u.h * p.G + (r & (p.G - 1))) * D + c;
+#pragma unroll 1
+      for (int y = 0; y < 8; ++y)
+        if ((hit >> y) & 1u) at[y] = E::bits(reached(E::to_float(at[y]), mode));
+    }
+  }
+  return tiles - before;
+}
+
+// 64 columns from c0 on of this thread's row of a cluster's partial results, just written.
+// noted: this thread's words of a bit a column for +inf, -inf and NaN, to be cleared, or
+// (settle) what they say is set.
+template <int D>
+__device__ __forceinline__ void settle_part(uint32_t part, int row, int c0, uint32_t noted, bool settle) {
+#pragma unroll 1
+  for (int c = c0; c < c0 + 64; ++c) {
+    const uint32_t at = part + part_off<D>(row, c / 4) + (c % 4) * 4;
+    float y;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(at));
+#pragma unroll 1
+    for (int kind = kPlusInf; kind <= kNaN; ++kind) {
+      const uint32_t word = noted + static_cast<uint32_t>((kind - kPlusInf) * 4 + c / 32) * 128;
+      uint32_t bits;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(bits) : "r"(word));
+      if (!settle) asm volatile("st.shared.b32 [%0], %1;" ::"r"(word), "r"(0u) : "memory");
+      else if ((bits >> (c & 31)) & 1u) y = reached(y, kind);
+    }
+    if (settle) asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(y) : "memory");
+  }
+}
+
+__device__ __forceinline__ void note_met(uint32_t met, uint32_t bits) {
+  asm volatile("red.shared.or.b32 [%0], %1;" ::"r"(met), "r"(bits) : "memory");
+}
+
+// What the warps of a CTA share, beside the dynamic shared memory.
+template <int D>
+struct Shared {
+  static constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
+  uint64_t bars[3 * ST + 2 * QB + 11 + 2 * kSlots];
+  Unit units[kSlots];
+  Unit join;        // the block whose partial results a cluster joins
+  int met[kSlots];  // of the unit in the slot (see kPlain)
+  uint32_t tmem;
+  int abort;
+
+  __device__ __forceinline__ void release(int n, int lane);
+  // All warps meet behind the CTA's last unit; false: one of the units before has to run
+  // once more (all of them see the same; the drawing warp waits until they have).
+  __device__ __forceinline__ bool all_done() {
+    tc_fence_before();
+    named_sync(1, kThreads);
+    if (*static_cast<volatile int*>(&abort)) return true;
+    bool more = false;
+#pragma unroll
+    for (int x = 0; x < kSlots; ++x) {
+      const volatile Unit& u = units[x];
+      more = more || (u.more != 0 && (u.mode != kPlain || (*static_cast<volatile int*>(&met[x]) & 1) != 0));
+    }
+    return !more;
+  }
+  // Waits for unit number n of this CTA, or the one behind it; false: the CTA is done, or a
+  // wait ran out and this warp has still to meet the others.
+  __device__ __forceinline__ bool next(int& n, bool& lost, int lane);
+};
+
+// Their barriers.
+template <int D>
+struct Bars {
+  static constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
+  uint32_t at;
+  __device__ uint32_t full(int s) const { return at + 8 * s; }
+  __device__ uint32_t empty(int s) const { return at + 8 * (ST + s); }
+  __device__ uint32_t q_full(int b) const { return at + 8 * (2 * ST + b); }
+  __device__ uint32_t q_empty(int b) const { return at + 8 * (2 * ST + QB + b); }
+  __device__ uint32_t s_full(int m) const { return at + 8 * (2 * ST + 2 * QB + m); }
+  __device__ uint32_t p_full(int m, int half) const { return at + 8 * (2 * ST + 2 * QB + 2 + 2 * m + half); }
+  __device__ uint32_t o_full(int m) const { return at + 8 * (2 * ST + 2 * QB + 6 + m); }
+  __device__ uint32_t o_seen(int m) const { return at + 8 * (2 * ST + 2 * QB + 8 + m); }
+  __device__ uint32_t met() const { return at + 8 * (2 * ST + 2 * QB + 10); }  // both softmax warpgroups
+  __device__ uint32_t u_full(int s) const { return at + 8 * (2 * ST + 2 * QB + 11 + s); }
+  __device__ uint32_t u_empty(int s) const { return at + 8 * (2 * ST + 2 * QB + 11 + kSlots + s); }
+  __device__ uint32_t landed(int s) const { return at + 8 * (2 * ST + 2 * QB + 11 + 2 * kSlots + s); }  // V, to be filtered
+};
+
+template <int D>
+__device__ __forceinline__ void Shared<D>::release(int n, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(Bars<D>{smem_addr(bars)}.u_empty(n % kSlots));
+}
+template <int D>
+__device__ __forceinline__ bool Shared<D>::next(int& n, bool& lost, int lane) {
+  for (;; ++n) {
+    lost = !mbar_wait(Bars<D>{smem_addr(bars)}.u_full(n % kSlots), (n / kSlots) & 1);
+    if (lost) return false;
+    if (units[n % kSlots].more != 0) return true;
+    if (all_done()) return false;
+    release(n, lane);
+  }
+}
+
+// The drawing warp's part of a run that is not the first: the `count` tiles of V, number
+// `first` of the CTA on, as they land, filtered and passed on to the products' warp.
+// phases: of the stages' barriers, a bit each.  Returns them as they are then, or
+// kLostPhase if a wait ran out.
+constexpr uint32_t kLostPhase = 0x80000000u;
+template <typename E, int D>
+__device__ __forceinline__ uint32_t pass_on_values(Shared<D>& sh, uint32_t stages, int first, int count, uint32_t phases, int mode, int slot) {
+  constexpr int ST = kPromptStages<D>;
+  constexpr uint32_t kStage = kKeys * D * 2;
+  const Bars<D> bar{smem_addr(sh.bars)};
+  const int lane = threadIdx.x & 31;
+  uint32_t met = 0u;
+  for (int t = 0; t < count; ++t) {
+    const int s = (2 * (first + t) + 1) % ST;
+    if (!mbar_wait(bar.landed(s), (phases >> s) & 1u) || *static_cast<volatile int*>(&sh.abort)) return kLostPhase;
+    phases ^= 1u << s;
+    met |= filter_values<E>(stages + s * kStage, kStage, mode, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.full(s));
+  }
+  if (mode == kWithout && met) note_met(smem_addr(&sh.met[slot]), met);
+  __syncwarp();
+  return phases;
+}
+
+// How far a softmax warp is: its unit, tiles and blocks of its row tile done, meetings of
+// both warpgroups; `again`: the unit is one that runs once more.
+struct SoftmaxPlace {
+  int nu, tiles, blocks;
+  uint32_t meets;
+  bool again, lost;
+};
+
+// The softmax warps' work on units from at.nu on: to the first that runs once more, or
+// (AGAIN) all that follow.
+template <typename E, int D, bool PAIR, bool AGAIN>
+__device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& sh, uint32_t base, SoftmaxPlace& at) {
+  constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
+  const uint32_t sOut = base + (QB * 2 + ST) * kRows * D * 2, sPart = base, sLse = sOut + 7 * 4096 + 1024;
+  const Bars<D> bar{smem_addr(sh.bars)};
+  const int shift_g = p.shift_g, per_tile = kRows >> shift_g;
+  const long long tok_stride = static_cast<long long>(p.Hq) * D;
+  auto t_scores = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
+  auto t_out = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
+  // (read anew: kept from the kernel's beginning they would be spilled here)
+  int tid;
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+  const int lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t tmem = sh.tmem;
+  const int m = warp >> 2;
+  const int r = tid & (kRows - 1);  // row of the tile = lane of tensor memory
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  const float NEG_INF = __int_as_float(0xff800000);
+  int tiles = at.tiles, blocks = at.blocks, nu = at.nu;
+  uint32_t meets = at.meets;
+  bool lost = false;
+  auto meet = [&]() {  // of both warpgroups; sets `lost` if the other does not come
+    mbar_arrive(bar.met());
+    lost = lost || !mbar_wait(bar.met(), meets & 1);
+    ++meets;
+  };
+  for (; !lost && sh.next(nu, lost, lane); ++nu) {
+    const Unit& blk = sh.units[nu % kSlots];  // (not released before the block is done)
+    if (blk.k0 == blk.soft) {
+      if (!AGAIN && blk.mode != kPlain) {
+        at.again = true;
+        break;
+      }
+      if (blk.k0 == blk.k1 || blk.mode > kWithout) {
+        if (AGAIN && blk.mode > kWithout) {
+          const int done = look_at_values<E, D, PAIR>(p, blk, tiles, blocks, sh.tmem, bar.s_full(0), sOut);
+          lost = done < 0;
+          tiles += done;
+          ++blocks;
+          if constexpr (PAIR) meet();  // both have read the accumulators
+          if (lost) break;
+        } else if (p.splits > 1 && blk.count > 0) {  // (a cluster's CTA without a share has nothing to add)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + tid * 4), "f"(NEG_INF) : "memory");
+        }
+        sh.release(nu, lane);
+        continue;
+      }
+    }
+    const int mq = PAIR ? 0 : m, token = mq * per_tile + (r >> shift_g);
+    const int last = blk.slot + blk.ntok - 1;
+    const int i = min(blk.slot + token, last);
+    const int f = blk.slot + mq * per_tile;                // first and last query of the tile
+    const int e = min(last, f + per_tile - 1);
+    const Tiles sees = tiles_of(p, blk, mq);  // (as the products' warp has them)
+    float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
+    float2 sum2 = make_float2(0.f, 0.f);
+    int n = 0;
+    for (int k = blk.k0; k < blk.k1; ++k) {
+      if (PAIR ? ((k - blk.k0) & 1) != m : !sees.has(k)) continue;  // not this row tile's
+      // which keys this row sees, found while the scores are on their way
+      const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
+      const bool edge = (k << (7 - p.shift_box)) < blk.sink_boxes || cols.base + kKeys - 1 > f || cols.base <= e - p.window;
+      uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+      if (edge) {
+        // sinks, or an edge of the causal mask or of the window
+#pragma unroll
+        for (int c = 0; c < 4; ++c) vis[c] = visible_of(cols, c * 32, i, p.window, p.sinks);
+      }
+      if (!mbar_wait(bar.s_full(m), tiles & 1)) {
+        lost = true;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sc[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(tmem, m) + lanes + c * 32, sc[c]);
+      tmem_wait_ld();
+      if constexpr (AGAIN) {  // a visible score of -inf, whose weight is 0
+        bool none = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int x = 0; x < 32; ++x) none = none || (sc[c][x] == 0xff800000u && (vis[c] & (1u << x)));
+        if (none && blk.mode == kWithout && token < blk.ntok) note_met(smem_addr(&sh.met[nu % kSlots]), 1u << (kNoWeight - 1));
+      }
+      if (edge) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (__all_sync(0xffffffffu, vis[c] == 0xffffffffu)) continue;
+#pragma unroll
+          for (int x = 0; x < 32; ++x) sc[c][x] = (vis[c] & (1u << x)) ? sc[c][x] : 0xff800000u;
+        }
+      }
+      float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+      for (int x = 0; x < 32; x += 2)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], __uint_as_float(sc[c][x]), __uint_as_float(sc[c][x + 1]));
+      const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+      if (n == 0) {
+        top = now;
+      } else if (__any_sync(0xffffffffu, now > top + kGrow)) {
+        // the products of the earlier key tiles are complete (the scores' commit
+        // came after theirs), and the next waits for this tile's weights
+        const float to = fmaxf(top, now);
+        const float by = exp2f(top - (to == NEG_INF ? 0.f : to));
+#pragma unroll 1
+        for (int c = 0; c < D; c += 8) {
+          uint32_t o[8];
+          tmem_ld8(t_out(tmem, m) + lanes + c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+          tmem_st8(t_out(tmem, m) + lanes + c, o);
+        }
+        sum2.x *= by;
+        sum2.y *= by;
+        top = to;
+      }
+      const float shift = top == NEG_INF ? 0.f : -top;
+      const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[32];
+        float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int x = 0; x < 32; ++x) {
+          const int c = 2 * half + (x >> 4), y = 2 * (x & 15);
+          const float2 a = ffma2(make_float2(__uint_as_float(sc[c][y]), __uint_as_float(sc[c][y + 1])), scale2, shift2);
+          const float2 v = make_float2(exp2f(a.x), exp2f(a.y));
+          add[x & 1] = fadd2(add[x & 1], v);
+          w[x] = E::pack2(v.x, v.y);
+        }
+        sum2 = fadd2(sum2, fadd2(add[0], add[1]));
+        tmem_st32(t_scores(tmem, m) + lanes + half * 32, w);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(bar.p_full(m, half));
+      }
+      ++n;
+      ++tiles;
+    }
+    float sum = sum2.x + sum2.y;
+    if (lost || !mbar_wait(bar.o_full(m), blocks & 1) || ((PAIR || p.splits > 1) && !mbar_wait(bar.o_full(m ^ 1), blocks & 1))) {
+      lost = true;
+      break;
+    }
+    if (lane == 0) mbar_arrive(bar.o_seen(m));
+    ++blocks;
+    tc_fence_after();
+    // The row's output is w0 O_0 + w1 O_1 (the accumulators of both warpgroups, who
+    // tell each other their sums) for a pair, which shares the columns between the
+    // warpgroups, and O_m / sum otherwise.  A warpgroup that saw no key of a row
+    // has sum 0, and what its accumulator holds does not count.
+    const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
+    float w0 = sum == 0.f ? 0.f : 1.f / sum, w1 = 0.f;
+    float lse = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+    if constexpr (PAIR) {
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
+      meet();
+      float top1, sum1;
+      asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(top1), "=f"(sum1) : "r"(sOut + static_cast<uint32_t>(warp ^ 4) * 4096 + lane * 8));
+      meet();  // the staging space is used again below
+      if (lost) break;
+      if (m == 1) {  // in the same order on both sides
+        const float t = top, u = sum;
+        top = top1;
+        sum = sum1;
+        top1 = t;
+        sum1 = u;
+      }
+      const float both = fmaxf(top, top1), shift = both == NEG_INF ? 0.f : both;
+      const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
+      const float all = a * sum + b * sum1;
+      lse = all > 0.f ? both + log2f(all) : (all == 0.f ? NEG_INF : all);
+      w0 = sum == 0.f ? 0.f : at_least_tiny(a / all);
+      w1 = sum1 == 0.f ? 0.f : at_least_tiny(b / all);
+    }
+    // 64 columns at a time: c0 is the first
+    float2 probe = make_float2(0.f, 0.f);  // becomes NaN with any output that is NaN or infinite
+    auto load = [&](int c0, uint32_t (&o)[64]) {
+      const uint32_t src = t_out(tmem, mq);
+      uint32_t x[32], y[32];
+      tmem_ld32(src + lanes + c0, x);
+      tmem_ld32(src + lanes + c0 + 32, y);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 64; ++i) {
+        const uint32_t v = i < 32 ? x[i] : y[i - 32];
+        o[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(v) * w0);
+      }
+      if constexpr (PAIR) {
+        tmem_ld32(t_out(tmem, 1) + lanes + c0, x);
+        tmem_ld32(t_out(tmem, 1) + lanes + c0 + 32, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          const uint32_t v = i < 32 ? x[i] : y[i - 32];
+          o[i] = w1 == 0.f ? o[i] : __float_as_uint(fmaf(__uint_as_float(v), w1, __uint_as_float(o[i])));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 64; i += 2)
+        probe = ffma2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), make_float2(0.f, 0.f), probe);
+    };
+    const int c_begin = PAIR ? 64 * m : 0, c_end = PAIR ? min(D, 64 * m + 64) : D;
+    const int part_row = mq * kRows + r;
+    // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
+    // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
+    // lines each.  (Those of a cluster stay in shared memory, in fp32.)
+    uint16_t* dst = p.out + (blk.first + mq * per_tile) * tok_stride + static_cast<long long>(blk.h) * p.G * D + (lane & 7) * 8;
+    const int row0 = (warp & 3) * 32 + (lane >> 3);  // this lane's rows: row0 + 4 x
+    dst += (row0 >> shift_g) * tok_stride + (row0 & (p.G - 1)) * D;
+    const int left = ((blk.ntok - mq * per_tile) << shift_g) - row0;
+    for (int c0 = c_begin; c0 < c_end; c0 += 64) {
+      uint32_t o[64];
+      load(c0, o);
+      if (p.splits > 1) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPart + part_off<D>(part_row, c0 / 4 + x)),
+                       "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
+                       : "memory");
+        if (AGAIN && blk.mode != kPlain) settle_part<D>(sPart, part_row, c0, stage + 2048 + lane * 4, blk.settle != 0);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          uint32_t w[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            w[y] = E::pack2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[0]), "r"(w[1]),
+                       "r"(w[2]), "r"(w[3])
+                       : "memory");
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          uint4 v;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                       : "r"(stage + swz128(4 * x + (lane >> 3), lane & 7)));
+          // (row0 has no bits that 4 x has: the two offsets add up)
+          if (4 * x < left)
+            *reinterpret_cast<uint4*>(dst + ((4 * x) >> shift_g) * tok_stride + ((4 * x) & (p.G - 1)) * D + c0) = v;
+        }
+        __syncwarp();
+      }
+    }
+    if (p.splits > 1 && (!PAIR || m == 0)) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + part_row * 4), "f"(lse) : "memory");
+    // an output that is no number, in a row whose sum is one: it may come from a value that the row does not see
+    if (probe.x + probe.y != 0.f && lse > NEG_INF && token < blk.ntok && (!AGAIN || blk.mode == kPlain))
+      note_met(smem_addr(&sh.met[nu % kSlots]), 1u);
+    if (p.splits > 1) fence_proxy_async_smem();  // (what was left, before the copies of a run that follows)
+    if constexpr (PAIR) {
+      meet();  // both have read the accumulators
+      if (lost) break;
+    }
+    sh.release(nu, lane);
+  }
+  at.nu = nu;
+  at.tiles = tiles;
+  at.blocks = blocks;
+  at.meets = meets;
+  at.lost = lost;
+}
+
+// The same from a unit that runs once more on, out of line.
+template <typename E, int D, bool PAIR>
+__device__ __noinline__ bool softmax_again(const PromptParams& p, Shared<D>& sh, uint32_t base, int nu, int tiles, int blocks,
+                                           uint32_t meets) {
+  SoftmaxPlace at{nu, tiles, blocks, meets, false, false};
+  softmax_units<E, D, PAIR, true>(p, sh, base, at);
+  return at.lost;
 }
 
 template <typename E, int D, bool PAIR>
@@ -291,11 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   constexpr uint32_t kScores = tc_kind_f16(kRows, kKeys, !E::kF16, false);
   constexpr uint32_t kValues = tc_kind_f16(kRows, D, !E::kF16, true);
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ Unit s_units[kSlots];
-  __shared__ uint64_t s_bars[2 * ST + 2 * QB + 11 + 2 * kSlots];
-  __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
-  __shared__ uint32_t s_again[8];  // rows of a softmax warp that ended with a NaN (PAIR)
+  __shared__ Shared<D> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int shift_g = p.shift_g, per_tile = kRows >> shift_g;  // tokens of a row tile
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
@@ -304,24 +819,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   const uint32_t sQ = base, sKV = base + QB * 2 * kQTile, sOut = sKV + ST * kStage;
   // partial results of a CTA in a cluster, over the queries and stages, and beside them
   const uint32_t sPart = base, sLse = sOut + 7 * 4096 + 1024;  // (behind what the last warp stages)
-  const uint32_t bars = smem_addr(s_bars);
-  auto full = [&](int s) { return bars + 8 * s; };
-  auto empty = [&](int s) { return bars + 8 * (ST + s); };
-  auto q_full = [&](int b) { return bars + 8 * (2 * ST + b); };
-  auto q_empty = [&](int b) { return bars + 8 * (2 * ST + QB + b); };
-  auto s_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + m); };
-  auto p_full = [&](int m, int half) { return bars + 8 * (2 * ST + 2 * QB + 2 + 2 * m + half); };
-  auto o_full = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 6 + m); };
-  auto o_seen = [&](int m) { return bars + 8 * (2 * ST + 2 * QB + 8 + m); };
-  const uint32_t met = bars + 8 * (2 * ST + 2 * QB + 10);  // both softmax warpgroups
-  auto u_full = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 11 + s); };
-  auto u_empty = [&](int s) { return bars + 8 * (2 * ST + 2 * QB + 11 + kSlots + s); };
-  volatile int* abort_flag = &s_abort;
+  const Bars<D> bar{smem_addr(sh.bars)};
+  auto full = [&](int s) { return bar.full(s); };
+  auto empty = [&](int s) { return bar.empty(s); };
+  auto q_full = [&](int b) { return bar.q_full(b); };
+  auto q_empty = [&](int b) { return bar.q_empty(b); };
+  auto s_full = [&](int m) { return bar.s_full(m); };
+  auto p_full = [&](int m, int half) { return bar.p_full(m, half); };
+  auto o_full = [&](int m) { return bar.o_full(m); };
+  auto o_seen = [&](int m) { return bar.o_seen(m); };
+  auto u_full = [&](int s) { return bar.u_full(s); };
+  auto u_empty = [&](int s) { return bar.u_empty(s); };
+  volatile int* abort_flag = &sh.abort;
   if (tid == 0) {
-    s_abort = 0;
+    sh.abort = 0;
+    for (int x = 0; x < kSlots; ++x) {
+      sh.units[x].more = 0;
+      sh.met[x] = 0;
+    }
     for (int s = 0; s < ST; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
+      mbar_init(bar.landed(s), 1);
     }
     for (int b = 0; b < QB; ++b) {
       mbar_init(q_full(b), 1);
@@ -334,32 +853,23 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       mbar_init(o_full(m), 1);
       mbar_init(o_seen(m), 4);
     }
-    mbar_init(met, 2 * kRows);
+    mbar_init(bar.met(), 2 * kRows);
     for (int x = 0; x < kSlots; ++x) {
       mbar_init(u_full(x), 1);
       mbar_init(u_empty(x), 11);  // every warp but the drawing one
     }
     fence_barrier_init();
   }
-  if (warp == kProductWarp) tmem_alloc(smem_addr(&s_tmem), kTmem);
+  if (warp == kProductWarp) tmem_alloc(smem_addr(&sh.tmem), kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   pdl_begin();
-  auto t_scores = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(m * kKeys); };
-  auto t_out = [](uint32_t tmem, int m) { return tmem + static_cast<uint32_t>(2 * kKeys + m * D); };
-  // waits for unit number n of this CTA; false: the CTA is done (or gives up)
-  auto next_unit = [&](int n, bool& lost) -> bool {
-    lost = !mbar_wait(u_full(n % kSlots), (n / kSlots) & 1);
-    return !lost && s_units[n % kSlots].more != 0;
-  };
-  auto release_unit = [&](int n) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(u_empty(n % kSlots));
-  };
+  auto release_unit = [&](int n) { sh.release(n, lane); };
   auto give_up = [&]() {
     if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
     *abort_flag = 1;
+    __syncwarp();
   };
 
   if (warp >= kProductWarp) {
@@ -369,21 +879,73 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       // ======================= the CTA's next unit =====================================
       // The first is the CTA's own number; the others come from the counter, which
       // the last draw of all sets back for the next call.  A cluster has one unit a CTA.
+      // A unit that has to run once more does so in its slot, before the slot is given
+      // to another.  In those runs this warp takes V from the copies, and passes it on
+      // filtered.
       Rows rows{};
       if (p.B <= 32) rows = rows_of(p, lane);
       const int units = p.blocks * p.Hkv * p.splits;
       int u = blockIdx.x;
+      uint32_t kinds[kSlots] = {};  // modes that the slot's unit has still to run in, as bits
+      bool lost = false;
+      int tiles = 0;                // of V copied for the units published so far
+      uint32_t landings = 0u;       // phases of the stages' barriers
       for (int n = 0;; ++n) {
-        if (n >= kSlots && !mbar_wait(u_empty(n % kSlots), ((n / kSlots) - 1) & 1)) {
-          give_up();
-          break;
+        Unit& slot = sh.units[n % kSlots];
+        int mode = kPlain;
+        if (n >= kSlots) {
+          lost = !mbar_wait(u_empty(n % kSlots), ((n / kSlots) - 1) & 1);
+          if (lost) break;
+          __syncwarp();
+          const uint32_t met = static_cast<uint32_t>(*reinterpret_cast<volatile int*>(&sh.met[n % kSlots]));
+          uint32_t todo = n % kSlots ? kinds[1] : kinds[0];
+          if (slot.mode == kPlain) {
+            if (met & 1u) mode = kWithout;
+          } else {
+            if (slot.mode == kWithout && !slot.settle) {
+              todo = met & 6u ? met : met & 8u;
+              if (todo && p.splits > 1) todo |= 1u << (kSettle - 1);
+            }
+            if (todo) mode = __ffs(todo);
+            todo &= todo - 1u;
+          }
+          if (n % kSlots) kinds[1] = todo;
+          else kinds[0] = todo;
+          __syncwarp();
+          if (lane == 0) sh.met[n % kSlots] = 0;
         }
         Unit x{};
-        if (u < units) x = unit_of(p, rows, u, lane);
-        if (lane == 0) s_units[n % kSlots] = x;
+        if (mode != kPlain) {
+          x = slot;
+          x.mode = mode == kSettle ? kWithout : mode;
+          x.settle = mode == kSettle;
+          x.soft = x.k0;
+        } else if (u < units) {
+          x = unit_of(p, rows, u, lane);
+          x.soft = x.k1;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          slot = x;
+          if (n == 0) sh.join = x;
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(u_full(n % kSlots));
-        if (u >= units || *abort_flag) break;
+        if (!x.more) {
+          if (sh.all_done()) break;
+          lost = !mbar_wait(u_empty(n % kSlots), (n / kSlots) & 1);
+          if (lost) break;
+          continue;
+        }
+        lost = *abort_flag != 0;
+        if (lost) break;
+        if (x.mode != kPlain) {
+          landings = pass_on_values<E, D>(sh, sKV, tiles, x.k1 - x.k0, landings, x.mode, n % kSlots);
+          lost = landings == kLostPhase;
+          if (lost) break;
+        }
+        tiles += x.k1 - x.k0;
+        if (mode != kPlain || u >= units) continue;
         if (p.splits > 1) {
           u = units;
         } else {
@@ -394,6 +956,10 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           }
           u = __shfl_sync(0xffffffffu, u, 0);
         }
+      }
+      if (lost) {
+        give_up();
+        named_sync(1, kThreads);
       }
     } else
     if (warp == kCopyWarp || warp == kCopyWarp + 1) {
@@ -408,10 +974,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       const int nbox = kKeys / p.box;
       int issued = kv, nq = 0;  // number in the ring, blocks of queries
       bool lost = false;
-      for (int n = 0; !lost && next_unit(n, lost); ++n) {
-        const Unit u = s_units[n % kSlots];
+      for (int n = 0; !lost && sh.next(n, lost, lane); ++n) {
+        const Unit u = sh.units[n % kSlots];
         release_unit(n);
         if (u.k0 == u.k1) continue;
+        // (the drawing warp passes on V of a unit that runs once more)
+        const uint32_t done0 = kv == 1 && u.mode != kPlain ? bar.landed(0) : full(0);
         for (int k = u.k0; k < u.k1 && !lost; ++k, issued += 2) {
           // page and first token of this lane's box (at most 16 boxes a tile)
           int page = p.num_pages, tok = 0;
@@ -432,14 +1000,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             lost = true;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(full(s), kStage);
+          const uint32_t done = done0 + 8 * s;
+          if (leader) mbar_arrive_expect_tx(done, kStage);
           for (int x = 0; x < nbox; ++x) {
             const int pg = __shfl_sync(0xffffffffu, page, x), tk = __shfl_sync(0xffffffffu, tok, x);
             if (leader) {
               const int c1 = p.tm_tok_dim == 1 ? tk : u.h, c2 = p.tm_tok_dim == 1 ? u.h : tk;
               const uint32_t dst = sKV + s * kStage + x * p.box * 128;
 #pragma unroll
-              for (int hf = 0; hf < HALVES; ++hf) tma_load_4d(dst + hf * kBlockBytes, map, hf * 64, c1, c2, pg, full(s));
+              for (int hf = 0; hf < HALVES; ++hf) tma_load_4d(dst + hf * kBlockBytes, map, hf * 64, c1, c2, pg, done);
             }
           }
           if (k == u.k0 && kv == 0) {
@@ -468,6 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
         for (int x = max(kv, issued - 2 * ST); x < issued; x += 2)
           if (x + ST >= issued) (void)mbar_wait(full(x % ST), (x / ST) & 1);
         for (int x = max(0, nq - QB); x < nq; ++x) (void)mbar_wait(q_full(x % QB), (x / QB) & 1);
+        named_sync(1, kThreads);
       }
     } else if (warp == kProductWarp) {
       // ======================= products =============================================
@@ -476,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       // warp stays together: a wait that ran out is noted and acted on once a tile
       // (what is multiplied until then is garbage in this CTA's own memory).
       const uint32_t issue = leader ? 1u : 0u;
-      const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
+      const uint32_t tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
       uint32_t ki = 0, kp = 0, vi = 1, vp = 0;  // ring place and phase of the next K and V
       auto next = [&](uint32_t& i, uint32_t& ph) {
         i += 2;
@@ -491,11 +1061,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       auto wait = [&](uint32_t bar, uint32_t parity) { ran_out |= !mbar_wait(bar, parity); };
       bool lost = false;
       const uint32_t k_operand = tc_operand(sKV, 16), v_operand = tc_operand(sKV, kBlockBytes);
-      for (int n = 0;; ++n) {
+      int n = 0;
+      for (;;) {  // (a second time only where units run once more)
+      for (;; ++n) {
         wait(u_full(n % kSlots), (n / kSlots) & 1);
         lost = __any_sync(0xffffffffu, ran_out);
         auto field = [&](const int& x) { return __shfl_sync(0xffffffffu, x, 0); };  // (uniform, and known to be)
-        const Unit& from = s_units[n % kSlots];
+        const Unit& from = sh.units[n % kSlots];
         if (lost || field(from.more) == 0) break;
         Unit blk;
         blk.slot = field(from.slot);
@@ -638,277 +1210,37 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           }
         }
       }
+      if (lost || sh.all_done()) break;
+      release_unit(n);
+      ++n;
+      }
       if (lost) {
         give_up();
         // products in flight end before the tensor memory is freed (row tile 0's output
         // barrier serves for that; its softmax has given up or will)
         tc_commit(issue, o_full(0));
         for (int x = 0; x < 2; ++x) (void)mbar_wait(o_full(0), x);
+        named_sync(1, kThreads);
       }
     }
   } else {
     // ======================= softmax of row tile m =================================
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // (read anew: kept from the kernel's beginning they would be spilled here)
-    int tid;
-    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
-    const int lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const uint32_t tmem = s_tmem;
-    const int m = warp >> 2;
-    const int r = tid & (kRows - 1);  // row of the tile = lane of tensor memory
-    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float NEG_INF = __int_as_float(0xff800000);
-    int tiles = 0, blocks = 0;
-    uint32_t meets = 0;
-    bool lost = false;
-    auto meet = [&]() {  // of both warpgroups; sets `lost` if the other does not come
-      mbar_arrive(met);
-      lost = lost || !mbar_wait(met, meets & 1);
-      ++meets;
-    };
-    for (int nu = 0; !lost && next_unit(nu, lost); ++nu) {
-      const Unit& blk = s_units[nu % kSlots];  // (not released before the block is done)
-      if (blk.k0 == blk.k1) {
-        if (p.splits > 1 && blk.count > 0)  // (a cluster's CTA without a share has nothing to add)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + tid * 4), "f"(NEG_INF) : "memory");
-        release_unit(nu);
-        continue;
-      }
-      const int mq = PAIR ? 0 : m, token = mq * per_tile + (r >> shift_g);
-      const int last = blk.slot + blk.ntok - 1;
-      const int i = min(blk.slot + token, last);
-      const int f = blk.slot + mq * per_tile;                // first and last query of the tile
-      const int e = min(last, f + per_tile - 1);
-      // the key tiles that the row tile sees (as the products' warp has it)
-      const int shift_tile = 7 - p.shift_box, to = blk.sink_boxes + (e >> p.shift_box) - blk.from;
-      const int s_end = f > last ? 0 : min((blk.sink_boxes + (1 << shift_tile) - 1) >> shift_tile, (e >> 7) + 1);
-      const int w_begin = (blk.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - blk.from)) >> shift_tile;
-      const int w_end = f > last || to < blk.sink_boxes ? 0 : (to >> shift_tile) + 1;
-      float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
-      float2 sum2 = make_float2(0.f, 0.f);
-      int n = 0;
-      for (int k = blk.k0; k < blk.k1; ++k) {
-        if (PAIR ? ((k - blk.k0) & 1) != m : !(k < s_end || (k >= w_begin && k < w_end))) continue;  // not this row tile's
-        // which keys this row sees, found while the scores are on their way
-        const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
-        const bool edge = (k << shift_tile) < blk.sink_boxes || cols.base + kKeys - 1 > f || cols.base <= e - p.window;
-        uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-        if (edge) {
-          // sinks, or an edge of the causal mask or of the window
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int jc = cols.base + c * 32;
-            vis[c] = visible32(i + 1 - jc, i - p.window + 1 - jc, p.sinks - jc);
-            if (cols.jump < kKeys) {
-              const int jg = jc + cols.gap;  // the word's first slot behind the jump
-              const uint32_t lead = below32(cols.jump - c * 32);
-              vis[c] = (vis[c] & lead) | (visible32(i + 1 - jg, i - p.window + 1 - jg, p.sinks - jg) & ~lead);
-            }
-          }
-        }
-        if (!mbar_wait(s_full(m), tiles & 1)) {
-          lost = true;
-          break;
-        }
-        tc_fence_after();
-        uint32_t sc[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_scores(tmem, m) + lanes + c * 32, sc[c]);
-        tmem_wait_ld();
-        if (edge) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (__all_sync(0xffffffffu, vis[c] == 0xffffffffu)) continue;
-#pragma unroll
-            for (int x = 0; x < 32; ++x) sc[c][x] = (vis[c] & (1u << x)) ? sc[c][x] : 0xff800000u;
-          }
-        }
-        float mx[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
-#pragma unroll
-        for (int x = 0; x < 32; x += 2)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = fmax3(mx[c], __uint_as_float(sc[c][x]), __uint_as_float(sc[c][x + 1]));
-        const float now = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        if (n == 0) {
-          top = now;
-        } else if (__any_sync(0xffffffffu, now > top + kGrow)) {
-          // the products of the earlier key tiles are complete (the scores' commit
-          // came after theirs), and the next waits for this tile's weights
-          const float to = fmaxf(top, now);
-          const float by = exp2f(top - (to == NEG_INF ? 0.f : to));
-#pragma unroll 1
-          for (int c = 0; c < D; c += 8) {
-            uint32_t o[8];
-            tmem_ld8(t_out(tmem, m) + lanes + c, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 8; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
-            tmem_st8(t_out(tmem, m) + lanes + c, o);
-          }
-          sum2.x *= by;
-          sum2.y *= by;
-          top = to;
-        }
-        const float shift = top == NEG_INF ? 0.f : -top;
-        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t w[32];
-          float2 add[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const int c = 2 * half + (x >> 4), y = 2 * (x & 15);
-            const float2 a = ffma2(make_float2(__uint_as_float(sc[c][y]), __uint_as_float(sc[c][y + 1])), scale2, shift2);
-            const float2 v = make_float2(exp2f(a.x), exp2f(a.y));
-            add[x & 1] = fadd2(add[x & 1], v);
-            w[x] = E::pack2(v.x, v.y);
-          }
-          sum2 = fadd2(sum2, fadd2(add[0], add[1]));
-          tmem_st32(t_scores(tmem, m) + lanes + half * 32, w);
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(p_full(m, half));
-        }
-        ++n;
-        ++tiles;
-      }
-      float sum = sum2.x + sum2.y;
-      if (lost || !mbar_wait(o_full(m), blocks & 1) || ((PAIR || p.splits > 1) && !mbar_wait(o_full(m ^ 1), blocks & 1))) {
-        lost = true;
-        break;
-      }
-      if (lane == 0) mbar_arrive(o_seen(m));
-      ++blocks;
-      tc_fence_after();
-      // The row's output is w0 O_0 + w1 O_1 (the accumulators of both warpgroups, who
-      // tell each other their sums) for a pair, which shares the columns between the
-      // warpgroups, and O_m / sum otherwise.  A warpgroup that saw no key of a row
-      // has sum 0, and what its accumulator holds does not count.
-      const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
-      float w0 = sum > 0.f || sum != sum ? 1.f / sum : 0.f, w1 = 0.f;
-      float lse = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
-      if constexpr (PAIR) {
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
-        meet();
-        float top1, sum1;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(top1), "=f"(sum1) : "r"(sOut + static_cast<uint32_t>(warp ^ 4) * 4096 + lane * 8));
-        meet();  // the staging space is used again below
-        if (lost) break;
-        if (m == 1) {  // in the same order on both sides
-          const float t = top, u = sum;
-          top = top1;
-          sum = sum1;
-          top1 = t;
-          sum1 = u;
-        }
-        const float both = fmaxf(top, top1), shift = both == NEG_INF ? 0.f : both;
-        const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
-        const float all = a * sum + b * sum1;
-        lse = all > 0.f ? both + log2f(all) : (all == 0.f ? NEG_INF : all);
-        const float inv = all > 0.f || all != all ? 1.f / all : 0.f;
-        w0 = a * inv;
-        w1 = b * inv;
-      }
-      // 64 columns at a time: c0 is the first
-      float2 probe = make_float2(0.f, 0.f);  // becomes NaN with any output that is NaN or infinite
-      auto load = [&](int c0, uint32_t (&o)[64]) {
-        const uint32_t src = t_out(tmem, mq);
-        uint32_t x[32], y[32];
-        tmem_ld32(src + lanes + c0, x);
-        tmem_ld32(src + lanes + c0 + 32, y);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 64; ++i) {
-          const uint32_t v = i < 32 ? x[i] : y[i - 32];
-          o[i] = w0 == 0.f ? 0u : __float_as_uint(__uint_as_float(v) * w0);
-        }
-        if constexpr (PAIR) {
-          tmem_ld32(t_out(tmem, 1) + lanes + c0, x);
-          tmem_ld32(t_out(tmem, 1) + lanes + c0 + 32, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            const uint32_t v = i < 32 ? x[i] : y[i - 32];
-            o[i] = w1 == 0.f ? o[i] : __float_as_uint(fmaf(__uint_as_float(v), w1, __uint_as_float(o[i])));
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 64; i += 2)
-          probe = ffma2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), make_float2(0.f, 0.f), probe);
-      };
-      const int c_begin = PAIR ? 64 * m : 0, c_end = PAIR ? min(D, 64 * m + 64) : D;
-      const int part_row = mq * kRows + r;
-      if (p.splits > 1) {
-        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
-          uint32_t o[64];
-          load(c0, o);
-#pragma unroll
-          for (int x = 0; x < 16; ++x)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sPart + part_off<D>(part_row, c0 / 4 + x)),
-                         "r"(o[4 * x]), "r"(o[4 * x + 1]), "r"(o[4 * x + 2]), "r"(o[4 * x + 3])
-                         : "memory");
-        }
-        if (!PAIR || m == 0) asm volatile("st.shared.f32 [%0], %1;" ::"r"(sLse + part_row * 4), "f"(lse) : "memory");
-      } else {
-        // The warp's 32 rows leave through 4 KB of shared memory, 128 bytes of each at
-        // a time: a thread holds a row, and stores of 16 bytes a row would touch 32
-        // lines each.
-        uint16_t* dst = p.out + (blk.first + mq * per_tile) * tok_stride + static_cast<long long>(blk.h) * p.G * D + (lane & 7) * 8;
-        const int row0 = (warp & 3) * 32 + (lane >> 3);  // this lane's rows: row0 + 4 x
-        dst += (row0 >> shift_g) * tok_stride + (row0 & (p.G - 1)) * D;
-        const int left = ((blk.ntok - mq * per_tile) << shift_g) - row0;
-        for (int c0 = c_begin; c0 < c_end; c0 += 64) {
-          uint32_t o[64];
-          load(c0, o);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              w[y] = E::pack2(__uint_as_float(o[8 * x + 2 * y]), __uint_as_float(o[8 * x + 2 * y + 1]));
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + swz128(lane, x)), "r"(w[0]), "r"(w[1]),
-                         "r"(w[2]), "r"(w[3])
-                         : "memory");
-          }
-          __syncwarp();
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint4 v;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(stage + swz128(4 * x + (lane >> 3), lane & 7)));
-            // (row0 has no bits that 4 x has: the two offsets add up)
-            if (4 * x < left)
-              *reinterpret_cast<uint4*>(dst + ((4 * x) >> shift_g) * tok_stride + ((4 * x) & (p.G - 1)) * D + c0) = v;
-          }
-          __syncwarp();
-        }
-      }
-      // Rows that ended with a NaN (or an infinity), once more over what they see alone.
-      const float probed = probe.x + probe.y;
-      uint32_t again = __ballot_sync(0xffffffffu, probed != probed && token < blk.ntok);
-      if constexpr (PAIR) {
-        // warpgroup 0 takes them for both halves of the columns, once both have read
-        // the accumulators and written what they have
-        if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&s_again[warp]) = again;
-        meet();
-        if (lost) break;
-        again |= *reinterpret_cast<volatile uint32_t*>(&s_again[warp ^ 4]);
-        if (m == 1) again = 0u;
-      }
-      if (again) attend_alone<E, D>(p, blk, mq, again, sPart, sLse);
-      release_unit(nu);
+    SoftmaxPlace at{};
+    softmax_units<E, D, PAIR, false>(p, sh, base, at);
+    if (at.again) at.lost = softmax_again<E, D, PAIR>(p, sh, base, at.nu, at.tiles, at.blocks, at.meets);
+    if (at.lost) {
+      give_up();
+      tc_fence_before();
+      named_sync(1, kThreads);
     }
-    if (lost) give_up();
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == kProductWarp) tmem_free(s_tmem, kTmem);
+  if (warp == kProductWarp) tmem_free(sh.tmem, kTmem);
   if (p.splits == 1) return;
 
   // ======================= the cluster's partial results ============================
   // (all CTAs of a cluster work on one block: they agree on whether there is one)
-  const Unit& u = s_units[0];
+  const Unit& u = sh.join;
   if (u.count == 0) return;
   cluster_sync();
   if (!*abort_flag) {
@@ -920,7 +1252,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       float top = lse;
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float w = exp2f(lse - (top == NEG_INF ? 0.f : top));
+      const float w = lse == NEG_INF ? 0.f : at_least_tiny(exp2f(lse - top));
       float sum = w;
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);

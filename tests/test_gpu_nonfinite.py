@@ -1,0 +1,159 @@
+"""Infinities and NaN in the cache under the windowed decode and the prompt
+attention, against float64: they have to reach the outputs whose queries see
+them, as they would in float64, and no others; and a call must stay about as fast."""
+import math
+import random
+import statistics
+
+import pytest
+import torch
+
+import test_gpu_window as W
+import window_batch as X
+import window_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+INF, NAN = math.inf, math.nan
+KINDS = {"inf": [INF], "minus": [-INF], "nan": [NAN], "both": [INF, -INF], "all": [INF, -INF, NAN]}
+
+
+def plant(r, which, values, count, seed, heads=None):
+    """`count` elements of K (0) or V (1), at slots that some query sees."""
+    rng = random.Random(seed)
+    x = r.view(r.pool, which)
+    rows = [b for b in range(r.B) if r.active[b] and r.news[b]]
+    for c in range(count):
+        b = rng.choice(rows)
+        j = rng.choice(r.seen(b))
+        x[int(r.table[b, j // r.P]), j % r.P, rng.randrange(r.Hkv), rng.randrange(r.D)] = values[c % len(values)]
+
+
+def column(r, b, j, head, value, dims=slice(None), which=1):
+    r.view(r.pool, which)[int(r.table[b, j // r.P]), j % r.P, head, dims] = value
+
+
+def check(r, decode, scale=0.0, **kw):
+    q = R.queries(r, torch.float32 if decode else r.pool.dtype)
+    out, err = (W.decode if decode else W.prompt)(r, q, scale=scale, **kw)
+    assert err == 0
+    ref = X.attention(r, q, scale)
+    bad = X.differs(out, ref, R.tolerance(ref, r.pool.dtype, r.D, decode, 8.0))
+    assert bad is None, bad
+    return out, ref
+
+
+# small blocks (128 rows), shares of the keys, and blocks of 256 rows (more than 152 of the small ones)
+PROMPTS = {
+    "causal": (dict(lens=[260, 31], news=[260, 31], Hq=4, Hkv=2), {}),
+    "window": (dict(lens=[300, 90], news=[200, 90], Hq=8, Hkv=2, window=40, sinks=5, P=48), {}),
+    "shared": (dict(lens=[1500, 700], news=[20, 3], Hq=8, Hkv=2, window=1100, sinks=10, P=8), dict(splits=4)),
+    "shared_all": (dict(lens=[900], news=[30], Hq=8, Hkv=1), dict(splits=2)),
+    "large": (dict(lens=[900, 800], news=[900, 740], Hq=16, Hkv=8, window=300, sinks=7), {}),
+    "large_all": (dict(lens=[700, 600, 300], news=[700, 600, 300], Hq=8, Hkv=8, P=64), {}),
+    "large_shared": (dict(lens=[900, 900], news=[800, 700], Hq=16, Hkv=8, window=500, sinks=130), dict(splits=2)),
+}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (64, FP), (128, FP)])
+@pytest.mark.parametrize("shape", PROMPTS)
+def test_prompt_values(shape, D, dtype, kind):
+    make, call = PROMPTS[shape]
+    for seed, count in ((1, 1), (2, 7)):
+        r = R.make(**make, D=D, dtype=dtype, layout="HND" if seed == 2 else "NHD", seed=seed)
+        plant(r, 1, KINDS[kind], count, seed)
+        check(r, False, **call)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("shape", PROMPTS)
+def test_prompt_values_seen_by_all_some_and_none(shape, dtype):
+    """The first slot (all, or a sink, or nobody), the last (one query), and whole tokens of NaN."""
+    make, call = PROMPTS[shape]
+    for j in (0, -1, -17):
+        r = R.make(**make, dtype=dtype, seed=5)
+        seen = r.seen(0)
+        column(r, 0, seen[j], 0, INF, 3)
+        column(r, 0, seen[j], 1 % r.Hkv, NAN)
+        check(r, False, **call)
+
+
+@pytest.mark.parametrize("shape", PROMPTS)
+def test_prompt_keys_and_values(shape):
+    """One infinite element of a key: scores of +inf (NaN rows) and -inf (no weight), the latter also with an
+    infinite value; and weights far below the largest."""
+    make, call = PROMPTS[shape]
+    r = R.make(**make, seed=6)
+    plant(r, 0, [INF, -INF], 2, 6)
+    check(r, False, **call)
+    r = R.make(**make, seed=7)
+    j = r.seen(0)[len(r.seen(0)) // 2]
+    column(r, 0, j, 0, -INF, 5, which=0)
+    column(r, 0, j, 0, INF, 9)
+    plant(r, 1, [NAN, INF], 2, 7)
+    check(r, False, **call)
+    for dtype in (BF, FP):
+        r = R.make(**make, dtype=dtype, seed=8)
+        plant(r, 1, [INF, -INF, INF], 9, 8)
+        check(r, False, scale=0.7, **call)
+
+
+def test_prompt_bad_page_beside_an_infinity():
+    v = W.vh()
+    r = R.make([200, 40], [200, 40], Hq=4, Hkv=2, window=100, sinks=2, seed=12)
+    q = R.queries(r, BF)
+    plant(r, 1, [INF, NAN], 4, 3)
+    bad = R.Ragged(**{**r.__dict__, "table": r.table.clone()})
+    page = int(bad.table[0, 5])
+    bad.table[0, 5] = 1 << 28
+    out, err = W.prompt(bad, q)
+    assert err == v.VH_ERR_PAGE
+    r.pool[page] = 0
+    ref = X.attention(r, q)
+    assert X.differs(out, ref, R.tolerance(ref, BF, 128, False, 8.0)) is None
+
+
+def timed(call):
+    for _ in range(3):
+        call()
+    ms = []
+    for _ in range(7):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        torch.cuda.synchronize()
+        ms.append(a.elapsed_time(b))
+    return statistics.median(ms)
+
+
+@pytest.mark.parametrize("where", ["all", "some", "none"])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_time_with_a_bad_value(where, value):
+    """A value that is no number costs a block a second run and one for each kind of value, not a
+    run of its own for each query: within six times the time of finite values (and 50 us of start)."""
+    v = W.vh()
+    r = R.make([4160], [4096], Hq=16, Hkv=8, window=1024 if where == "none" else 0, seed=2)
+    g = W.on_gpu(r)
+    q = R.queries(r, BF).cuda()
+    out = torch.zeros_like(q)
+    ws = v.alloc_prompt_workspace(4096, 1, 16, 8, 128)
+    call = lambda: v.vh_window_prompt_attn(q, g["k"], g["v"], g["table"], g["starts"], g["lens"], g["active"], out, ws,  # noqa: E731
+                                           window=r.window, err_flag=g["err"])
+    plain = timed(call)
+    j = {"all": 3, "some": 2000, "none": 3000}[where]
+    g["v"][int(r.table[0, j // 16]), j % 16, :, 7] = value
+    bad = timed(call)
+    assert int(g["err"]) == 0 and not ws.any()
+    assert bad < 6 * plain + 0.05, f"{bad * 1e3:.0f} us against {plain * 1e3:.0f} us"
+
+
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_long_context_with_a_bad_value(value):
+    """No wait runs out over a context of 120,000 tokens, and a request beside it is served."""
+    lens, news = [120000, 500], [512, 300]
+    r = R.make(lens, news, Hq=8, Hkv=1, D=64, P=64, seed=4)
+    column(r, 0, 3, 0, value, 7)
+    column(r, 0, 119900, 0, value, 9)
+    check(r, False)
