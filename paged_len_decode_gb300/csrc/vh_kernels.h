@@ -18,6 +18,13 @@ constexpr int kPlanMagic = 0x56485031;
 constexpr int kPlanWindow = 64;
 constexpr int kPlanRecInts = 4 + 2 * kPlanWindow;
 
+// The K and V caches as memory (the kernels copy them through tensor maps).
+struct CacheMemory {
+  const uint16_t* k;
+  const uint16_t* v;
+  long long page_stride, token_stride, head_stride;  // elements
+};
+
 struct RopeAppendParams {
   const uint16_t* q;
   const uint16_t* k_new;

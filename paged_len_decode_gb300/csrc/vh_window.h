@@ -7,6 +7,8 @@
 #include <cuda.h>  // CUtensorMap (the type only)
 #include <cuda_runtime.h>
 
+#include "vh_kernels.h"
+
 namespace vh {
 
 // A window that never ends, for W = 0 (slots are below 2^24).
@@ -47,6 +49,7 @@ struct WindowDecodeParams {
   // heads, and of 8 tokens x 1 head
   CUtensorMap tmap_k, tmap_v, tmap_k8, tmap_v8;
   int tm_tok_dim, full_boxes;
+  CacheMemory memory;          // the same caches
   const float* q_rot;          // [B][Hq][D]
   int num_pages;
   const int32_t* page_table;   // null: contiguous cache

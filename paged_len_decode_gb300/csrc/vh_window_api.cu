@@ -374,6 +374,7 @@ int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e1
   p.tmap_v8 = a.tmap_v8;
   p.tm_tok_dim = a.tm_tok_dim;
   p.full_boxes = a.full_boxes;
+  p.memory = {k_cache, v_cache, page_stride, token_stride, head_stride};
   p.q_rot = q_rot;
   p.num_pages = num_pages;
   p.page_table = page_table;

@@ -22,6 +22,10 @@
 //    high part and a residual of the element type so that products keep 16
 //    bits of them (22 in fp16).  Keys outside V get -inf before the max, and
 //    their rows of V are zeroed in shared memory, so nothing they hold counts.
+//    Infinities that are seen make a NaN of a residual's product (0 times infinity,
+//    or infinities of both signs) that the definition does not have: a warp whose
+//    outputs come out as no numbers computes its share of the row once more, with
+//    plain products in fp32.
 //  * Merge: partial (o, lse) go to the workspace; a counter per row tells the
 //    last CTA to arrive, which adds the pieces in their order in the row, so
 //    the result does not depend on who is last.
@@ -99,6 +103,111 @@ __device__ __forceinline__ int row_of(const int* cum, int lo, int B, int t) {
     if (cum[mid + 1] > t) hi = mid; else lo = mid + 1;
   }
   return lo;
+}
+
+// Outputs of row b and kv head h from tiles k0 .. k1 - 1 of the row's list, by one warp and
+// without split operands, for rows whose outputs are no numbers: a key has a lane for each
+// half of its dimensions, then a lane has its columns of the values.  piece, lse: where the
+// partial outputs go, or null: the final ones go to p.out.  About four times the time of
+// the tiles' first pass; out of line, so that the common path keeps its registers.
+template <int D, int G, typename E>
+__device__ __noinline__ void plain_outputs(const WindowDecodeParams& p, int b, int h, int L, int k0, int k1, float* piece, float* lse) {
+  constexpr int PER = D / 32;
+  const float NEG_INF = __int_as_float(0xff800000);
+  const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
+  const RowTiles rt = tiles_of(L, p.window, p.sinks);
+  const long long row = (static_cast<long long>(b) * p.Hq + static_cast<long long>(h) * G) * D;
+  float o[G][PER], M[G], sum[G];
+#pragma unroll
+  for (int n = 0; n < G; ++n) {
+    M[n] = NEG_INF;
+    sum[n] = 0.f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) o[n][e] = 0.f;
+  }
+#pragma unroll 1
+  for (int k = k0; k < k1; ++k) {
+    const int tile = rt.tile(k);
+    const uint32_t mask = visible16(tile, L, p.window, p.sinks);
+    long long at[2];  // of the tile's halves (one page, but for pages of 8 tokens); -1: a page id out of range, read as zeros
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int j = tile * kTile + 8 * x;
+      at[x] = -1;
+      if (!(mask & (0xFFu << (8 * x)))) continue;
+      const long long lp = static_cast<long long>(b) * p.max_pages_per_seq + j / p.P;
+      const int page = p.page_table ? p.page_table[lp] : static_cast<int>(lp);
+      if (page >= 0 && page < p.num_pages)
+        at[x] = page * p.memory.page_stride + (j % p.P) * p.memory.token_stride + h * p.memory.head_stride;
+    }
+    // scores
+    float s[G];
+#pragma unroll
+    for (int n = 0; n < G; ++n) s[n] = 0.f;
+    const bool seen = (mask >> key) & 1u;
+    const long long mine = (key < 8 ? at[0] : at[1]) + (key & 7) * p.memory.token_stride;
+    if (seen && (key < 8 ? at[0] : at[1]) >= 0)
+#pragma unroll 1
+      for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p.memory.k + mine + d);
+        const float2 x = E::to_float2(w.x), y = E::to_float2(w.y);
+#pragma unroll
+        for (int n = 0; n < G; ++n) {
+          const float4 a = *reinterpret_cast<const float4*>(p.q_rot + row + n * D + d);
+          s[n] += a.x * x.x + a.y * x.y + a.z * y.x + a.w * y.y;
+        }
+      }
+#pragma unroll
+    for (int n = 0; n < G; ++n) {
+      s[n] += __shfl_xor_sync(0xffffffffu, s[n], 16);
+      s[n] = seen ? s[n] * p.scale_log2 : NEG_INF;
+      float mx = s[n];
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      mx = fmaxf(mx, M[n]);
+      const float ms = mx == NEG_INF ? 0.f : mx, by = at_least_tiny(exp2f(M[n] - ms));
+      M[n] = mx;
+      s[n] = s[n] == NEG_INF ? 0.f : at_least_tiny(exp2f(s[n] - ms));  // the weight
+      float add = s[n];
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
+      sum[n] = sum[n] * by + add;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) o[n][e] *= by;
+    }
+    // values
+#pragma unroll 1
+    for (int r = 0; r < kTile; ++r) {
+      if (!((mask >> r) & 1u)) continue;
+      const long long page = r < 8 ? at[0] : at[1];
+      float v[PER];
+#pragma unroll
+      for (int e = 0; e < PER; e += 2) {
+        const uint32_t w = page < 0 ? 0u : *reinterpret_cast<const uint32_t*>(p.memory.v + page + (r & 7) * p.memory.token_stride + lane * PER + e);
+        const float2 x = E::to_float2(w);
+        v[e] = x.x;
+        v[e + 1] = x.y;
+      }
+#pragma unroll
+      for (int n = 0; n < G; ++n) {
+        const float w = __shfl_sync(0xffffffffu, s[n], r);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) o[n][e] += w * v[e];
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < G; ++n) {
+    const float il = piece && sum[n] == 0.f ? 0.f : 1.f / sum[n];
+#pragma unroll
+    for (int e = 0; e < PER; e += 2) {
+      const int d = n * D + lane * PER + e;
+      if (piece) *reinterpret_cast<float2*>(piece + d) = make_float2(o[n][e] * il, o[n][e + 1] * il);
+      else *reinterpret_cast<uint32_t*>(p.out + row + d) = E::pack2(o[n][e] * il, o[n][e + 1] * il);
+    }
+    if (piece && lane == 0) lse[n] = M[n] + log2f(sum[n]);
+  }
+  __syncwarp();
 }
 
 template <int D, int G, typename E>
@@ -481,6 +590,14 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         L1 += __shfl_xor_sync(0xffffffffu, L1, off);
       }
       const int n0 = 2 * t4, n1 = 2 * t4 + 1;
+      float probe0 = 0.f, probe1 = 0.f;  // become NaN with an output that is no number
+#pragma unroll
+      for (int mt = 0; mt < KS; ++mt) {
+        probe0 += acc[mt][0] * 0.f + acc[mt][2] * 0.f;
+        probe1 += acc[mt][1] * 0.f + acc[mt][3] * 0.f;
+      }
+      const bool odd = (n0 < G && probe0 != 0.f) || (n1 < G && probe1 != 0.f);
+      float *piece = nullptr, *lse = nullptr;
       if (rt0 >= t0 && rt1 <= t1) {
         const float il0 = 1.f / L0, il1 = 1.f / L1;
         uint16_t* o0 = p.out + (static_cast<long long>(b) * p.Hq + static_cast<long long>(h) * G + n0) * D;
@@ -501,7 +618,9 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         // piece slot 0 of a CTA belongs to its first row, slot 1 to a later one
         const float il0 = L0 > 0.f ? 1.f / L0 : (L0 == 0.f ? 0.f : L0), il1 = L1 > 0.f ? 1.f / L1 : (L1 == 0.f ? 0.f : L1);
         const long long base = ((static_cast<long long>(gy) * p.N + c) * 2 + (b == b0 ? 0 : 1)) * HG + w * G;
-        float* o0 = p.part_o + (base + n0) * D;
+        piece = p.part_o + base * D;
+        lse = p.part_lse + base;
+        float* o0 = piece + n0 * D;
         float* o1 = o0 + D;
 #pragma unroll
         for (int mt = 0; mt < KS; ++mt) {
@@ -520,6 +639,17 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
           if (n1 < G) p.part_lse[base + n1] = m1 + log2f(L1);
         }
         part_row[npart++ & 1] = b;
+      }
+      if (__any_sync(0xffffffffu, odd)) {
+        __syncwarp();
+        plain_outputs<D, G, E>(p, b, h, lens[b], max(t0, rt0) - rt0, t + 1 - rt0, piece, lse);
+        // (the next row sets these anew: nothing of them is kept over the call)
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          qh[k][0] = qh[k][1] = ql[k][0] = ql[k][1] = 0u;
+          acc[k][0] = acc[k][1] = acc[k][2] = acc[k][3] = 0.f;
+        }
+        m0 = m1 = l0 = l1 = 0.f;
       }
     }
   }
@@ -578,9 +708,9 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
         for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         mx = fmaxf(mx, M[n]);
         const float ms = mx == NEG_INF ? 0.f : mx;
-        const float sc = exp2f(M[n] - ms);
+        const float sc = at_least_tiny(exp2f(M[n] - ms));
         M[n] = mx;
-        wt[n] = exp2f(lse - ms);
+        wt[n] = lse == NEG_INF ? 0.f : at_least_tiny(exp2f(lse - ms));
         float add = wt[n];
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);

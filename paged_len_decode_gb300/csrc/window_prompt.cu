@@ -678,7 +678,10 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     // warpgroups, and O_m / sum otherwise.  A warpgroup that saw no key of a row
     // has sum 0, and what its accumulator holds does not count.
     const uint32_t stage = sOut + static_cast<uint32_t>(warp) * 4096;
-    float w0 = sum == 0.f ? 0.f : 1.f / sum, w1 = 0.f;
+    // A live row without weight, whose visible scores are all -inf, is NaN; a share of
+    // its keys without weight adds nothing.
+    const float none = p.splits == 1 && token < blk.ntok ? __int_as_float(0x7fffffff) : 0.f;
+    float w0 = sum == 0.f ? none : 1.f / sum, w1 = 0.f;
     float lse = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
     if constexpr (PAIR) {
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
@@ -698,7 +701,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
       const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
       const float all = a * sum + b * sum1;
       lse = all > 0.f ? both + log2f(all) : (all == 0.f ? NEG_INF : all);
-      w0 = sum == 0.f ? 0.f : at_least_tiny(a / all);
+      w0 = all == 0.f ? none : (sum == 0.f ? 0.f : at_least_tiny(a / all));
       w1 = sum1 == 0.f ? 0.f : at_least_tiny(b / all);
     }
     // 64 columns at a time: c0 is the first

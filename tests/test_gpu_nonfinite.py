@@ -114,6 +114,30 @@ def test_prompt_bad_page_beside_an_infinity():
     assert X.differs(out, ref, R.tolerance(ref, BF, 128, False, 8.0)) is None
 
 
+@pytest.mark.parametrize("large", [False, True])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_rows_whose_scores_are_all_minus_infinity(splits, large):
+    """NaN, whichever way the keys are shared, in the prompt as in the decode."""
+    lens = [700, 900] if large else [90]
+    r = R.make(lens, lens, Hq=16 if large else 4, Hkv=8 if large else 2, window=1, seed=3)
+    q = R.queries(r, BF)
+    q[..., 5] = 1.0
+    for j in (7, 80):
+        column(r, 0, j, 1, -INF, 5, which=0)
+    ref = X.attention(r, q)
+    assert torch.isnan(ref[0]).any() and not torch.isnan(ref[0]).all()
+    out, err = W.prompt(r, q, splits=splits)
+    assert err == 0 and X.differs(out, ref, R.tolerance(ref, BF, 128, False, 8.0)) is None
+    if not large:
+        d = R.make([90, 8], [1, 1], Hq=4, Hkv=2, window=1, seed=4)
+        qd = R.queries(d, torch.float32)
+        qd[..., 5] = 1.0
+        column(d, 1, 7, 0, -INF, 5, which=0)
+        ref = X.attention(d, qd)
+        out, err = W.decode(d, qd)
+        assert err == 0 and X.differs(out, ref, R.tolerance(ref, BF, 128, True, 8.0)) is None
+
+
 def timed(call):
     for _ in range(3):
         call()
