@@ -67,6 +67,10 @@ constexpr int kThreads = 384;    // two softmax warpgroups, and one whose warps 
 constexpr int kProductWarp = 8, kCopyWarp = 9, kDrawWarp = 11;  // the copy warp takes K and the queries, the next one V
 constexpr int kSlots = 2;        // blocks drawn: this one and the next
 constexpr float kGrow = 8.f;     // log2 of the growth that rescales
+// log2 of the weight of the row's maximum: fp16 weights stay below 2^15 then, and those down to
+// 2^-32 of the largest count (at 2^-24 the type's range would end).  bf16 has fp32's range.
+template <typename E>
+constexpr float kLift = E::kF16 ? 7.f : 0.f;
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
 // What a block is run for: its outputs; and where some of them are no numbers, its
@@ -642,7 +646,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
         sum2.y *= by;
         top = to;
       }
-      const float shift = top == NEG_INF ? 0.f : -top;
+      const float shift = top == NEG_INF ? 0.f : kLift<E> - top;
       const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -682,7 +686,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     // its keys without weight adds nothing.
     const float none = p.splits == 1 && token < blk.ntok ? __int_as_float(0x7fffffff) : 0.f;
     float w0 = sum == 0.f ? none : 1.f / sum, w1 = 0.f;
-    float lse = sum > 0.f ? top + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+    float lse = sum > 0.f ? top - kLift<E> + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
     if constexpr (PAIR) {
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
       meet();
@@ -700,7 +704,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
       const float both = fmaxf(top, top1), shift = both == NEG_INF ? 0.f : both;
       const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
       const float all = a * sum + b * sum1;
-      lse = all > 0.f ? both + log2f(all) : (all == 0.f ? NEG_INF : all);
+      lse = all > 0.f ? both - kLift<E> + log2f(all) : (all == 0.f ? NEG_INF : all);
       w0 = all == 0.f ? none : (sum == 0.f ? 0.f : at_least_tiny(a / all));
       w1 = sum1 == 0.f ? 0.f : at_least_tiny(b / all);
     }

@@ -138,6 +138,28 @@ def test_rows_whose_scores_are_all_minus_infinity(splits, large):
         assert err == 0 and X.differs(out, ref, R.tolerance(ref, BF, 128, True, 8.0)) is None
 
 
+def test_small_fp16_weights_count():
+    """One key far above the others, each of which has 2^-27 of its weight: 4000 of them count together.  fp16
+    weights are at least 2^7 at a row's maximum, so one loses at most 2^-25 2^-7 = 2^-32 of it.  (One CTA a block:
+    a share of the keys without the first would have a maximum of its own.)"""
+    lens, D = [4000], 64
+    r = R.make(lens, [70], Hq=2, Hkv=1, D=D, dtype=FP, seed=2)
+    k, v = r.view(r.pool, 0), r.view(r.pool, 1)
+    k.zero_()
+    v.fill_(1.0)
+    column(r, 0, 0, 0, 18.75, 0, which=0)
+    column(r, 0, 0, 0, 0.0)
+    q = torch.zeros(70, 2, D, dtype=FP)
+    q[..., 0] = 1.0
+    out, err = W.prompt(r, q, scale=1.0, splits=1)
+    ref = X.attention(r, q, 1.0)
+    o, A, a, n = ref
+    half = 2.0 ** -11
+    tol = half * o.abs() + A * (2 * (a * (D + 4) * 2.0 ** -23 + 2.0 ** -20) + half + n * 2.0 ** -23) * (1 + half) + 2.0 ** -25 + n * 2.0 ** -32
+    assert (ref[0] > 20 * tol).all()      # weights lost would show
+    assert err == 0 and X.differs(out, ref, tol) is None
+
+
 def timed(call):
     for _ in range(3):
         call()
