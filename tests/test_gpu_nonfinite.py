@@ -138,6 +138,49 @@ def test_rows_whose_scores_are_all_minus_infinity(splits, large):
         assert err == 0 and X.differs(out, ref, R.tolerance(ref, BF, 128, True, 8.0)) is None
 
 
+DECODES = {
+    "rows": (dict(lens=[1, 2, 15, 16, 17, 333, 90], Hq=16, Hkv=8, window=64, sinks=5, P=8), {}),
+    "whole": (dict(lens=[333, 90, 12], Hq=8, Hkv=2, P=48), dict(num_ctas=1)),
+    "split": (dict(lens=[900, 3, 411], Hq=8, Hkv=4, window=700, sinks=20), dict(num_ctas=40)),
+    "one_head": (dict(lens=[3000, 17], Hq=8, Hkv=1, window=2500, sinks=40), {}),
+    "three": (dict(lens=[700, 60], Hq=3, Hkv=3, P=64), dict(num_ctas=7)),
+}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,dtype", [(64, BF), (128, BF), (64, FP), (128, FP)])
+@pytest.mark.parametrize("shape", DECODES)
+def test_decode_values(shape, D, dtype, kind):
+    make, call = DECODES[shape]
+    for seed, count in ((1, 1), (2, 7)):
+        r = R.make(**make, news=[1] * len(make["lens"]), D=D, dtype=dtype, layout="HND" if seed == 2 else "NHD", seed=seed)
+        plant(r, 1, KINDS[kind], count, seed)
+        check(r, True, **call)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("shape", DECODES)
+def test_decode_keys_and_values(shape, dtype):
+    make, call = DECODES[shape]
+    make = dict(make, news=[1] * len(make["lens"]), dtype=dtype)
+    r = R.make(**make, seed=6)
+    plant(r, 0, [INF, -INF], 2, 6)
+    check(r, True, **call)
+    r = R.make(**make, seed=7)
+    j = r.seen(0)[len(r.seen(0)) // 2] if len(r.seen(0)) > 1 else 0
+    column(r, 0, j, 0, -INF, 5, which=0)
+    column(r, 0, j, 0, INF, 9)
+    plant(r, 1, [NAN, INF], 2, 7)
+    check(r, True, **call)
+    r = R.make(**make, seed=8)
+    plant(r, 1, [INF, -INF, INF], 9, 8)
+    check(r, True, scale=0.7, **call)
+    r = R.make(**make, seed=9)          # a whole token
+    column(r, 0, r.seen(0)[0], 0, NAN)
+    column(r, 1, r.seen(1)[-1], r.Hkv - 1, INF)
+    check(r, True, **call)
+
+
 def test_small_fp16_weights_count():
     """One key far above the others, each of which has 2^-27 of its weight: 4000 of them count together.  fp16
     weights are at least 2^7 at a row's maximum, so one loses at most 2^-25 2^-7 = 2^-32 of it.  (One CTA a block:
@@ -203,3 +246,7 @@ def test_long_context_with_a_bad_value(value):
     column(r, 0, 3, 0, value, 7)
     column(r, 0, 119900, 0, value, 9)
     check(r, False)
+    d = R.make([120000, 500], [1, 1], Hq=8, Hkv=1, D=64, P=64, seed=5)
+    column(d, 0, 3, 0, value, 7)
+    check(d, True)
+    check(d, True, num_ctas=1)
