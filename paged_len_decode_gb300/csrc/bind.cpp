@@ -223,6 +223,17 @@ PyObject* guarded(F f) {
 
 int32_t* ints(void* p) { return static_cast<int32_t*>(p); }
 
+// A call of a C function without Python's lock: a launch waits where the device's
+// queue is full, and other threads go on meanwhile.  (The caller holds the
+// arguments' tensors.  All that touches Python is done before.)
+template <typename F>
+int without_lock(F f) {
+  PyThreadState* t = PyEval_SaveThread();
+  const int status = f();
+  PyEval_RestoreThread(t);
+  return status;
+}
+
 PyObject* mrope_kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, PyObject* kw) {
   return guarded([&]() -> PyObject* {
     enum { Q, K, V, CS, KC, VC, TABLE, LENS, ACTIVE, QROT, START, POS, AXIS, ERR, QW, KW, EPS, ILV, STREAM, COUNT };
@@ -281,16 +292,23 @@ PyObject* mrope_kv_append(PyObject*, PyObject* const* args, Py_ssize_t nargs, Py
                    *vp = tokens(vn, c.type, dev, "v_new", &vs);
     const unsigned flags = c.flags() | (truth(a[ILV]) ? VH_FLAG_ROPE_INTERLEAVED : 0u) |
                            (rot.scalar_type() == c.type ? VH_FLAG_Q16 : 0u);
-    const int st = vh_mrope_kv_append(
-        qp, kp, vp, qs, ks, vs, static_cast<const float*>(address(cs, at::kFloat, dev, "cos_sin")),
-        static_cast<int>(cs.size(0)), ints(address_or_null(a[POS], at::kInt, dev, "positions")),
-        given(a[AXIS]) ? axis : nullptr, axes, static_cast<const float*>(address_or_null(a[QW], at::kFloat, dev, "q_norm_w")),
-        static_cast<const float*>(address_or_null(a[KW], at::kFloat, dev, "k_norm_w")), real(a[EPS], 1e-6f), c.k, c.v,
-        c.page, c.token, c.head, c.NP, c.table, c.per_row, ints(address_or_null(a[START], at::kInt, dev, "token_start")),
-        ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
-        ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active")),
-        address(rot, rot.scalar_type(), dev, "q_rot"), ints(address_or_null(a[ERR], at::kInt, dev, "err_flag")), flags,
-        static_cast<int>(T), B, static_cast<int>(Hq), c.Hkv, static_cast<int>(D), c.P, stream_of(a[STREAM], dev));
+    const float* angles = static_cast<const float*>(address(cs, at::kFloat, dev, "cos_sin"));
+    const int32_t *pos = ints(address_or_null(a[POS], at::kInt, dev, "positions")),
+                  *start = ints(address_or_null(a[START], at::kInt, dev, "token_start")),
+                  *lens = ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
+                  *active = ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active"));
+    const float *qw = static_cast<const float*>(address_or_null(a[QW], at::kFloat, dev, "q_norm_w")),
+                *kw_ = static_cast<const float*>(address_or_null(a[KW], at::kFloat, dev, "k_norm_w"));
+    const float eps = real(a[EPS], 1e-6f);
+    void *to = address(rot, rot.scalar_type(), dev, "q_rot"), *stream = stream_of(a[STREAM], dev);
+    int32_t* err = ints(address_or_null(a[ERR], at::kInt, dev, "err_flag"));
+    const uint8_t* pair_axis = given(a[AXIS]) ? axis : nullptr;
+    const int max_pos = static_cast<int>(cs.size(0));
+    const int st = without_lock([&] {
+      return vh_mrope_kv_append(qp, kp, vp, qs, ks, vs, angles, max_pos, pos, pair_axis, axes, qw, kw_, eps, c.k, c.v, c.page,
+                                c.token, c.head, c.NP, c.table, c.per_row, start, lens, active, to, err, flags,
+                                static_cast<int>(T), B, static_cast<int>(Hq), c.Hkv, static_cast<int>(D), c.P, stream);
+    });
     return done(st, sig.function, a[QROT]);
   });
 }
@@ -313,14 +331,22 @@ PyObject* window_decode_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs,
     if (q.size(0) != B) raise(PyExc_ValueError, "shape mismatch: q_rot has %lld rows, seq_lens %d", static_cast<long long>(q.size(0)), B);
     const int dev = device_of(q, "q_rot");
     c.locate(a[TABLE], B, dev);
-    const int st = vh_window_decode_attn(
-        static_cast<const float*>(address(q, at::kFloat, dev, "q_rot")), c.k, c.v, c.page, c.token, c.head, c.NP, c.table,
-        c.per_row, ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
-        ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active")), integer32(a[WINDOW], 0, "window"),
-        integer32(a[SINKS], 0, "sinks"), static_cast<uint16_t*>(address(out, c.type, dev, "out")), real(a[SCALE], 0.f),
-        integer32(a[CTAS], 0, "num_ctas"), address(ws, ws.scalar_type(), dev, "workspace"), ws.nbytes(),
-        ints(address_or_null(a[ERR], at::kInt, dev, "err_flag")), c.flags() | (truth(a[PDL]) ? VH_FLAG_PDL : 0u), B,
-        static_cast<int>(Hq), c.Hkv, static_cast<int>(D), c.P, stream_of(a[STREAM], dev));
+    const float* qp = static_cast<const float*>(address(q, at::kFloat, dev, "q_rot"));
+    const int32_t *lens = ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
+                  *active = ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active"));
+    const int window = integer32(a[WINDOW], 0, "window"), sinks = integer32(a[SINKS], 0, "sinks"),
+              ctas = integer32(a[CTAS], 0, "num_ctas");
+    uint16_t* to = static_cast<uint16_t*>(address(out, c.type, dev, "out"));
+    const float scale = real(a[SCALE], 0.f);
+    void *work = address(ws, ws.scalar_type(), dev, "workspace"), *stream = stream_of(a[STREAM], dev);
+    const size_t bytes = ws.nbytes();
+    int32_t* err = ints(address_or_null(a[ERR], at::kInt, dev, "err_flag"));
+    const unsigned flags = c.flags() | (truth(a[PDL]) ? VH_FLAG_PDL : 0u);
+    const int st = without_lock([&] {
+      return vh_window_decode_attn(qp, c.k, c.v, c.page, c.token, c.head, c.NP, c.table, c.per_row, lens, active, window, sinks,
+                                   to, scale, ctas, work, bytes, err, flags, B, static_cast<int>(Hq), c.Hkv,
+                                   static_cast<int>(D), c.P, stream);
+    });
     return done(st, sig.function, a[OUT]);
   });
 }
@@ -342,15 +368,22 @@ PyObject* window_prompt_attn(PyObject*, PyObject* const* args, Py_ssize_t nargs,
     const int B = rows_of(a[LENS], a[ACTIVE], a[START], a[TABLE]);
     const int dev = device_of(q, "q");
     c.locate(a[TABLE], B, dev);
-    const int st = vh_window_prompt_attn(
-        static_cast<const uint16_t*>(address(q, c.type, dev, "q")), c.k, c.v, c.page, c.token, c.head, c.NP, c.table,
-        c.per_row, ints(address(tensor(a[START], "token_start"), at::kInt, dev, "token_start")),
-        ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
-        ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active")), integer32(a[WINDOW], 0, "window"),
-        integer32(a[SINKS], 0, "sinks"), static_cast<uint16_t*>(address(out, c.type, dev, "out")), real(a[SCALE], 0.f),
-        integer32(a[SPLITS], 0, "num_splits"), address(ws, ws.scalar_type(), dev, "workspace"), ws.nbytes(),
-        ints(address_or_null(a[ERR], at::kInt, dev, "err_flag")), c.flags(), static_cast<int>(T), B,
-        static_cast<int>(Hq), c.Hkv, static_cast<int>(D), c.P, stream_of(a[STREAM], dev));
+    const uint16_t* qp = static_cast<const uint16_t*>(address(q, c.type, dev, "q"));
+    const int32_t *start = ints(address(tensor(a[START], "token_start"), at::kInt, dev, "token_start")),
+                  *lens = ints(address(tensor(a[LENS], "seq_lens"), at::kInt, dev, "seq_lens")),
+                  *active = ints(address(tensor(a[ACTIVE], "active"), at::kInt, dev, "active"));
+    const int window = integer32(a[WINDOW], 0, "window"), sinks = integer32(a[SINKS], 0, "sinks"),
+              splits = integer32(a[SPLITS], 0, "num_splits");
+    uint16_t* to = static_cast<uint16_t*>(address(out, c.type, dev, "out"));
+    const float scale = real(a[SCALE], 0.f);
+    void *work = address(ws, ws.scalar_type(), dev, "workspace"), *stream = stream_of(a[STREAM], dev);
+    const size_t bytes = ws.nbytes();
+    int32_t* err = ints(address_or_null(a[ERR], at::kInt, dev, "err_flag"));
+    const int st = without_lock([&] {
+      return vh_window_prompt_attn(qp, c.k, c.v, c.page, c.token, c.head, c.NP, c.table, c.per_row, start, lens, active, window,
+                                   sinks, to, scale, splits, work, bytes, err, c.flags(), static_cast<int>(T), B,
+                                   static_cast<int>(Hq), c.Hkv, static_cast<int>(D), c.P, stream);
+    });
     return done(st, sig.function, a[OUT]);
   });
 }
