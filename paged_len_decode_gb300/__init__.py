@@ -377,8 +377,21 @@ def decode_step(q, k_new, v_new, cos_sin, k_cache, v_cache, page_table, seq_lens
 
 # The calls for prompts, several rotary axes and sliding windows are bound in
 # C++ (csrc/bind.cpp): they are short, and taking a dozen tensors apart in
-# Python would cost more than they run.
-from ._vh_bind import vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn  # noqa: E402
+# Python would cost more than they run.  All other calls need libvh.so alone, so
+# a binding that is missing, or built for another torch, is reported by these three.
+try:
+    from ._vh_bind import vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn  # noqa: E402
+except ImportError as _e:
+    def _unbound(name: str, why: str):
+        def call(*args, **kwargs):
+            raise ImportError(f"{name} needs the C++ binding _vh_bind.so, which could not be loaded: {why} "
+                              '(build it with python -c "import __graft_entry__ as g; g.build()")')
+
+        call.__name__ = name
+        return call
+
+    vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn = (
+        _unbound(n, str(_e)) for n in ("vh_mrope_kv_append", "vh_window_decode_attn", "vh_window_prompt_attn"))
 
 
 def mrope_pair_axis(sections, D: int, cyclic: bool = False) -> list[int]:
