@@ -50,7 +50,25 @@ def _torch_dir() -> str:
     return list(spec.submodule_search_locations)[0]
 
 
-def _compile_bind(src: str, obj: str) -> str:
+def _bind_stamp() -> str:
+    """What the binding is built against besides its sources: torch (found without
+    importing it) and this Python."""
+    d = _torch_dir()
+    version = os.path.join(d, "version.py")
+    with open(version) as f:
+        return f"{d}\n{f.read()}\n{sys.version}\n{sysconfig.get_config_var('EXT_SUFFIX')}\n"
+
+
+def _bind_stale(obj: str, deps: list[str], stamp: str) -> bool:
+    """Whether the binding's object has to be compiled anew; `stamp` is the file
+    that says what it was built against."""
+    if _stale(obj, deps) or not os.path.exists(stamp):
+        return True
+    with open(stamp) as f:
+        return f.read() != _bind_stamp()
+
+
+def _compile_bind(src: str, obj: str, stamp: str) -> str:
     t = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     inc = [t, os.path.join(t, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"], cuda]
@@ -58,6 +76,8 @@ def _compile_bind(src: str, obj: str) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as f:
+        f.write(_bind_stamp())
     return r.stderr
 
 
@@ -82,11 +102,11 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
     bind_src, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
-    bind_deps = [bind_src, os.path.join(HERE, "..", "include", "vh.h")]
+    bind_deps, stamp = [bind_src, os.path.join(HERE, "..", "include", "vh.h")], os.path.join(BUILD, "bind.stamp")
 
     def compile_one(src, obj):
         if src == bind_src:
-            return _compile_bind(src, obj) if force or _stale(obj, bind_deps) else ""
+            return _compile_bind(src, obj, stamp) if force or _bind_stale(obj, bind_deps, stamp) else ""
         if not force and not _stale(obj, [src] + headers):
             return ""
         cmd = [cc, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]

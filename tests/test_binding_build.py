@@ -4,7 +4,6 @@ import os
 import subprocess
 import sys
 
-import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -31,3 +30,46 @@ def test_other_calls_work_without_the_binding():
     assert r.returncode == 0, r.stderr
     assert r.stdout.split("\n")[:4] == ["True True 256"] + [
         f"{n} True True" for n in ("vh_mrope_kv_append", "vh_window_decode_attn", "vh_window_prompt_attn")], r.stdout
+
+
+def build_script():
+    spec = importlib.util.spec_from_file_location("_vh_build_test", os.path.join(ROOT, "paged_len_decode_gb300", "build.py"))
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_binding_is_stale_after_another_torch(tmp_path, monkeypatch):
+    b = build_script()
+    src, obj, stamp = (str(tmp_path / n) for n in ("bind.cpp", "bind.o", "bind.stamp"))
+    for f in (src, obj):
+        open(f, "w").close()
+    assert b._bind_stale(obj, [src], stamp)                       # built before there was a stamp
+    with open(stamp, "w") as f:
+        f.write(b._bind_stamp())
+    assert not b._bind_stale(obj, [src], stamp)
+    os.utime(src, (os.path.getmtime(obj) + 5,) * 2)
+    assert b._bind_stale(obj, [src], stamp)                       # the source is newer
+    os.utime(src, (os.path.getmtime(obj) - 5,) * 2)
+    other = tmp_path / "torch"
+    other.mkdir()
+    (other / "version.py").write_text("__version__ = '9.9'\n")
+    monkeypatch.setattr(b, "_torch_dir", lambda: str(other))
+    assert b._bind_stale(obj, [src], stamp)                       # another torch
+    with open(stamp, "w") as f:
+        f.write(b._bind_stamp())
+    assert not b._bind_stale(obj, [src], stamp)
+    (other / "version.py").write_text("__version__ = '9.10'\n")
+    assert b._bind_stale(obj, [src], stamp)                       # the same place, another version
+
+
+def test_build_compiles_a_stale_binding_only(monkeypatch, tmp_path):
+    b = build_script()
+    b.build()
+    compiled = []
+    monkeypatch.setattr(b, "_compile_bind", lambda src, obj, stamp: compiled.append(obj) or "")
+    b.build()
+    assert compiled == []
+    monkeypatch.setattr(b, "_bind_stamp", lambda: "another")
+    b.build()
+    assert len(compiled) == 1
