@@ -393,19 +393,28 @@ int vh_paged_decode_attn_noalloc(const float* q_rot, const vh_bf16* k_cache, con
  * them: its token t has the logical slot
  *     i = seq_lens[b] - (token_start[b+1] - t).
  * T is the size of the token arrays (a static upper bound for captured
- * graphs); tokens before token_start[0] and from token_start[B] on belong to
- * no row, and nothing of theirs is read or written.  Active rows need
+ * graphs), which hold that many tokens; tokens before token_start[0] and from
+ * token_start[B] on belong to no row: they may be read, but count for nothing,
+ * and nothing of theirs is written.  Active rows need
  * 0 <= token_start[b] <= token_start[b+1] <= T and, if they bring tokens,
  * token_start[b+1] - token_start[b] <= seq_lens[b] <= max_pages_per_seq*P;
  * others are flagged VH_ERR_SEQLEN and treated as inactive.
  *
  * Windows: with window W and S sinks, the query in slot i sees key j <= i if
  * i - j < W (the last W tokens, itself among them) or j < S (the first S
- * tokens).  W = 0: no window, every j <= i is seen.  Slots that no query of
- * the call sees are never read, nor their page-table entries used: pages
+ * tokens).  W = 0: no window, every j <= i is seen.  The page-table entry of
+ * a page without a slot that some query of the call sees is not used: pages
  * that fell behind the window may have been given back, and their entries
- * may hold anything.  Keys or values that one query does not see never
- * change its result, whatever they hold (NaN and infinities too).
+ * may hold anything.  Other slots of a page in use may be read (keys and values
+ * are copied in runs of 8 to 128 slots).  Keys or values that a query does not see
+ * never change its result, whatever they hold (NaN and infinities too).
+ *
+ * Infinities and NaN that a query sees give what sum_j p_j V_j gives in exact
+ * weights: an infinite value makes its output infinite (NaN with one of the
+ * other sign), a NaN makes it NaN; a score of NaN or +inf, or visible scores that
+ * are all -inf, make the whole row NaN; a key with a score of -inf has no weight,
+ * and an infinite value of its makes NaN.  Queries that meet them cost a few
+ * times their usual time.
  *
  * The kernels are launched as programmatic dependents of the previous kernel
  * on the stream and wait for it before they touch memory (but for what
