@@ -113,6 +113,7 @@ __device__ __forceinline__ int row_of(const int* cum, int lo, int B, int t) {
 template <int D, int G, typename E>
 __device__ __noinline__ void plain_outputs(const WindowDecodeParams& p, int b, int h, int L, int k0, int k1, float* piece, float* lse) {
   constexpr int PER = D / 32;
+  constexpr float kDown = 24.f;  // weights of 2^-24 at most: 2^24 values near the type's end do not overflow
   const float NEG_INF = __int_as_float(0xff800000);
   const int lane = threadIdx.x & 31, key = lane & 15, half = lane >> 4;
   const RowTiles rt = tiles_of(L, p.window, p.sinks);
@@ -167,7 +168,7 @@ __device__ __noinline__ void plain_outputs(const WindowDecodeParams& p, int b, i
       mx = fmaxf(mx, M[n]);
       const float ms = mx == NEG_INF ? 0.f : mx, by = at_least_tiny(exp2f(M[n] - ms));
       M[n] = mx;
-      s[n] = s[n] == NEG_INF ? 0.f : at_least_tiny(exp2f(s[n] - ms));  // the weight
+      s[n] = s[n] == NEG_INF ? 0.f : at_least_tiny(exp2f(s[n] - ms - kDown));  // the weight
       float add = s[n];
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
@@ -205,7 +206,7 @@ __device__ __noinline__ void plain_outputs(const WindowDecodeParams& p, int b, i
       if (piece) *reinterpret_cast<float2*>(piece + d) = make_float2(o[n][e] * il, o[n][e + 1] * il);
       else *reinterpret_cast<uint32_t*>(p.out + row + d) = E::pack2(o[n][e] * il, o[n][e + 1] * il);
     }
-    if (piece && lane == 0) lse[n] = M[n] + log2f(sum[n]);
+    if (piece && lane == 0) lse[n] = M[n] + kDown + log2f(sum[n]);
   }
   __syncwarp();
 }

@@ -71,6 +71,10 @@ constexpr float kGrow = 8.f;     // log2 of the growth that rescales
 // 2^-32 of the largest count (at 2^-24 the type's range would end).  bf16 has fp32's range.
 template <typename E>
 constexpr float kLift = E::kF16 ? 7.f : 0.f;
+// The same where a block runs again for its outputs: bf16 values near the type's end may have
+// overflowed in the sum of the products, so the weights are 2^-24 at most, for 2^24 keys.
+template <typename E>
+constexpr float kLiftAgain = E::kF16 ? 7.f : -32.f;
 constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then their outputs
 
 // What a block is run for: its outputs; and where some of them are no numbers, its
@@ -313,7 +317,7 @@ __device__ __forceinline__ float reached(float old, int mode) {
 // then p_full, o_full and o_seen.  Returns the key tiles done, or -1 if a wait ran out.
 template <typename E, int D, bool PAIR>
 __device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit& u, int tiles, int blocks, uint32_t tmem,
-                                           uint32_t bars, uint32_t staging) {
+                                              uint32_t bars, uint32_t staging) {
   const int m = threadIdx.x >> 7, warp = threadIdx.x >> 5;
   const uint32_t noted = staging + static_cast<uint32_t>(warp) * 4096 + 2048;
   tmem += static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -583,6 +587,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     const Tiles sees = tiles_of(p, blk, mq);  // (as the products' warp has them)
     float top = NEG_INF;  // the maximum that the weights refer to, times scale_log2
     float2 sum2 = make_float2(0.f, 0.f);
+    const float lift = AGAIN && blk.mode == kWithout ? kLiftAgain<E> : kLift<E>;
     int n = 0;
     for (int k = blk.k0; k < blk.k1; ++k) {
       if (PAIR ? ((k - blk.k0) & 1) != m : !sees.has(k)) continue;  // not this row tile's
@@ -646,7 +651,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
         sum2.y *= by;
         top = to;
       }
-      const float shift = top == NEG_INF ? 0.f : kLift<E> - top;
+      const float shift = top == NEG_INF ? 0.f : lift - top;
       const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), shift2 = make_float2(shift, shift);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -686,7 +691,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     // its keys without weight adds nothing.
     const float none = p.splits == 1 && token < blk.ntok ? __int_as_float(0x7fffffff) : 0.f;
     float w0 = sum == 0.f ? none : 1.f / sum, w1 = 0.f;
-    float lse = sum > 0.f ? top - kLift<E> + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
+    float lse = sum > 0.f ? top - lift + log2f(sum) : (sum == 0.f ? NEG_INF : sum);
     if constexpr (PAIR) {
       asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(stage + lane * 8), "f"(top), "f"(sum) : "memory");
       meet();
@@ -704,7 +709,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
       const float both = fmaxf(top, top1), shift = both == NEG_INF ? 0.f : both;
       const float a = sum == 0.f ? 0.f : exp2f(top - shift), b = sum1 == 0.f ? 0.f : exp2f(top1 - shift);
       const float all = a * sum + b * sum1;
-      lse = all > 0.f ? both - kLift<E> + log2f(all) : (all == 0.f ? NEG_INF : all);
+      lse = all > 0.f ? both - lift + log2f(all) : (all == 0.f ? NEG_INF : all);
       w0 = all == 0.f ? none : (sum == 0.f ? 0.f : at_least_tiny(a / all));
       w1 = sum1 == 0.f ? 0.f : at_least_tiny(b / all);
     }
@@ -1070,156 +1075,156 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       const uint32_t k_operand = tc_operand(sKV, 16), v_operand = tc_operand(sKV, kBlockBytes);
       int n = 0;
       for (;;) {  // (a second time only where units run once more)
-      for (;; ++n) {
-        wait(u_full(n % kSlots), (n / kSlots) & 1);
-        lost = __any_sync(0xffffffffu, ran_out);
-        auto field = [&](const int& x) { return __shfl_sync(0xffffffffu, x, 0); };  // (uniform, and known to be)
-        const Unit& from = sh.units[n % kSlots];
-        if (lost || field(from.more) == 0) break;
-        Unit blk;
-        blk.slot = field(from.slot);
-        blk.ntok = field(from.ntok);
-        blk.sink_boxes = field(from.sink_boxes);
-        blk.from = field(from.from);
-        blk.count = field(from.count);
-        const int k0 = field(from.k0), k1 = field(from.k1);
-        release_unit(n);
-        if (k0 == k1) continue;
-        const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
-        const int qb = nq % QB;
-        // the key tiles that row tile m sees: below s_end, and from w_begin to w_end
-        int s_end[2], w_begin[2], w_end[2];
-        const int shift = 7 - p.shift_box;  // log2 of the boxes of a tile
+        for (;; ++n) {
+          wait(u_full(n % kSlots), (n / kSlots) & 1);
+          lost = __any_sync(0xffffffffu, ran_out);
+          auto field = [&](const int& x) { return __shfl_sync(0xffffffffu, x, 0); };  // (uniform, and known to be)
+          const Unit& from = sh.units[n % kSlots];
+          if (lost || field(from.more) == 0) break;
+          Unit blk;
+          blk.slot = field(from.slot);
+          blk.ntok = field(from.ntok);
+          blk.sink_boxes = field(from.sink_boxes);
+          blk.from = field(from.from);
+          blk.count = field(from.count);
+          const int k0 = field(from.k0), k1 = field(from.k1);
+          release_unit(n);
+          if (k0 == k1) continue;
+          const int last = blk.slot + blk.ntok - 1, low = max(0, blk.slot - p.window + 1);
+          const int qb = nq % QB;
+          // the key tiles that row tile m sees: below s_end, and from w_begin to w_end
+          int s_end[2], w_begin[2], w_end[2];
+          const int shift = 7 - p.shift_box;  // log2 of the boxes of a tile
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-          const int f = blk.slot + m * per_tile, e = min(last, f + per_tile - 1);
-          const int to = blk.sink_boxes + (e >> p.shift_box) - blk.from;  // last box, if it is one of the window's
-          s_end[m] = f > last ? 0 : min((blk.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
-          w_begin[m] = (blk.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - blk.from)) >> shift;
-          w_end[m] = f > last || to < blk.sink_boxes ? 0 : (to >> shift) + 1;
-        }
-        auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
-        const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
-        auto scores = [&](int m) {
-          const uint32_t qa = q_operand + (PAIR ? 0 : m) * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
-#pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
-            tc_mma(issue, tmem + m * kKeys, qa + off, kb + off, kScores, s > 0);
+          for (int m = 0; m < 2; ++m) {
+            const int f = blk.slot + m * per_tile, e = min(last, f + per_tile - 1);
+            const int to = blk.sink_boxes + (e >> p.shift_box) - blk.from;  // last box, if it is one of the window's
+            s_end[m] = f > last ? 0 : min((blk.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
+            w_begin[m] = (blk.sink_boxes + max(0, (max(0, f - p.window + 1) >> p.shift_box) - blk.from)) >> shift;
+            w_end[m] = f > last || to < blk.sink_boxes ? 0 : (to >> shift) + 1;
           }
-          tc_commit(issue, s_full(m));
-        };
-        bool add0 = false, add1 = false;
-        // the block's last products of row tile m are issued; its softmax has seen the end
-        // of the block before (else it could miss this one)
-        auto finish = [&](int m) {
-          if (nq > 1) wait(o_seen(m), (nq - 2) & 1);
-          tc_commit(issue, o_full(m));
-        };
-        // values of key tile k: slots that nobody sees may hold anything where an end of
-        // what the block sees lies inside the tile, so they become zeros
-        const int last_sinks = blk.sink_boxes > 0 ? (blk.sink_boxes - 1) >> shift : -1, first_window = blk.sink_boxes >> shift;
-        auto clean = [&](int k) {
-          if (k + 1 != blk.count && k != last_sinks && k != first_window) return;
-          const uint32_t vb = sKV + vi * kStage;
-          const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
-          for (int r = lane / 8; r < kKeys; r += 4) {
-            const int j = cols.slot(r);
-            if (j <= last && (j < p.sinks || j >= low)) continue;
+          auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
+          const uint32_t q_operand = tc_operand(sQ + 2 * qb * kQTile, 16);
+          auto scores = [&](int m) {
+            const uint32_t qa = q_operand + (PAIR ? 0 : m) * (kQTile >> 4), kb = k_operand + ki * (kStage >> 4);
 #pragma unroll
-            for (int hf = 0; hf < HALVES; ++hf)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
-                           "r"(0u)
-                           : "memory");
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        };
-        // the weights arrive in two halves of 64 keys
-        auto values = [&](int m, uint32_t& weights, bool& add) {
-          const uint32_t va = v_operand + vi * (kStage >> 4), scores_at = tmem + m * kKeys, out_at = tmem + 2 * kKeys + m * D;
-          wait(p_full(m, 0), weights);
+            for (int s = 0; s < KS; ++s) {
+              const uint32_t off = ((s >> 2) * kBlockBytes + (s & 3) * 32) >> 4;
+              tc_mma(issue, tmem + m * kKeys, qa + off, kb + off, kScores, s > 0);
+            }
+            tc_commit(issue, s_full(m));
+          };
+          bool add0 = false, add1 = false;
+          // the block's last products of row tile m are issued; its softmax has seen the end
+          // of the block before (else it could miss this one)
+          auto finish = [&](int m) {
+            if (nq > 1) wait(o_seen(m), (nq - 2) & 1);
+            tc_commit(issue, o_full(m));
+          };
+          // values of key tile k: slots that nobody sees may hold anything where an end of
+          // what the block sees lies inside the tile, so they become zeros
+          const int last_sinks = blk.sink_boxes > 0 ? (blk.sink_boxes - 1) >> shift : -1, first_window = blk.sink_boxes >> shift;
+          auto clean = [&](int k) {
+            if (k + 1 != blk.count && k != last_sinks && k != first_window) return;
+            const uint32_t vb = sKV + vi * kStage;
+            const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
+            for (int r = lane / 8; r < kKeys; r += 4) {
+              const int j = cols.slot(r);
+              if (j <= last && (j < p.sinks || j >= low)) continue;
+#pragma unroll
+              for (int hf = 0; hf < HALVES; ++hf)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + hf * kBlockBytes + r * 128 + (lane & 7) * 16),
+                             "r"(0u)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          };
+          // the weights arrive in two halves of 64 keys
+          auto values = [&](int m, uint32_t& weights, bool& add) {
+            const uint32_t va = v_operand + vi * (kStage >> 4), scores_at = tmem + m * kKeys, out_at = tmem + 2 * kKeys + m * D;
+            wait(p_full(m, 0), weights);
+            tc_fence_after();
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, add || s > 0);
+            wait(p_full(m, 1), weights);
+            tc_fence_after();
+#pragma unroll
+            for (int s = 4; s < 8; ++s) tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, true);
+            weights ^= 1u;
+            add = true;
+          };
+          wait(q_full(qb), (nq / QB) & 1);
+          wait(full(ki), kp);
+          ++nq;
           tc_fence_after();
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, add || s > 0);
-          wait(p_full(m, 1), weights);
-          tc_fence_after();
-#pragma unroll
-          for (int s = 4; s < 8; ++s) tc_mma_ta(issue, out_at, scores_at + s * 8, va + s * (2048 >> 4), kValues, true);
-          weights ^= 1u;
-          add = true;
-        };
-        wait(q_full(qb), (nq / QB) & 1);
-        wait(full(ki), kp);
-        ++nq;
-        tc_fence_after();
-        if constexpr (PAIR) {
-          scores(0);
-          tc_commit(issue, empty(ki));
-          next(ki, kp);
-          if (k0 + 1 < k1) {
-            wait(full(ki), kp);
-            scores(1);
+          if constexpr (PAIR) {
+            scores(0);
             tc_commit(issue, empty(ki));
             next(ki, kp);
-          }
-          if (k0 + 2 >= k1) tc_commit(issue, q_empty(qb));
-          // key tile k by row tile place m: its values, then the scores of the tile after next
-          auto step = [&](int m, int k, uint32_t& weights, bool& add) {
-            wait(full(vi), vp);
-            clean(k);
-            values(m, weights, add);
-            tc_commit(issue, empty(vi));
-            next(vi, vp);
-            if (k + 2 < k1) {
+            if (k0 + 1 < k1) {
               wait(full(ki), kp);
-              scores(m);
+              scores(1);
               tc_commit(issue, empty(ki));
-              if (k + 3 == k1) tc_commit(issue, q_empty(qb));
               next(ki, kp);
             }
-          };
-          for (int k = k0; k < k1; k += 2) {
-            step(0, k, weights0, add0);
-            if (k + 1 < k1) step(1, k + 1, weights1, add1);
-            if (__any_sync(0xffffffffu, ran_out)) break;
-          }
-          finish(0);
-          finish(1);
-        } else {
-          bool see0 = sees_k(0, k0), see1 = sees_k(1, k0);
-          if (see0) scores(0);
-          if (see1) scores(1);
-          tc_commit(issue, empty(ki));
-          if (k0 + 1 == k1) tc_commit(issue, q_empty(qb));
-          next(ki, kp);
-          for (int k = k0; k < k1; ++k) {
-            const bool more = k + 1 < k1;
-            const bool next0 = more && sees_k(0, k + 1), next1 = more && sees_k(1, k + 1);
-            wait(full(vi), vp);
-            clean(k);
-            if (see0) values(0, weights0, add0);
-            if (more) wait(full(ki), kp);
-            if (next0) scores(0);
-            if (!more) finish(0);
-            if (see1) values(1, weights1, add1);
-            if (next1) scores(1);
-            if (!more) finish(1);
-            tc_commit(issue, empty(vi));
-            if (more) tc_commit(issue, empty(ki));
-            if (k + 2 == k1) tc_commit(issue, q_empty(qb));  // the block's last scores are issued
-            next(vi, vp);
-            if (more) next(ki, kp);
-            see0 = next0;
-            see1 = next1;
-            if (__any_sync(0xffffffffu, ran_out)) break;
+            if (k0 + 2 >= k1) tc_commit(issue, q_empty(qb));
+            // key tile k by row tile place m: its values, then the scores of the tile after next
+            auto step = [&](int m, int k, uint32_t& weights, bool& add) {
+              wait(full(vi), vp);
+              clean(k);
+              values(m, weights, add);
+              tc_commit(issue, empty(vi));
+              next(vi, vp);
+              if (k + 2 < k1) {
+                wait(full(ki), kp);
+                scores(m);
+                tc_commit(issue, empty(ki));
+                if (k + 3 == k1) tc_commit(issue, q_empty(qb));
+                next(ki, kp);
+              }
+            };
+            for (int k = k0; k < k1; k += 2) {
+              step(0, k, weights0, add0);
+              if (k + 1 < k1) step(1, k + 1, weights1, add1);
+              if (__any_sync(0xffffffffu, ran_out)) break;
+            }
+            finish(0);
+            finish(1);
+          } else {
+            bool see0 = sees_k(0, k0), see1 = sees_k(1, k0);
+            if (see0) scores(0);
+            if (see1) scores(1);
+            tc_commit(issue, empty(ki));
+            if (k0 + 1 == k1) tc_commit(issue, q_empty(qb));
+            next(ki, kp);
+            for (int k = k0; k < k1; ++k) {
+              const bool more = k + 1 < k1;
+              const bool next0 = more && sees_k(0, k + 1), next1 = more && sees_k(1, k + 1);
+              wait(full(vi), vp);
+              clean(k);
+              if (see0) values(0, weights0, add0);
+              if (more) wait(full(ki), kp);
+              if (next0) scores(0);
+              if (!more) finish(0);
+              if (see1) values(1, weights1, add1);
+              if (next1) scores(1);
+              if (!more) finish(1);
+              tc_commit(issue, empty(vi));
+              if (more) tc_commit(issue, empty(ki));
+              if (k + 2 == k1) tc_commit(issue, q_empty(qb));  // the block's last scores are issued
+              next(vi, vp);
+              if (more) next(ki, kp);
+              see0 = next0;
+              see1 = next1;
+              if (__any_sync(0xffffffffu, ran_out)) break;
+            }
           }
         }
-      }
-      if (lost || sh.all_done()) break;
-      release_unit(n);
-      ++n;
+        if (lost || sh.all_done()) break;
+        release_unit(n);
+        ++n;
       }
       if (lost) {
         give_up();

@@ -203,6 +203,28 @@ def test_small_fp16_weights_count():
     assert err == 0 and X.differs(out, ref, tol) is None
 
 
+@pytest.mark.parametrize("shape", PROMPTS)
+def test_values_near_the_end_of_bf16(shape):
+    """Finite outputs although sums of unnormalised products would overflow fp32."""
+    make, call = PROMPTS[shape]
+    for big in (2.0 ** 121, 2.0 ** 124):    # (a merge of up to 8 pieces stays finite)
+        r = R.make(**make, D=64, seed=11)
+        v = r.view(r.pool, 1)
+        v.copy_(torch.where(torch.isfinite(v.float()), v.float().sign() * big, v.float()).to(BF))
+        out, ref = check(r, False, **call)
+        assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("shape", DECODES)
+def test_decode_values_near_the_end_of_bf16(shape):
+    make, call = DECODES[shape]
+    r = R.make(**make, news=[1] * len(make["lens"]), seed=11)
+    v = r.view(r.pool, 1)
+    v.copy_(torch.where(torch.isfinite(v.float()), v.float().sign() * 2.0 ** 120, v.float()).to(BF))
+    out, ref = check(r, True, **call)
+    assert torch.isfinite(out.float()).all()
+
+
 def timed(call):
     for _ in range(3):
         call()
