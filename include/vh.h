@@ -224,6 +224,8 @@ size_t vh_decode_workspace_bytes(int B, int Hq, int Hkv, int D, int page_size, i
  * scale; keys beyond seq_len (tail of the last page) are never used.  With
  * fp16, q_rot is split into an fp16 high part and residual for the tensor
  * cores, so its elements must lie within the fp16 range (|x| <= 65504).
+ * Weights are split likewise, so an infinite key or value makes NaN of what it
+ * reaches, here and in vh_decode_fused (vh_window_decode_attn gives infinities).
  * Errors: VH_EINVAL (also for unknown flags), VH_EALIGN, VH_EWORKSPACE, VH_ECUDA. */
 int vh_paged_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e16* v_cache,
                          int64_t page_stride, int64_t token_stride, int64_t head_stride, int num_pages,

@@ -17,7 +17,7 @@
 // first of them and the values are under way before anything is looked up.
 // What counts is bytes in flight and the length of the chain of look-ups: 20 warps
 // an SM with three heads' loads a lane each measured 64 us on 16384 tokens (32 / 8
-// heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.3 us on 2413 with the norm;
+// heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.6 us on 2413 with the norm;
 // 24 warps with two 63.6 and 10.1 us.  In an earlier form four heads took 68 us
 // where two took 66, and a CTA of 4 tokens with its angles in shared memory
 // behind a barrier 82 us.  Angles gathered beside
@@ -224,9 +224,10 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
 
 cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
   MropeParams p = pp;
-  // A token's heads over several warps while the tokens do not fill the GPU: 64
-  // tokens (16 / 8 heads) take 4.4 us with 8 warps each and 6.3 with 1, 800 6.3 with
-  // up to 4 and 8.4 with 8, 2000 10.4 with 1, 11.8 with 2 and 16.6 with 8.
+  // A token's heads over several warps while the tokens do not fill the GPU.  16 / 8
+  // heads of 128 with the norm, 8, 2 and 1 warps a token: 1 token 3.3, 3.7 and 4.9 us,
+  // 128 4.0, 3.9 and 5.1, 512 7.0, 4.4 and 5.3, 1216 11.3, 5.6 and 6.4; without it 64
+  // tokens 3.1, 3.1 and 3.8, 2000 14.7, 8.0 and 8.0.
   p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32)));
   return launch_dependent(p.D == 128 ? (p.f16 ? mrope_kv_append_kernel<ElemF16, 128> : mrope_kv_append_kernel<ElemBf16, 128>)

@@ -231,17 +231,18 @@ long long likely_blocks(int T, int B, int shift) {
 }
 
 // Small blocks (128 rows, both warpgroups on them) where they fit the SMs once: a
-// prompt of 1000 tokens (16 / 8 heads, 128 such blocks, window 256) takes 12 us
-// with them and 19 us with blocks of 256 rows, one of 2000 tokens (256) 18 and 15.
+// prompt of 1000 tokens (16 / 8 heads, 128 such blocks, window 256) takes 10.0 us
+// with them and 18.9 us with blocks of 256 rows, one of 2000 tokens (256) 15.4 and 14.1.
 bool small_blocks(int T, int B, int G, int Hkv, const DeviceInfo& dev) {
   return likely_blocks(T, B, 7 - __builtin_ctz(G)) * Hkv <= dev.sm_count;
 }
 
 // CTAs that share a block's keys: as many as leave every cluster running at
 // once, and two key tiles each at least.  (16 tokens over 4100 keys,
-// 8 kv heads: 33 us with one CTA a block, 23, 17 and 15 us with 2, 4 and 8, and
-// 27 us with 16, of which half the clusters wait for the others; over 300 keys 9.5
-// us with one and 10.8 with 2.)
+// 8 kv heads: 29 us with one CTA a block, 20, 15 and 14 us with 2, 4 and 8, and
+// 25 us with 16, of which half the clusters wait for the others; over 300 keys 8.4
+// us with one and 9.8 with 2; 128 tokens over 4200 30, 23 and 19 us with 1, 2 and 4,
+// and 33 with 8.)
 int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
   const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
                                                 static_cast<long long>(p.window) + p.sinks + (1 << p.shift_block));
