@@ -2,6 +2,7 @@
 attention, against float64: they have to reach the outputs whose queries see
 them, as they would in float64, and no others; and a call must stay about as fast."""
 import math
+import os
 import random
 import statistics
 
@@ -9,6 +10,7 @@ import pytest
 import torch
 
 import test_gpu_window as W
+import test_gpu_window_fuzz as F
 import window_batch as X
 import window_ref as R
 
@@ -223,6 +225,96 @@ def test_decode_values_near_the_end_of_bf16(shape):
     v.copy_(torch.where(torch.isfinite(v.float()), v.float().sign() * 2.0 ** 120, v.float()).to(BF))
     out, ref = check(r, True, **call)
     assert torch.isfinite(out.float()).all()
+
+
+CASES = int(os.environ.get("VH_NONFINITE_CASES", "24"))
+
+
+def planted(rng, r):
+    for which, count in ((1, rng.choice([0, 1, 3, 20])), (0, rng.choice([0, 0, 1, 2]))):
+        values = KINDS[rng.choice(list(KINDS))] if which else [INF, -INF, NAN][:rng.choice([2, 2, 3])]
+        plant(r, which, values, count, rng.randrange(1 << 20))
+    if rng.random() < 0.3:
+        b = rng.choice([b for b in range(r.B) if r.active[b] and r.news[b]])
+        column(r, b, rng.choice(r.seen(b)), rng.randrange(r.Hkv), rng.choice([INF, -INF, NAN]))
+    return r
+
+
+def alive(make):
+    if not any(a and n for a, n in zip(make["active"], make["news"])):
+        make["active"], make["news"] = [1] * len(make["active"]), [max(1, n) for n in make["news"]]
+    return make
+
+
+@pytest.mark.parametrize("case", range(CASES))
+def test_random_decode_cases(case):
+    rng = random.Random(31000 + case)
+    r = planted(rng, R.make(**alive(F.pick(rng, True))))
+    check(r, True, scale=rng.choice([0.0, 0.05, 0.5]), num_ctas=rng.choice([0, 0, 1, 2, 5, 33]), pdl=rng.random() < 0.5)
+
+
+@pytest.mark.parametrize("case", range(CASES))
+def test_random_prompt_cases(case):
+    rng = random.Random(32000 + case)
+    r = planted(rng, R.make(**alive(F.pick(rng, False))))
+    check(r, False, scale=rng.choice([0.0, 0.05, 0.5]), splits=rng.choice([0, 0, 0, 1, 2, 4, 8]), extra=rng.choice([0, 3]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_more_than_32_requests(D):
+    lens = [1 + (37 * b) % 250 for b in range(70)]
+    news = [min(n, (13 * b) % 90) for b, n in enumerate(lens)]
+    r = R.make(lens, news, Hq=16, Hkv=8, D=D, window=100, sinks=3, active=[int(b % 7 != 2) for b in range(70)], seed=D)
+    plant(r, 1, [INF, NAN, -INF], 40, 5)
+    check(r, False, extra=2)
+
+
+def test_replayed_graph_with_values_that_come_and_go():
+    """A captured prompt and decode call, replayed with finite values, bad ones and finite ones again."""
+    v = W.vh()
+    r = R.make([700, 500], [700, 450], Hq=16, Hkv=8, window=300, sinks=4, seed=3)
+    d = R.make([700, 500], [1, 1], Hq=16, Hkv=8, window=300, sinks=4, seed=4)
+    gp, gd = W.on_gpu(r), W.on_gpu(d)
+    q, qd = R.queries(r, BF).cuda(), R.queries(d, torch.float32).cuda()
+    out, outd = torch.zeros_like(q), torch.zeros(2, 16, 128, dtype=BF, device="cuda")
+    ws, wd = v.alloc_prompt_workspace(1150, 2, 16, 8, 128), v.alloc_workspace(2, 16, 8, 128, 16)
+
+    def call():
+        v.vh_window_prompt_attn(q, gp["k"], gp["v"], gp["table"], gp["starts"], gp["lens"], gp["active"], out, ws, window=300,
+                                sinks=4, err_flag=gp["err"])
+        v.vh_window_decode_attn(qd, gd["k"], gd["v"], gd["table"], gd["lens"], gd["active"], outd, wd, window=300, sinks=4,
+                                err_flag=gd["err"])
+
+    call()
+    torch.cuda.synchronize()
+    first = out.clone(), outd.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s), torch.cuda.graph(g, stream=s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    places = [(gp, r, 0, 1, 3), (gp, r, 1, 60, 90), (gp, r, 0, 650, 100), (gd, d, 0, 2, 5), (gd, d, 1, 499, 7)]
+    for _ in range(3):
+        kept = []
+        for (t, x, b, j, e), value in zip(places, (NAN, INF, -INF, INF, NAN)):
+            at = t["v"][int(x.table[b, j // 16]), j % 16, :, e]
+            kept.append((at, at.clone()))
+            at.fill_(value)
+            x.view(x.pool, 1)[int(x.table[b, j // 16]), j % 16, :, e] = value
+        g.replay()
+        torch.cuda.synchronize()
+        for o, x, y, split in ((out, r, q, False), (outd, d, qd, True)):
+            ref = X.attention(x, y.cpu())
+            bad = X.differs(o, ref, R.tolerance(ref, BF, 128, split, 8.0))
+            assert bad is None, bad
+        for (at, was), (t, x, b, j, e) in zip(kept, places):
+            at.copy_(was)
+            x.view(x.pool, 1)[int(x.table[b, j // 16]), j % 16, :, e] = was.cpu()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first[0]) and torch.equal(outd, first[1])
+        assert not ws.any() and int(gp["err"]) == 0 and int(gd["err"]) == 0
 
 
 def timed(call):
