@@ -521,6 +521,116 @@ __device__ __forceinline__ uint32_t pass_on_values(Shared<D>& sh, uint32_t stage
   return phases;
 }
 
+// How far the drawing warp is: the next unit's number in the CTA, and of all, and the tiles
+// of V copied for the units so far; `again`: a unit has to run once more.
+struct DrawPlace {
+  int n, u, tiles;
+  bool again, lost;
+};
+
+// The drawing warp's work: the CTA's units one after the other, to the first that has to run
+// once more, or (AGAIN) all that follow.  The first unit is the CTA's own number; the
+// others come from the counter, which the last draw of all sets back for the next call.  A
+// cluster has one unit a CTA.  A unit that has to run once more does so in its slot, before
+// the slot is given to another.  In those runs this warp takes V from the copies, and passes it
+// on filtered.
+template <typename E, int D, bool AGAIN>
+__device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh, uint32_t stages, DrawPlace& at) {
+  const Bars<D> bar{smem_addr(sh.bars)};
+  const int lane = threadIdx.x & 31;
+  Rows rows{};
+  if (p.B <= 32) rows = rows_of(p, lane);
+  const int units = p.blocks * p.Hkv * p.splits;
+  int n = at.n, u = at.u, tiles = at.tiles;
+  uint32_t kinds[kSlots] = {};  // modes that the slot's unit has still to run in, as bits
+  uint32_t landings = 0u;       // phases of the stages' barriers
+  bool lost = false;
+  for (;; ++n) {
+    Unit& slot = sh.units[n % kSlots];
+    int mode = kPlain;
+    if (n >= kSlots) {
+      lost = !mbar_wait(bar.u_empty(n % kSlots), ((n / kSlots) - 1) & 1);
+      if (lost) break;
+      __syncwarp();
+      const uint32_t met = static_cast<uint32_t>(*static_cast<volatile int*>(&sh.met[n % kSlots]));
+      if constexpr (AGAIN) {
+        uint32_t todo = n % kSlots ? kinds[1] : kinds[0];
+        if (slot.mode == kPlain) {
+          if (met & 1u) mode = kWithout;
+        } else {
+          if (slot.mode == kWithout && !slot.settle) {
+            todo = met & 6u ? met : met & 8u;
+            if (todo && p.splits > 1) todo |= 1u << (kSettle - 1);
+          }
+          if (todo) mode = __ffs(todo);
+          todo &= todo - 1u;
+        }
+        if (n % kSlots) kinds[1] = todo;
+        else kinds[0] = todo;
+        __syncwarp();
+        if (lane == 0) sh.met[n % kSlots] = 0;
+      } else if (met != 0u) {
+        at.again = true;
+        break;
+      }
+    }
+    Unit x{};
+    if (mode != kPlain) {
+      x = slot;
+      x.mode = mode == kSettle ? kWithout : mode;
+      x.settle = mode == kSettle;
+      x.soft = x.k0;
+    } else if (u < units) {
+      x = unit_of(p, rows, u, lane);
+      x.soft = x.k1;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      slot = x;
+      if (n == 0) sh.join = x;
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar.u_full(n % kSlots));
+    if (!x.more) {
+      if (sh.all_done()) break;
+      lost = !mbar_wait(bar.u_empty(n % kSlots), (n / kSlots) & 1);
+      if (lost) break;
+      continue;
+    }
+    lost = *static_cast<volatile int*>(&sh.abort) != 0;
+    if (lost) break;
+    if (AGAIN && x.mode != kPlain) {
+      landings = pass_on_values<E, D>(sh, stages, tiles, x.k1 - x.k0, landings, x.mode, n % kSlots);
+      lost = landings == kLostPhase;
+      if (lost) break;
+    }
+    tiles += x.k1 - x.k0;
+    if (mode != kPlain || u >= units) continue;
+    if (p.splits > 1) {
+      u = units;
+    } else {
+      if (lane == 0) {
+        const int drawn = atomicAdd(p.counter, 1);
+        if (drawn == units - 1) *p.counter = 0;
+        u = gridDim.x + drawn;
+      }
+      u = __shfl_sync(0xffffffffu, u, 0);
+    }
+  }
+  at.n = n;
+  at.u = u;
+  at.tiles = tiles;
+  at.lost = lost;
+}
+
+// The same from a unit that runs once more on, out of line.
+template <typename E, int D>
+__device__ __noinline__ bool draw_again(const PromptParams& p, Shared<D>& sh, uint32_t stages, int n, int u, int tiles) {
+  DrawPlace at{n, u, tiles, false, false};
+  draw_units<E, D, true>(p, sh, stages, at);
+  return at.lost;
+}
+
 // How far a softmax warp is: its unit, tiles and blocks of its row tile done, meetings of
 // both warpgroups; `again`: the unit is one that runs once more.
 struct SoftmaxPlace {
@@ -889,87 +999,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
     const bool leader = elect_one();
     if (warp == kDrawWarp) {
       // ======================= the CTA's next unit =====================================
-      // The first is the CTA's own number; the others come from the counter, which
-      // the last draw of all sets back for the next call.  A cluster has one unit a CTA.
-      // A unit that has to run once more does so in its slot, before the slot is given
-      // to another.  In those runs this warp takes V from the copies, and passes it on
-      // filtered.
-      Rows rows{};
-      if (p.B <= 32) rows = rows_of(p, lane);
-      const int units = p.blocks * p.Hkv * p.splits;
-      int u = blockIdx.x;
-      uint32_t kinds[kSlots] = {};  // modes that the slot's unit has still to run in, as bits
-      bool lost = false;
-      int tiles = 0;                // of V copied for the units published so far
-      uint32_t landings = 0u;       // phases of the stages' barriers
-      for (int n = 0;; ++n) {
-        Unit& slot = sh.units[n % kSlots];
-        int mode = kPlain;
-        if (n >= kSlots) {
-          lost = !mbar_wait(u_empty(n % kSlots), ((n / kSlots) - 1) & 1);
-          if (lost) break;
-          __syncwarp();
-          const uint32_t met = static_cast<uint32_t>(*reinterpret_cast<volatile int*>(&sh.met[n % kSlots]));
-          uint32_t todo = n % kSlots ? kinds[1] : kinds[0];
-          if (slot.mode == kPlain) {
-            if (met & 1u) mode = kWithout;
-          } else {
-            if (slot.mode == kWithout && !slot.settle) {
-              todo = met & 6u ? met : met & 8u;
-              if (todo && p.splits > 1) todo |= 1u << (kSettle - 1);
-            }
-            if (todo) mode = __ffs(todo);
-            todo &= todo - 1u;
-          }
-          if (n % kSlots) kinds[1] = todo;
-          else kinds[0] = todo;
-          __syncwarp();
-          if (lane == 0) sh.met[n % kSlots] = 0;
-        }
-        Unit x{};
-        if (mode != kPlain) {
-          x = slot;
-          x.mode = mode == kSettle ? kWithout : mode;
-          x.settle = mode == kSettle;
-          x.soft = x.k0;
-        } else if (u < units) {
-          x = unit_of(p, rows, u, lane);
-          x.soft = x.k1;
-        }
-        __syncwarp();
-        if (lane == 0) {
-          slot = x;
-          if (n == 0) sh.join = x;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(u_full(n % kSlots));
-        if (!x.more) {
-          if (sh.all_done()) break;
-          lost = !mbar_wait(u_empty(n % kSlots), (n / kSlots) & 1);
-          if (lost) break;
-          continue;
-        }
-        lost = *abort_flag != 0;
-        if (lost) break;
-        if (x.mode != kPlain) {
-          landings = pass_on_values<E, D>(sh, sKV, tiles, x.k1 - x.k0, landings, x.mode, n % kSlots);
-          lost = landings == kLostPhase;
-          if (lost) break;
-        }
-        tiles += x.k1 - x.k0;
-        if (mode != kPlain || u >= units) continue;
-        if (p.splits > 1) {
-          u = units;
-        } else {
-          if (lane == 0) {
-            const int drawn = atomicAdd(p.counter, 1);
-            if (drawn == units - 1) *p.counter = 0;
-            u = gridDim.x + drawn;
-          }
-          u = __shfl_sync(0xffffffffu, u, 0);
-        }
-      }
-      if (lost) {
+      DrawPlace at{};
+      at.u = blockIdx.x;
+      draw_units<E, D, false>(p, sh, sKV, at);
+      if (at.again) at.lost = draw_again<E, D>(p, sh, sKV, at.n, at.u, at.tiles);
+      if (at.lost) {
         give_up();
         named_sync(1, kThreads);
       }
