@@ -30,7 +30,7 @@
 //    outputs of this one are under way.
 //  * Softmax.  Running maximum and sum in fp32; the accumulator is rescaled
 //    only when a row's maximum has grown by more than 2^8 since the last time
-//    (weights stay below 2^8, far inside fp32, bf16 and fp16), so it is rare.
+//    (weights stay below 2^8, in fp16, scaled, below 2^15: inside each type), so it is rare.
 //    Weights go back to tensor memory as 16-bit operands of the value product,
 //    over the scores: rounding them costs one half step of the element type
 //    relatively, as the output's own rounding does, and saves a second product.
