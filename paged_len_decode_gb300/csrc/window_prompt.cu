@@ -43,8 +43,9 @@
 //    values as zeros, and then once for each kind of them (+inf, -inf, NaN) that was
 //    met, with the values of that kind as ones and the others as zeros and weight 1
 //    for every visible key: outputs that come out above zero are set to what they
-//    must be.  A block takes about its usual time each of these times, whatever the
-//    cache holds, so no wait of the pipeline grows longer.  In a cluster, where
+//    must be.  A block takes two to three times its usual time each of these times (V
+//    is filtered between copy and product), whatever the cache holds, and its waits
+//    remain those of a tile.  In a cluster, where
 //    partial outputs lie in memory that the runs need, the kinds are noted beside
 //    them and set in a last run.  All of this is kept apart from the common path: a
 //    function call, or code for it between the products, costs that 2 to 8 us of 43
