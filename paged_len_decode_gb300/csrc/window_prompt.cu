@@ -40,12 +40,12 @@
 //    harmless unless it is infinite or NaN; so does one whose weight is too small
 //    for the element type.  A block with an output that is no number, although its
 //    row's sum is one, therefore runs once more, by the same pipeline, with such
-//    values as zeros, and then once for each kind of them (+inf, -inf, NaN) that was
-//    met, with the values of that kind as ones and the others as zeros and weight 1
-//    for every visible key: outputs that come out above zero are set to what they
-//    must be.  A block takes two to three times its usual time each of these times (V
-//    is filtered between copy and product), whatever the cache holds, and its waits
-//    remain those of a tile.  In a cluster, where
+//    values as zeros (two to three times its usual time: V is filtered between copy
+//    and product), and then once for each kind of them (+inf, -inf, NaN) that was met,
+//    over the key tiles from the first to the last that hold one, with the values of that
+//    kind as ones and the others as zeros and weight 1 for every visible key: outputs
+//    that come out above zero are set to what they must be.  That is bounded whatever
+//    the cache holds, and the waits remain those of a tile.  In a cluster, where
 //    partial outputs lie in memory that the runs need, the kinds are noted beside
 //    them and set in a last run.  All of this is kept apart from the common path: a
 //    function call, or code for it between the products, costs that 2 to 8 us of 43
@@ -96,6 +96,7 @@ struct Unit {
   int mode;                     // kPlain, or once more
   int settle;                   // the last of a cluster's runs: what was noted is set
   int soft;                     // k1, or k0 where the unit runs once more (or has nothing to do)
+  int all0, all1;               // k0 and k1 of the first run
   int more;                     // 0: no unit, the CTA is done
 };
 
@@ -438,6 +439,7 @@ struct Shared {
   Unit units[kSlots];
   Unit join;        // the block whose partial results a cluster joins
   int met[kSlots];  // of the unit in the slot (see kPlain)
+  int span[kSlots][2];  // its key tiles that hold values that are no numbers: the first, and the one behind the last
   uint32_t tmem;
   int abort;
 
@@ -508,16 +510,28 @@ __device__ __forceinline__ uint32_t pass_on_values(Shared<D>& sh, uint32_t stage
   const Bars<D> bar{smem_addr(sh.bars)};
   const int lane = threadIdx.x & 31;
   uint32_t met = 0u;
+  int begin = 0, end = 0;
   for (int t = 0; t < count; ++t) {
     const int s = (2 * (first + t) + 1) % ST;
     if (!mbar_wait(bar.landed(s), (phases >> s) & 1u) || *static_cast<volatile int*>(&sh.abort)) return kLostPhase;
     phases ^= 1u << s;
-    met |= filter_values<E>(stages + s * kStage, kStage, mode, lane);
+    const uint32_t here = filter_values<E>(stages + s * kStage, kStage, mode, lane);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar.full(s));
+    met |= here;
+    if (__any_sync(0xffffffffu, here != 0u)) {
+      if (end == 0) begin = t;
+      end = t + 1;
+    }
   }
-  if (mode == kWithout && met) note_met(smem_addr(&sh.met[slot]), met);
+  if (mode == kWithout) {
+    if (met) note_met(smem_addr(&sh.met[slot]), met);
+    if (lane == 0) {
+      sh.span[slot][0] = begin;
+      sh.span[slot][1] = end;
+    }
+  }
   __syncwarp();
   return phases;
 }
@@ -578,8 +592,15 @@ __device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh,
     Unit x{};
     if (mode != kPlain) {
       x = slot;
+      if (x.mode == kPlain) {
+        x.all0 = x.k0;
+        x.all1 = x.k1;
+      }
+      const bool looks = mode > kWithout && mode < kSettle;
       x.mode = mode == kSettle ? kWithout : mode;
       x.settle = mode == kSettle;
+      x.k0 = x.all0 + (looks ? sh.span[n % kSlots][0] : 0);
+      x.k1 = looks ? x.all0 + sh.span[n % kSlots][1] : x.all1;
       x.soft = x.k0;
     } else if (u < units) {
       x = unit_of(p, rows, u, lane);
