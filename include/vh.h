@@ -99,6 +99,7 @@ extern "C" {
 
 typedef uint16_t vh_bf16;  /* a bf16 bit pattern */
 typedef uint16_t vh_e16;   /* a 16-bit element: bf16, or fp16 under VH_FLAG_FP16 */
+typedef uint8_t vh_e4m3;   /* an 8-bit element: sign, 4 bits of exponent, 3 of mantissa; finite up to 448, NaN, no infinity */
 
 /* return codes */
 #define VH_OK 0
@@ -514,6 +515,119 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
                           int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
                           void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
                           int T, int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* ---- drafted tokens that form a tree ---------------------------------------
+ *
+ * Speculative decoding: the n drafted tokens of a row, in slots base .. L-1
+ * (base = seq_lens[b] - n), are the new tokens of a ragged batch as above, but
+ * a token's context among them is its chain of ancestors. */
+
+/* Attention of a ragged batch of drafted tokens over the paged cache, which
+ * already holds their keys and values (vh_mrope_kv_append with the tokens'
+ * positions).  Arguments, result and errors as for vh_window_prompt_attn, and
+ * tree_mask int64 [T][mask_words], 8-byte aligned: bit k % 64 of word k / 64 of
+ *        token t says that the row's k-th drafted token is an ancestor of t.
+ *        Only bits below t's own number i = t - token_start[b] count; a token
+ *        always sees itself, whatever its own bit.
+ * mask_words 1 .. VH_TREE_WORDS_MAX; an active row that brings more than
+ *        64 mask_words tokens is flagged VH_ERR_SEQLEN and treated as inactive.
+ * Token i sees the context's slots j < base, all of them or under a window W
+ * those with at - j < W or j < S, where at = base + (number of its ancestors) is
+ * its position; the drafted tokens of its mask (a window does not hide
+ * them); and itself.  With masks of all ones this is vh_window_prompt_attn's
+ * causal attention, but for a window's hold on the drafted tokens.
+ * workspace: vh_prompt_workspace_bytes, as for vh_window_prompt_attn (the same
+ *        buffer may serve both, one after the other). */
+#define VH_TREE_WORDS_MAX 16
+int vh_tree_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache,
+                 int64_t page_stride, int64_t token_stride, int64_t head_stride, int num_pages,
+                 const int32_t* page_table, int max_pages_per_seq,
+                 const int32_t* token_start, const int32_t* seq_lens, const int32_t* active,
+                 const int64_t* tree_mask, int mask_words,
+                 int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
+                 void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
+                 int T, int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* ---- a cache of 8 bits ------------------------------------------------------
+ *
+ * Keys and values as e4m3 with a scale for every (slot, kv head): half the bytes
+ * of the 16-bit cache, which are what a decode step's time is made of.  The
+ * source pages have no counterpart.  Pages, layouts, page tables, ragged batches,
+ * windows and error bits are those of the calls above; strides of the values are
+ * in elements (bytes) and multiples of 16, k_cache and v_cache 16-byte aligned.
+ * Scales: float, that of head h of slot t of page n at
+ *     n*scale_page_stride + h*scale_head_stride + t
+ * (a page's slots follow one another), for K and V alike; both strides are
+ * multiples of 4 and k_scale and v_scale 16-byte aligned.  [NP][2][Hkv][P] with
+ * v_scale = k_scale + Hkv*P is such a layout for P a multiple of 4.
+ * A head x (after norm and rotation, in fp32) is stored as the scale
+ * s = max(max|x| / 448, 2^-126) and the bytes e4m3(x * (1 / s)), divisions and
+ * conversions rounded to nearest (even): off by at most half a step of e4m3, 2^-4
+ * relatively and s 2^-10 near zero.  (bf16 values below 2^-126 are taken as
+ * zeros.)  A head with an infinity or a NaN has the scale NaN, and so reads as NaN
+ * as a whole.  Scales that others write must be >= 0, or NaN. */
+
+/* vh_mrope_kv_append into a cache of 8 bits: arguments, result and errors are its
+ * own, with the scales beside the cache; k and v take the steps above instead
+ * of their rounding to 16 bits.  flags: VH_FLAG_FP16 and VH_FLAG_Q16 speak of q,
+ * k_new, v_new and q_rot. */
+int vh_quant_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new,
+                       int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                       const float* cos_sin, int max_pos, const int32_t* positions,
+                       const uint8_t* pair_axis, int num_axes,
+                       const float* q_norm_w, const float* k_norm_w, float norm_eps,
+                       vh_e4m3* k_cache, vh_e4m3* v_cache, int64_t page_stride, int64_t token_stride,
+                       int64_t head_stride, float* k_scale, float* v_scale,
+                       int64_t scale_page_stride, int64_t scale_head_stride, int num_pages,
+                       const int32_t* page_table, int max_pages_per_seq,
+                       const int32_t* token_start, const int32_t* seq_lens, const int32_t* active,
+                       void* q_rot, int32_t* err_flag, unsigned flags,
+                       int T, int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* Single-token attention over a cache of 8 bits, in one launch: arguments,
+ * result, workspace and errors as for vh_window_decode_attn (window = 0: every
+ * token), with the scales beside the cache.  Scores are scale <q_rot, k8_j> ks_j
+ * and the output sum_j p_j vs_j v8_j: nothing is rounded to 16 bits on the way but
+ * the weights (p_j vs_j of the largest, 2^-11 relatively) and q (to 2^-22 of a
+ * head's largest element).  A query head with an infinity or a NaN gives NaN; a
+ * visible key whose scale is NaN makes its rows NaN, a value its outputs.  A page id
+ * outside [0, num_pages) is flagged VH_ERR_PAGE and its keys and values are
+ * taken as zeros.  VH_FLAG_FP16: out is fp16. */
+int vh_quant_decode_attn(const float* q_rot, const vh_e4m3* k_cache, const vh_e4m3* v_cache,
+                         int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                         const float* k_scale, const float* v_scale,
+                         int64_t scale_page_stride, int64_t scale_head_stride, int num_pages,
+                         const int32_t* page_table, int max_pages_per_seq,
+                         const int32_t* seq_lens, const int32_t* active, int window, int sinks,
+                         vh_e16* out, float sm_scale, int num_ctas,
+                         void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags,
+                         int B, int Hq, int Hkv, int D, int page_size, void* stream);
+
+/* Slots of a cache of 8 bits, read back into the same slots of a 16-bit one with
+ * pages of its own (what vh_window_prompt_attn and vh_tree_attn then attend over):
+ * out = rne(e4m3 * scale).  Row b's slots first_slot[b] .. seq_lens[b]-1 and those
+ * below `sinks` are written, others are left as they were.
+ * first_slot int32 [B], or NULL: every slot.  (For new tokens from slot i on under a
+ *        window W: max(0, i - W + 1).)
+ * k_out, v_out, out_page_stride, out_token_stride, out_head_stride, out_num_pages,
+ *        out_page_table, out_max_pages_per_seq, out_page_size: the 16-bit cache, as for the
+ *        other calls (out_page_table NULL: contiguous); must not overlap the 8-bit one.
+ * Active rows need 1 <= seq_lens[b] <= the slots of both page tables and
+ * first_slot[b] >= 0; others are flagged VH_ERR_SEQLEN and nothing of them is
+ * written.  A page id of the 8-bit cache outside [0, num_pages) is flagged
+ * VH_ERR_PAGE and read as zeros; one of the 16-bit cache is flagged and not
+ * written.  flags: VH_FLAG_FP16 (k_out and v_out are fp16).
+ * Errors: VH_EINVAL, VH_EALIGN, VH_ENODEV, VH_ECUDA. */
+int vh_quant_kv_read(const vh_e4m3* k_cache, const vh_e4m3* v_cache,
+                     int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                     const float* k_scale, const float* v_scale,
+                     int64_t scale_page_stride, int64_t scale_head_stride, int num_pages,
+                     const int32_t* page_table, int max_pages_per_seq,
+                     const int32_t* seq_lens, const int32_t* active, const int32_t* first_slot, int sinks,
+                     vh_e16* k_out, vh_e16* v_out, int64_t out_page_stride, int64_t out_token_stride,
+                     int64_t out_head_stride, int out_num_pages, const int32_t* out_page_table,
+                     int out_max_pages_per_seq, int32_t* err_flag, unsigned flags,
+                     int B, int Hkv, int D, int page_size, int out_page_size, void* stream);
 
 /* Self-test of the failure path of the kernels' pipeline waits.  The source
  * pages have no counterpart: every wait of the attention kernels on an

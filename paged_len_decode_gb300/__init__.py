@@ -16,9 +16,14 @@ Functions mirror the C entry points by name:
     vh_decode_workspace_bytes, vh_paged_decode_attn, vh_decode_combine,
     vh_decode_fused, vh_decode_plan, vh_paged_decode_attn_noalloc, vh_selftest_wait_timeout,
     vh_status_string, and for prompts, several rotary axes and sliding windows
-    vh_mrope_kv_append, vh_window_decode_attn, vh_prompt_workspace_bytes, vh_window_prompt_attn
-plus `decode_step`, which issues the three calls of one decode step, and
-`mrope_pair_axis`, which spells out the axis of every rotated pair.
+    vh_mrope_kv_append, vh_window_decode_attn, vh_prompt_workspace_bytes, vh_window_prompt_attn,
+for drafted tokens
+    vh_tree_attn,
+and for a cache of 8 bits
+    vh_quant_kv_append, vh_quant_decode_attn, vh_quant_kv_read
+plus `decode_step`, which issues the three calls of one decode step,
+`mrope_pair_axis`, which spells out the axis of every rotated pair, `tree_masks`,
+which makes masks of parents, and `alloc_quant_cache`.
 """
 from __future__ import annotations
 
@@ -91,6 +96,18 @@ def _load() -> ctypes.CDLL:
     lib.vh_window_prompt_attn.argtypes = [P, P, P, I64, I64, I64, I, P, I, P, P, P, I, I, P, F, I, P, SZ, P, U,
                                           I, I, I, I, I, I, P]
     lib.vh_window_prompt_attn.restype = I
+    lib.vh_tree_attn.argtypes = [P, P, P, I64, I64, I64, I, P, I, P, P, P, P, I, I, I, P, F, I, P, SZ, P, U,
+                                 I, I, I, I, I, I, P]
+    lib.vh_tree_attn.restype = I
+    lib.vh_quant_kv_append.argtypes = [P, P, P, I64, I64, I64, P, I, P, P, I, P, P, F, P, P, I64, I64, I64, P, P, I64, I64,
+                                       I, P, I, P, P, P, P, P, U, I, I, I, I, I, I, P]
+    lib.vh_quant_kv_append.restype = I
+    lib.vh_quant_decode_attn.argtypes = [P, P, P, I64, I64, I64, P, P, I64, I64, I, P, I, P, P, I, I, P, F, I, P, SZ, P, U,
+                                         I, I, I, I, I, P]
+    lib.vh_quant_decode_attn.restype = I
+    lib.vh_quant_kv_read.argtypes = [P, P, I64, I64, I64, P, P, I64, I64, I, P, I, P, P, P, I, P, P, I64, I64, I64, I, P, I,
+                                     P, U, I, I, I, I, I, P]
+    lib.vh_quant_kv_read.restype = I
     return lib
 
 
@@ -375,12 +392,15 @@ def decode_step(q, k_new, v_new, cos_sin, k_cache, v_cache, page_table, seq_lens
     return out
 
 
-# The calls for prompts, several rotary axes and sliding windows are bound in
-# C++ (csrc/bind.cpp): they are short, and taking a dozen tensors apart in
-# Python would cost more than they run.  All other calls need libvh.so alone, so
-# a binding that is missing, or built for another torch, is reported by these three.
+# The calls for prompts, several rotary axes, sliding windows, trees and 8-bit
+# caches are bound in C++ (csrc/bind.cpp): they are short, and taking a dozen tensors
+# apart in Python would cost more than they run.  All other calls need libvh.so alone, so
+# a binding that is missing, or built for another torch, is reported by these.
+_BOUND = ("vh_mrope_kv_append", "vh_window_decode_attn", "vh_window_prompt_attn", "vh_tree_attn", "vh_quant_kv_append",
+          "vh_quant_decode_attn", "vh_quant_kv_read")
 try:
-    from ._vh_bind import vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn  # noqa: E402
+    from ._vh_bind import (vh_mrope_kv_append, vh_quant_decode_attn, vh_quant_kv_append, vh_quant_kv_read,  # noqa: E402
+                           vh_tree_attn, vh_window_decode_attn, vh_window_prompt_attn)
 except ImportError as _e:
     def _unbound(name: str, why: str):
         def call(*args, **kwargs):
@@ -390,8 +410,7 @@ except ImportError as _e:
         call.__name__ = name
         return call
 
-    vh_mrope_kv_append, vh_window_decode_attn, vh_window_prompt_attn = (
-        _unbound(n, str(_e)) for n in ("vh_mrope_kv_append", "vh_window_decode_attn", "vh_window_prompt_attn"))
+    globals().update({n: _unbound(n, str(_e)) for n in _BOUND})
 
 
 def mrope_pair_axis(sections, D: int, cyclic: bool = False) -> list[int]:
@@ -420,3 +439,33 @@ def vh_prompt_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int) -> int:
 def alloc_prompt_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, device=None) -> torch.Tensor:
     """Zero-filled device scratch for vh_window_prompt_attn (torch allocation)."""
     return torch.zeros(vh_prompt_workspace_bytes(T, B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
+
+
+def tree_masks(parents, device=None) -> torch.Tensor:
+    """tree_mask of vh_tree_attn (int64 [T, words]) for the rows' drafted tokens: for
+    every row the sequence of its tokens' parents, each the number of an earlier token of the
+    row, or -1 for a token that follows the context."""
+    parents = [[int(x) for x in row] for row in parents]
+    words = max(1, -(-max((len(row) for row in parents), default=0) // 64))
+    masks = []
+    for row in parents:
+        own = []
+        for i, up in enumerate(row):
+            if not -1 <= up < i:
+                raise ValueError(f"token {i} has the parent {up}: an earlier token of its row, or -1, is needed")
+            own.append((own[up] | 1 << up) if up >= 0 else 0)
+        masks += own
+    signed = [[w - (1 << 64) if w >> 63 else w for w in ((m >> 64 * k) & (1 << 64) - 1 for k in range(words))] for m in masks]
+    return torch.tensor(signed, dtype=torch.int64, device=device or "cuda").view(len(masks), words)
+
+
+def alloc_quant_cache(num_pages: int, page_size: int, Hkv: int, D: int, head_major: bool = False, device=None):
+    """(k_cache, v_cache, k_scale, v_scale) of a zeroed 8-bit cache: float8_e4m3fn views [NP, P, Hkv, D] of
+    pages laid out [2, P, Hkv, D], or with head_major [2, Hkv, P, D], and float32 views [NP, Hkv, P].
+    (Page sizes that are no multiple of 4, which only caches of one page a row have, take padded scales.)"""
+    dev = device or "cuda"
+    shape = (num_pages, 2, Hkv, page_size, D) if head_major else (num_pages, 2, page_size, Hkv, D)
+    pool = torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn)
+    k, v = (pool[:, i].transpose(1, 2) if head_major else pool[:, i] for i in (0, 1))
+    scale = torch.zeros(num_pages, 2, Hkv, -(-page_size // 4) * 4, dtype=torch.float32, device=dev)[..., :page_size]
+    return k, v, scale[:, 0], scale[:, 1]

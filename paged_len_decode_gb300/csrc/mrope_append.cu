@@ -22,6 +22,11 @@
 // where two took 66, and a CTA of 4 tokens with its angles in shared memory
 // behind a barrier 82 us.  Angles gathered beside
 // the row's look-up instead of after it, and weights by 16 bytes: 12.2 -> 10.1 us.
+//
+// Into a cache of 8 bits (Q8) go e4m3_rne(x / s) and the scale s = max |x| / 448 of the head
+// (at least 2^-126), each from the fp32 values before any other rounding: the lanes of a head
+// agree on its largest value, and write 8 bytes a run instead of 16.
+#include "vh_e4m3.cuh"
 #include "vh_ragged.cuh"
 #include "vh_window.h"
 
@@ -33,7 +38,24 @@ constexpr int kThreads = 64;  // (small CTAs: no two warps need each other)
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-template <typename E, int D>
+// Bits of |x|, the largest of a and b: a NaN's are above an infinity's, so neither is lost.
+__device__ __forceinline__ uint32_t larger_bits(uint32_t a, float x) { return max(a, __float_as_uint(x) & 0x7fffffffu); }
+
+// Of 8 values of a head, whose largest has the bits `top` over the `lanes` neighbouring lanes
+// that hold the head: the scale, and the e4m3 values.  (Divisions that round to nearest: a value
+// that another program quantises by the same rule has the same bits.)
+__device__ __forceinline__ float scale_of(uint32_t top, int lanes) {
+  for (int off = 1; off < lanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+  return top >= 0x7f800000u ? __int_as_float(0x7fffffff) : fmaxf(__fdiv_rn(__uint_as_float(top), kE4m3Max), kScaleMin);
+}
+__device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float inv) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = pack_e4m3x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+template <typename E, int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
   constexpr int HALF = D / 2;
   constexpr int UPH = HALF / 8;  // lanes of a head
@@ -126,7 +148,31 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
   if (!page_ok && lane == 0) flag_error(p.err_flag, VH_ERR_PAGE);
   const long long slot_off = static_cast<long long>(page) * p.page_stride + (slot % p.P) * p.token_stride;
 
-  if (page_ok) {
+  [[maybe_unused]] const long long scale_at = static_cast<long long>(page) * p.scale_page + slot % p.P;
+  if constexpr (Q8) {
+    // 8 elements a lane, D / 8 neighbouring lanes a head (every lane runs each round)
+    auto put = [&](int u, const uint4& w) {
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      float x[8];
+      uint32_t top = 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = E::to_float2(ws[k]);
+        x[2 * k] = f.x;
+        x[2 * k + 1] = f.y;
+        top = larger_bits(larger_bits(top, f.x), f.y);
+      }
+      const float scale = scale_of(top, D / 8);
+      if (u >= nv || !page_ok) return;
+      const int h = u / (D / 8), c = u % (D / 8);
+      *reinterpret_cast<uint2*>(p.v8 + slot_off + h * p.head_stride + c * 8) = e4m3x8(x, __frcp_rn(scale));
+      if (c == 0) p.v_scale[scale_at + h * p.scale_head] = scale;
+    };
+#pragma unroll
+    for (int x = 0; x < VU; ++x)
+      if (part * 32 + x * vstep < nv) put(v0 + x * vstep, v0 + x * vstep < nv ? v[x] : make_uint4(0u, 0u, 0u, 0u));
+    for (int u = v0 + VU * vstep; u - lane < nv; u += vstep) put(u, u < nv ? ldg16(vrow + u * 8) : make_uint4(0u, 0u, 0u, 0u));
+  } else if (page_ok) {
     auto to = [&](int u) {
       return reinterpret_cast<uint4*>(p.v_cache + slot_off + (u / (D / 8)) * p.head_stride + (u % (D / 8)) * 8);
     };
@@ -184,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
           }
         }
       }
-      if (h >= heads || !(is_q || page_ok)) continue;
+      if (!Q8 && (h >= heads || !(is_q || page_ok))) continue;
       float o0[8], o1[8];  // the two runs of 8 elements
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -200,6 +246,21 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
         } else {
           o0[k] = rx;
           o1[k] = ry;
+        }
+      }
+      if constexpr (Q8) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) top = larger_bits(larger_bits(top, o0[k]), o1[k]);
+        const float scale = scale_of(top, UPH);
+        if (h >= heads || !(is_q || page_ok)) continue;
+        if (!is_q) {
+          const float inv = __frcp_rn(scale);
+          uint8_t* dst = p.k8 + slot_off + (h - p.Hq) * p.head_stride;
+          *reinterpret_cast<uint2*>(dst + e0) = e4m3x8(o0, inv);
+          *reinterpret_cast<uint2*>(dst + e1) = e4m3x8(o1, inv);
+          if (lane % UPH == 0) p.k_scale[scale_at + (h - p.Hq) * p.scale_head] = scale;
+          continue;
         }
       }
       if (is_q && !p.q16) {
@@ -230,9 +291,12 @@ cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
   // tokens 3.1, 3.1 and 3.8, 2000 14.7, 8.0 and 8.0.
   p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32)));
-  return launch_dependent(p.D == 128 ? (p.f16 ? mrope_kv_append_kernel<ElemF16, 128> : mrope_kv_append_kernel<ElemBf16, 128>)
-                                     : (p.f16 ? mrope_kv_append_kernel<ElemF16, 64> : mrope_kv_append_kernel<ElemBf16, 64>),
-                          p, grid, kThreads, 0, stream);
+  using Kernel = void (*)(MropeParams);
+  const Kernel kernels[8] = {mrope_kv_append_kernel<ElemBf16, 64, false>,  mrope_kv_append_kernel<ElemBf16, 64, true>,
+                             mrope_kv_append_kernel<ElemF16, 64, false>,   mrope_kv_append_kernel<ElemF16, 64, true>,
+                             mrope_kv_append_kernel<ElemBf16, 128, false>, mrope_kv_append_kernel<ElemBf16, 128, true>,
+                             mrope_kv_append_kernel<ElemF16, 128, false>,  mrope_kv_append_kernel<ElemF16, 128, true>};
+  return launch_dependent(kernels[(p.D == 128 ? 4 : 0) + (p.f16 ? 2 : 0) + (p.k8 ? 1 : 0)], p, grid, kThreads, 0, stream);
 }
 
 }  // namespace vh

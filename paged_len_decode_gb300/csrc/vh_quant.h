@@ -1,0 +1,63 @@
+// vh_quant.h -- parameter blocks and launchers of the calls on an 8-bit cache
+// that are not in vh_window.h (internal; the public interface is vh.h).
+#pragma once
+
+#include "vh_window.h"
+
+namespace vh {
+
+// An 8-bit cache as memory: e4m3 values (strides in elements, bytes), and a scale
+// for every slot and head (strides in floats; a page's slots follow one another).
+struct QuantMemory {
+  const uint8_t* k;
+  const uint8_t* v;
+  long long page_stride, token_stride, head_stride;
+  const float* k_scale;
+  const float* v_scale;
+  long long scale_page, scale_head;
+};
+
+bool aligned_quant(const QuantMemory& m);  // (vh_window_api.cu)
+
+struct QuantDecodeParams {
+  QuantMemory memory;
+  const float* q_rot;          // [B][Hq][D]
+  int num_pages;
+  const int32_t* page_table;   // null: contiguous cache
+  int max_pages_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* active;
+  int window, sinks;           // window >= 1 (kNoWindow: none), sinks >= 0
+  uint16_t* out;
+  float scale_log2;            // softmax scale * log2(e)
+  int32_t* err_flag;
+  int f16;                     // of out
+  int B, Hq, Hkv, D, G, P;
+};
+
+struct QuantReadParams {
+  QuantMemory memory;
+  int num_pages;
+  const int32_t* page_table;   // null: contiguous cache
+  int max_pages_per_seq;
+  const int32_t* seq_lens;
+  const int32_t* active;
+  const int32_t* first_slot;   // [B], or null (0)
+  int sinks;
+  uint16_t* k_out;
+  uint16_t* v_out;
+  long long out_page, out_token, out_head;  // strides
+  int out_pages;
+  const int32_t* out_table;
+  int out_per_row;
+  int32_t* err_flag;
+  int f16;
+  int B, Hkv, D, P, out_P;
+  int ctas;
+};
+
+cudaError_t prepare_quant_read(int max_smem);
+cudaError_t launch_quant_read(const QuantReadParams& p, cudaStream_t stream);
+cudaError_t launch_quant_decode(const QuantDecodeParams& p, cudaStream_t stream);
+
+}  // namespace vh

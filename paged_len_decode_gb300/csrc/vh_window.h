@@ -30,6 +30,10 @@ struct MropeParams {
   uint16_t* k_cache;
   uint16_t* v_cache;
   long long page_stride, token_stride, head_stride;
+  // a cache of 8 bits instead: e4m3 values with the same strides, and a scale for every slot and head
+  uint8_t *k8, *v8;            // null: the cache has 16 bits
+  float *k_scale, *v_scale;
+  long long scale_page, scale_head;  // strides; a page's slots follow one another
   int num_pages;
   const int32_t* page_table;   // null: contiguous cache
   int max_pages_per_seq;
@@ -96,6 +100,8 @@ struct PromptParams {
   const int32_t* token_start;
   const int32_t* seq_lens;
   const int32_t* active;
+  const uint32_t* tree_mask;   // [T][mask_words] (the tree's kernels)
+  int mask_words;
   int window, sinks;
   uint16_t* out;
   float scale_log2;
@@ -132,6 +138,13 @@ inline cudaError_t launch_dependent(void (*kernel)(P), const P& p, dim3 grid, in
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Checks and tensor maps that the calls on ragged batches and 8-bit caches share
+// (vh_window_api.cu).
+bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                 int num_pages, const int32_t* page_table, int max_pages_per_seq);
+bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
+
 cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
@@ -139,5 +152,7 @@ cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t strea
 // once per device, every variant; clusters[x]: clusters of 2^x CTAs that run at a time
 cudaError_t prepare_window_prompt(int (&clusters)[5]);
 cudaError_t launch_window_prompt(const PromptParams& p, cudaStream_t stream);
+cudaError_t prepare_tree_attn(int (&clusters)[5]);
+cudaError_t launch_tree_attn(const PromptParams& p, cudaStream_t stream);
 
 }  // namespace vh

@@ -13,17 +13,59 @@
 
 #include "../../include/vh.h"
 #include "vh_plan.h"
-#include "vh_window.h"
+#include "vh_quant.h"
+
+namespace {
+
+// The driver's tensor-map encoder, looked up once through the runtime.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    cudaGetLastError();
+    return nullptr;
+  }();
+  return fn;
+}
+
+}  // namespace
+
+namespace vh {
+
+// Scalars that every call checks alike.
+bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                 int num_pages, const int32_t* page_table, int max_pages_per_seq) {
+  return valid_shape(B, Hq, Hkv, D, P) && num_pages >= 1 && page_stride >= 1 && token_stride >= 1 &&
+         head_stride >= 1 && valid_paging(P, max_pages_per_seq) && !too_many_tiles(B, max_pages_per_seq, P) &&
+         valid_table(page_table, B, max_pages_per_seq, num_pages);
+}
+
+bool aligned_quant(const QuantMemory& m) {
+  return aligned16(m.k) && aligned16(m.v) && aligned16(m.k_scale) && aligned16(m.v_scale) && m.page_stride % 16 == 0 &&
+         m.token_stride % 16 == 0 && m.head_stride % 16 == 0 && m.scale_page % 4 == 0 && m.scale_head % 4 == 0;
+}
+
+bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
+                  const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc && enc(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, one,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace vh
 
 namespace {
 
 using vh::DeviceInfo;
 using vh::aligned16;
 using vh::device_info;
-using vh::too_many_tiles;
-using vh::valid_paging;
+using vh::valid_cache;
 using vh::valid_shape;
-using vh::valid_table;
 using vh::kMaxDevices;
 
 constexpr int kMaxHc = 8;
@@ -38,18 +80,29 @@ struct Prepared {
   int clusters[5] = {};  // clusters of 2^x CTAs of the prompt kernel that run at a time
 };
 Prepared g_prepared[kMaxDevices];
+Prepared g_tree[kMaxDevices];  // the tree's kernels
 
-bool prepared(const DeviceInfo& dev) {
-  Prepared& s = g_prepared[dev.index];
+template <typename F>
+bool prepared(Prepared& s, F prepare) {
   if (s.ok.load(std::memory_order_acquire)) return true;
   std::lock_guard<std::mutex> lk(s.mu);
   if (s.ok.load(std::memory_order_relaxed)) return true;
-  if (vh::prepare_window_decode(dev.smem_optin) != cudaSuccess || vh::prepare_window_prompt(s.clusters) != cudaSuccess) {
+  if (!prepare(s)) {
     cudaGetLastError();
     return false;
   }
   s.ok.store(true, std::memory_order_release);
   return true;
+}
+
+bool prepared(const DeviceInfo& dev) {
+  return prepared(g_prepared[dev.index], [&](Prepared& s) {
+    return vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(s.clusters) == cudaSuccess;
+  });
+}
+
+bool prepared_tree(const DeviceInfo& dev) {
+  return prepared(g_tree[dev.index], [](Prepared& s) { return vh::prepare_tree_attn(s.clusters) == cudaSuccess; });
 }
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -162,39 +215,13 @@ int useful_ctas(const vh::WindowDecodeParams& p, int max_pages_per_seq) {
   return static_cast<int>(std::min<long long>(65535, (p.B * row + q - 1) / q));
 }
 
-// Scalars that every call of this file checks alike.
-bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int64_t token_stride, int64_t head_stride,
-                 int num_pages, const int32_t* page_table, int max_pages_per_seq) {
-  return valid_shape(B, Hq, Hkv, D, P) && num_pages >= 1 && page_stride >= 1 && token_stride >= 1 &&
-         head_stride >= 1 && valid_paging(P, max_pages_per_seq) && !too_many_tiles(B, max_pages_per_seq, P) &&
-         valid_table(page_table, B, max_pages_per_seq, num_pages);
-}
-
 bool aligned_cache(const void* k, const void* v, int64_t page_stride, int64_t token_stride, int64_t head_stride) {
   return aligned16(k) && aligned16(v) && page_stride % 8 == 0 && token_stride % 8 == 0 && head_stride % 8 == 0;
 }
 
-// The driver's tensor-map encoder, looked up once through the runtime.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    cudaGetLastError();
-    return nullptr;
-  }();
-  return fn;
-}
-
 bool encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
             const cuuint32_t* box) {
-  const PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return enc && enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides,
-                    box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return vh::encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, base, rank, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Tensor maps of the prompt kernel.  A K or V box is a run of tokens that
@@ -254,6 +281,109 @@ int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? VH_OK : VH_ECUDA; }
 
+// Both appends: p holds the arguments as they came.
+int append(vh::MropeParams& p, const uint8_t* pair_axis, unsigned flags, void* stream) {
+  if ((flags & ~(VH_FLAG_FP16 | VH_FLAG_ROPE_INTERLEAVED | VH_FLAG_Q16)) != 0 || p.T < 0 || p.max_pos < 1 ||
+      p.num_axes < 1 || p.num_axes > 4 || !(p.norm_eps >= 0.f) || !(p.norm_eps < 1e30f) ||
+      !valid_cache(p.B, p.Hq, p.Hkv, p.D, p.P, p.page_stride, p.token_stride, p.head_stride, p.num_pages, p.page_table,
+                   p.max_pages_per_seq) ||
+      (!p.token_start && p.T != p.B) || p.q_stride < static_cast<int64_t>(p.Hq) * p.D ||
+      p.k_stride < static_cast<int64_t>(p.Hkv) * p.D || p.v_stride < static_cast<int64_t>(p.Hkv) * p.D)
+    return VH_EINVAL;
+  if (pair_axis)
+    for (int i = 0; i < p.D / 2; ++i) {
+      if (pair_axis[i] >= p.num_axes) return VH_EINVAL;
+      p.axis[i >> 5] |= static_cast<unsigned long long>(pair_axis[i]) << (2 * (i & 31));
+    }
+  if (p.T == 0) return VH_OK;
+  const bool q8 = p.k_cache == nullptr;
+  const void *k = q8 ? static_cast<const void*>(p.k8) : p.k_cache, *v = q8 ? static_cast<const void*>(p.v8) : p.v_cache;
+  if (!p.q || !p.k_new || !p.v_new || !p.cos_sin || !k || !v || !p.seq_lens || !p.active || !p.q_rot) return VH_EINVAL;
+  if (!aligned16(p.q) || !aligned16(p.k_new) || !aligned16(p.v_new) || !aligned16(p.cos_sin) || !aligned16(p.q_rot) ||
+      !aligned16(p.q_norm_w) || !aligned16(p.k_norm_w) || p.q_stride % 8 != 0 || p.k_stride % 8 != 0 || p.v_stride % 8 != 0)
+    return VH_EALIGN;
+  if (q8 ? !vh::aligned_quant({p.k8, p.v8, p.page_stride, p.token_stride, p.head_stride, p.k_scale, p.v_scale, p.scale_page, p.scale_head})
+         : !aligned_cache(k, v, p.page_stride, p.token_stride, p.head_stride))
+    return VH_EALIGN;
+  if (!device_info()) return VH_ENODEV;
+  p.q16 = (flags & VH_FLAG_Q16) != 0;
+  p.rope_interleaved = (flags & VH_FLAG_ROPE_INTERLEAVED) != 0;
+  p.f16 = (flags & VH_FLAG_FP16) != 0;
+  return status_of(vh::launch_mrope_kv_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+// Both calls on ragged batches: with tree_mask, the drafted tokens' ancestors instead of all earlier ones.
+int prompt(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
+                          int64_t token_stride, int64_t head_stride, int num_pages, const int32_t* page_table,
+                          int max_pages_per_seq, const int32_t* token_start, const int32_t* seq_lens,
+                          const int32_t* active, const int64_t* tree_mask, int mask_words, int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
+                          void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B,
+                          int Hq, int Hkv, int D, int page_size, void* stream) {
+  if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 16 ||
+      (num_splits & (num_splits - 1)) != 0 || mask_words < 0 ||
+      !(sm_scale == sm_scale) ||
+      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
+                   max_pages_per_seq))
+    return VH_EINVAL;
+  if (T == 0) return VH_OK;
+  if (mask_words && !tree_mask) return VH_EINVAL;
+  if (!q || !k_cache || !v_cache || !token_start || !seq_lens || !active || !out) return VH_EINVAL;
+  if (reinterpret_cast<uintptr_t>(tree_mask) % 8 != 0) return VH_EALIGN;
+  if (!aligned16(q) || !aligned16(out) || !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
+    return VH_EALIGN;
+  if (!workspace) return VH_EWORKSPACE;
+  if (!aligned16(workspace)) return VH_EALIGN;
+  const DeviceInfo* dev = device_info();
+  if (!dev || !(mask_words ? prepared_tree(*dev) : prepared(*dev))) return VH_ENODEV;
+  if (workspace_bytes < vh_prompt_workspace_bytes(T, B, Hq, Hkv, D)) return VH_EWORKSPACE;
+  vh::PromptParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.token_start = token_start;
+  p.seq_lens = seq_lens;
+  p.active = active;
+  p.tree_mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.mask_words = 2 * mask_words;
+  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
+  p.sinks = std::min(sinks, vh::kNoWindow);
+  p.out = out;
+  const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D));
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.err_flag = err_flag;
+  p.f16 = (flags & VH_FLAG_FP16) != 0;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.G = Hq / Hkv;
+  p.P = page_size;
+  const int(&clusters)[5] = (mask_words ? g_tree : g_prepared)[dev->index].clusters;
+  p.shift_g = __builtin_ctz(p.G);
+  p.pair = small_blocks(T, B, p.G, Hkv, *dev);
+  p.shift_block = (p.pair ? 7 : 8) - p.shift_g;
+  p.splits = num_splits > 0 ? num_splits : prompt_splits(p, clusters);
+  while (p.splits > 1 && clusters[__builtin_ctz(p.splits)] < 1) p.splits /= 2;
+  const long long blocks = (static_cast<long long>(T) >> p.shift_block) + B, units = blocks * Hkv * p.splits;
+  if (units > INT32_MAX / 2 || blocks * Hkv > (1LL << 32) / Hkv - 1 || !encode_prompt_maps(p)) return VH_EINVAL;
+  p.shift_splits = __builtin_ctz(p.splits);
+  p.shift_page = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(page_size) : -1;
+  p.hkv_inverse = Hkv == 1 ? 0u : static_cast<uint32_t>(((1ULL << 32) + Hkv - 1) / Hkv);
+  p.blocks = static_cast<int>(blocks);
+  // CTAs draw units one after the other; a cluster's CTAs have one each
+  p.ctas = static_cast<int>(p.splits > 1 ? units : std::min<long long>(units, dev->sm_count));
+  p.counter = static_cast<int*>(workspace);
+  return status_of(mask_words ? vh::launch_tree_attn(p, static_cast<cudaStream_t>(stream))
+                              : vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -266,26 +396,8 @@ int vh_mrope_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new
                        const int32_t* token_start, const int32_t* seq_lens, const int32_t* active, void* q_rot,
                        int32_t* err_flag, unsigned flags, int T, int B, int Hq, int Hkv, int D, int page_size,
                        void* stream) {
-  if ((flags & ~(VH_FLAG_FP16 | VH_FLAG_ROPE_INTERLEAVED | VH_FLAG_Q16)) != 0 || T < 0 || max_pos < 1 ||
-      num_axes < 1 || num_axes > 4 || !(norm_eps >= 0.f) || !(norm_eps < 1e30f) ||
-      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
-                   max_pages_per_seq) ||
-      (!token_start && T != B) || q_stride < static_cast<int64_t>(Hq) * D || k_stride < static_cast<int64_t>(Hkv) * D ||
-      v_stride < static_cast<int64_t>(Hkv) * D)
-    return VH_EINVAL;
+  if (T != 0 && (!k_cache || !v_cache)) return VH_EINVAL;
   vh::MropeParams p{};
-  if (pair_axis)
-    for (int i = 0; i < D / 2; ++i) {
-      if (pair_axis[i] >= num_axes) return VH_EINVAL;
-      p.axis[i >> 5] |= static_cast<unsigned long long>(pair_axis[i]) << (2 * (i & 31));
-    }
-  if (T == 0) return VH_OK;
-  if (!q || !k_new || !v_new || !cos_sin || !k_cache || !v_cache || !seq_lens || !active || !q_rot) return VH_EINVAL;
-  if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(cos_sin) || !aligned16(q_rot) ||
-      !aligned16(q_norm_w) || !aligned16(k_norm_w) || q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 ||
-      !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
-    return VH_EALIGN;
-  if (!device_info()) return VH_ENODEV;
   p.q = q;
   p.k_new = k_new;
   p.v_new = v_new;
@@ -311,9 +423,6 @@ int vh_mrope_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new
   p.seq_lens = seq_lens;
   p.active = active;
   p.q_rot = q_rot;
-  p.q16 = (flags & VH_FLAG_Q16) != 0;
-  p.rope_interleaved = (flags & VH_FLAG_ROPE_INTERLEAVED) != 0;
-  p.f16 = (flags & VH_FLAG_FP16) != 0;
   p.err_flag = err_flag;
   p.T = T;
   p.B = B;
@@ -321,7 +430,58 @@ int vh_mrope_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new
   p.Hkv = Hkv;
   p.D = D;
   p.P = page_size;
-  return status_of(vh::launch_mrope_kv_append(p, static_cast<cudaStream_t>(stream)));
+  return append(p, pair_axis, flags, stream);
+}
+
+int vh_quant_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new, int64_t q_stride, int64_t k_stride,
+                       int64_t v_stride, const float* cos_sin, int max_pos, const int32_t* positions,
+                       const uint8_t* pair_axis, int num_axes, const float* q_norm_w, const float* k_norm_w,
+                       float norm_eps, vh_e4m3* k_cache, vh_e4m3* v_cache, int64_t page_stride, int64_t token_stride,
+                       int64_t head_stride, float* k_scale, float* v_scale, int64_t scale_page_stride,
+                       int64_t scale_head_stride, int num_pages, const int32_t* page_table, int max_pages_per_seq,
+                       const int32_t* token_start, const int32_t* seq_lens, const int32_t* active, void* q_rot,
+                       int32_t* err_flag, unsigned flags, int T, int B, int Hq, int Hkv, int D, int page_size,
+                       void* stream) {
+  if (scale_page_stride < 1 || scale_head_stride < 1 || (T != 0 && (!k_cache || !v_cache || !k_scale || !v_scale)))
+    return VH_EINVAL;
+  vh::MropeParams p{};
+  p.q = q;
+  p.k_new = k_new;
+  p.v_new = v_new;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.positions = positions;
+  p.num_axes = num_axes;
+  p.q_norm_w = q_norm_w;
+  p.k_norm_w = k_norm_w;
+  p.norm_eps = norm_eps;
+  p.k8 = k_cache;
+  p.v8 = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.scale_page = scale_page_stride;
+  p.scale_head = scale_head_stride;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.num_pages = num_pages;
+  p.page_table = page_table;
+  p.max_pages_per_seq = max_pages_per_seq;
+  p.token_start = token_start;
+  p.seq_lens = seq_lens;
+  p.active = active;
+  p.q_rot = q_rot;
+  p.err_flag = err_flag;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.P = page_size;
+  return append(p, pair_axis, flags, stream);
 }
 
 int vh_window_decode_attn(const float* q_rot, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
@@ -406,64 +566,21 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
                           const int32_t* active, int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
                           void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B,
                           int Hq, int Hkv, int D, int page_size, void* stream) {
-  if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 16 ||
-      (num_splits & (num_splits - 1)) != 0 ||
-      !(sm_scale == sm_scale) ||
-      !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
-                   max_pages_per_seq))
-    return VH_EINVAL;
-  if (T == 0) return VH_OK;
-  if (!q || !k_cache || !v_cache || !token_start || !seq_lens || !active || !out) return VH_EINVAL;
-  if (!aligned16(q) || !aligned16(out) || !aligned_cache(k_cache, v_cache, page_stride, token_stride, head_stride))
-    return VH_EALIGN;
-  if (!workspace) return VH_EWORKSPACE;
-  if (!aligned16(workspace)) return VH_EALIGN;
-  const DeviceInfo* dev = device_info();
-  if (!dev || !prepared(*dev)) return VH_ENODEV;
-  if (workspace_bytes < vh_prompt_workspace_bytes(T, B, Hq, Hkv, D)) return VH_EWORKSPACE;
-  vh::PromptParams p{};
-  p.q = q;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
-  p.page_stride = page_stride;
-  p.token_stride = token_stride;
-  p.head_stride = head_stride;
-  p.num_pages = num_pages;
-  p.page_table = page_table;
-  p.max_pages_per_seq = max_pages_per_seq;
-  p.token_start = token_start;
-  p.seq_lens = seq_lens;
-  p.active = active;
-  p.window = window > 0 ? std::min(window, vh::kNoWindow) : vh::kNoWindow;
-  p.sinks = std::min(sinks, vh::kNoWindow);
-  p.out = out;
-  const float scale = sm_scale > 0.f ? sm_scale : 1.0f / sqrtf(static_cast<float>(D));
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.err_flag = err_flag;
-  p.f16 = (flags & VH_FLAG_FP16) != 0;
-  p.T = T;
-  p.B = B;
-  p.Hq = Hq;
-  p.Hkv = Hkv;
-  p.D = D;
-  p.G = Hq / Hkv;
-  p.P = page_size;
-  const int(&clusters)[5] = g_prepared[dev->index].clusters;
-  p.shift_g = __builtin_ctz(p.G);
-  p.pair = small_blocks(T, B, p.G, Hkv, *dev);
-  p.shift_block = (p.pair ? 7 : 8) - p.shift_g;
-  p.splits = num_splits > 0 ? num_splits : prompt_splits(p, clusters);
-  while (p.splits > 1 && clusters[__builtin_ctz(p.splits)] < 1) p.splits /= 2;
-  const long long blocks = (static_cast<long long>(T) >> p.shift_block) + B, units = blocks * Hkv * p.splits;
-  if (units > INT32_MAX / 2 || blocks * Hkv > (1LL << 32) / Hkv - 1 || !encode_prompt_maps(p)) return VH_EINVAL;
-  p.shift_splits = __builtin_ctz(p.splits);
-  p.shift_page = (page_size & (page_size - 1)) == 0 ? __builtin_ctz(page_size) : -1;
-  p.hkv_inverse = Hkv == 1 ? 0u : static_cast<uint32_t>(((1ULL << 32) + Hkv - 1) / Hkv);
-  p.blocks = static_cast<int>(blocks);
-  // CTAs draw units one after the other; a cluster's CTAs have one each
-  p.ctas = static_cast<int>(p.splits > 1 ? units : std::min<long long>(units, dev->sm_count));
-  p.counter = static_cast<int*>(workspace);
-  return status_of(vh::launch_window_prompt(p, static_cast<cudaStream_t>(stream)));
+  return prompt(q, k_cache, v_cache, page_stride, token_stride, head_stride, num_pages, page_table, max_pages_per_seq,
+                token_start, seq_lens, active, nullptr, 0, window, sinks, out, sm_scale, num_splits, workspace,
+                workspace_bytes, err_flag, flags, T, B, Hq, Hkv, D, page_size, stream);
+}
+
+int vh_tree_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride, int64_t token_stride,
+                 int64_t head_stride, int num_pages, const int32_t* page_table, int max_pages_per_seq,
+                 const int32_t* token_start, const int32_t* seq_lens, const int32_t* active, const int64_t* tree_mask,
+                 int mask_words, int window, int sinks, vh_e16* out, float sm_scale, int num_splits, void* workspace,
+                 size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B, int Hq, int Hkv, int D,
+                 int page_size, void* stream) {
+  if (mask_words < 1 || mask_words > VH_TREE_WORDS_MAX) return VH_EINVAL;
+  return prompt(q, k_cache, v_cache, page_stride, token_stride, head_stride, num_pages, page_table, max_pages_per_seq,
+                token_start, seq_lens, active, tree_mask, mask_words, window, sinks, out, sm_scale, num_splits, workspace,
+                workspace_bytes, err_flag, flags, T, B, Hq, Hkv, D, page_size, stream);
 }
 
 }  // extern "C"
