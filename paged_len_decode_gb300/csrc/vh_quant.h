@@ -20,7 +20,10 @@ struct QuantMemory {
 bool aligned_quant(const QuantMemory& m);  // (vh_window_api.cu)
 
 struct QuantDecodeParams {
-  QuantMemory memory;
+  // K and V as 4-D tensors (head_dim, token, kv head, page), boxes of D x 16 tokens x Hc heads,
+  // and their scales as 3-D ones (token, kv head, page), boxes of 16 tokens x Hc heads; of 8
+  // tokens where pages have 8
+  CUtensorMap tmap_k, tmap_v, tmap_ks, tmap_vs;
   const float* q_rot;          // [B][Hq][D]
   int num_pages;
   const int32_t* page_table;   // null: contiguous cache
@@ -30,10 +33,21 @@ struct QuantDecodeParams {
   int window, sinks;           // window >= 1 (kNoWindow: none), sinks >= 0
   uint16_t* out;
   float scale_log2;            // softmax scale * log2(e)
+  int* counters;               // [groups][B] pieces delivered per row; zero between calls
+  float* part_o;               // [groups][N][2][Hc*G][D]
+  float* part_lse;             // [groups][N][2][Hc*G], base 2
   int32_t* err_flag;
   int f16;                     // of out
+  int early;                   // VH_FLAG_PDL: lengths, flags and page ids are read before the dependency wait
   int B, Hq, Hkv, D, G, P;
+  int Hc, groups, N, stages;
+  int stage_bytes;             // K and V of one tile [Hc][16][D], their scales (scale_bytes each)
+  int scale_bytes;
+  int q_off, cum_off, len_off, bar_off, smem_bytes;
 };
+
+// What a row's piece costs in the merge, by q head of a kv head, in the time that a CTA takes for a tile.
+constexpr float kQuantPiece = 0.05f;
 
 struct QuantReadParams {
   QuantMemory memory;
@@ -58,6 +72,8 @@ struct QuantReadParams {
 
 cudaError_t prepare_quant_read(int max_smem);
 cudaError_t launch_quant_read(const QuantReadParams& p, cudaStream_t stream);
+cudaError_t prepare_quant_decode(int max_smem);  // once per device, every variant
+cudaError_t quant_decode_occupancy(const QuantDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_quant_decode(const QuantDecodeParams& p, cudaStream_t stream);
 
 }  // namespace vh

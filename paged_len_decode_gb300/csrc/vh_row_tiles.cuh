@@ -70,4 +70,80 @@ __device__ __forceinline__ int row_of(const int* cum, int lo, int B, int t) {
   return lo;
 }
 
+// cum[0 .. B]: prefix sums of count_row(b) over the rows, and *most the largest of them (cum[0] and
+// *most are 0 and the warp `mine` is synchronised).  Up to kWarpRows rows are counted and summed by
+// that warp, which goes on to its first copies while the others wait for the sums; more rows
+// by all threads.  (Hardware barrier 2.)
+template <int kWarpRows, typename Count>
+__device__ __forceinline__ void sum_rows(int B, int* cum, int* most_of, int* tot, bool mine, Count count_row) {
+  const int lane = threadIdx.x & 31;
+  if (B > kWarpRows) {
+    __syncthreads();
+    int most = 0;
+    for (int b = threadIdx.x; b < B; b += blockDim.x) {
+      const int n = count_row(b);
+      cum[1 + b] = n;
+      most = max(most, n);
+    }
+    atomicMax(most_of, most);
+    __syncthreads();
+    scan_rows(cum, B, tot);
+  } else if (mine) {
+    int n[kWarpRows / 32], run = 0;
+#pragma unroll
+    for (int x = 0; x < kWarpRows / 32; ++x) n[x] = x * 32 + lane < B ? count_row(x * 32 + lane) : 0;
+#pragma unroll
+    for (int x = 0; x < kWarpRows / 32; ++x) {
+      if (x * 32 >= B) break;
+      int v = n[x];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += y;
+      }
+      v += run;
+      if (x * 32 + lane < B) cum[1 + x * 32 + lane] = v;
+      run = __shfl_sync(0xffffffffu, v, 31);
+    }
+    int most = 0;
+#pragma unroll
+    for (int x = 0; x < kWarpRows / 32; ++x) most = max(most, n[x]);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) *most_of = most;
+    __syncwarp();
+    asm volatile("bar.arrive 2, %0;" ::"r"(static_cast<int>(blockDim.x)) : "memory");
+  } else {
+    named_sync(2, blockDim.x);
+  }
+}
+
+// What CTA c of N takes of the list: tiles t0 .. t1 - 1, from row b0 (or a later one) on.
+struct Share {
+  int n_eff;       // CTAs that share the tiles; 0: whole rows a CTA
+  int t0, t1, b0;
+};
+
+// Either T / n tiles each, of which a CTA takes at least q: it reads a tile in some time, and the
+// longest row's pieces, R / q of them, are then added at `piece` times that each, so q = sqrt(R
+// piece) is the least of both; or whole rows, which need no merge: that takes about as long as 6 tiles.
+__device__ __forceinline__ Share share_of_cta(const int* cum, int B, int c, int N, int most, float piece) {
+  const int T = cum[B];
+  const int q = max(1, static_cast<int>(sqrtf(static_cast<float>(most) * piece) + 0.5f));
+  const int rows_each = (B + N - 1) / N;
+  const bool by_row = most * rows_each <= max(q, T / N) + 6;
+  Share s;
+  s.n_eff = by_row ? 0 : min(N, (T + q - 1) / q);
+  s.t0 = s.t1 = s.b0 = 0;
+  if (by_row) {
+    s.b0 = min(c * rows_each, B);
+    s.t0 = cum[s.b0];
+    s.t1 = cum[min(s.b0 + rows_each, B)];
+  } else if (c < s.n_eff) {
+    const int each = T / s.n_eff, rest = T - each * s.n_eff;  // the first `rest` CTAs take one tile more
+    s.t0 = c * each + min(c, rest);
+    s.t1 = s.t0 + each + (c < rest ? 1 : 0);
+  }
+  return s;
+}
+
 }  // namespace vh

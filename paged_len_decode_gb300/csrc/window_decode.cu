@@ -202,68 +202,14 @@ __global__ void __launch_bounds__(kThreadsMax, 1) window_decode_kernel(const __g
       cum[0] = 0;
     }
     __syncwarp();
-    if (p.B <= kWarpRows) {
-      int n[kWarpRows / 32], run = 0;
-#pragma unroll
-      for (int x = 0; x < kWarpRows / 32; ++x) n[x] = x * 32 + lane < p.B ? count_row(x * 32 + lane) : 0;
-#pragma unroll
-      for (int x = 0; x < kWarpRows / 32; ++x) {
-        if (x * 32 >= p.B) break;
-        int v = n[x];
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, v, off);
-          if (lane >= off) v += y;
-        }
-        v += run;
-        if (x * 32 + lane < p.B) cum[1 + x * 32 + lane] = v;
-        run = __shfl_sync(0xffffffffu, v, 31);
-      }
-      int most = 0;
-#pragma unroll
-      for (int x = 0; x < kWarpRows / 32; ++x) most = max(most, n[x]);
-      most = __reduce_max_sync(0xffffffffu, most);
-      if (lane == 0) misc[kMiscMost] = most;
-      __syncwarp();
-      asm volatile("bar.arrive 2, %0;" ::"r"(static_cast<int>(blockDim.x)) : "memory");
-    }
-  } else if (p.B <= kWarpRows) {
-    named_sync(2, blockDim.x);
   }
-  if (p.B > kWarpRows) {
-    __syncthreads();
-    int most = 0;
-    for (int b = tid; b < p.B; b += blockDim.x) {
-      const int n = count_row(b);
-      cum[1 + b] = n;
-      most = max(most, n);
-    }
-    atomicMax(misc + kMiscMost, most);
-    __syncthreads();
-    scan_rows(cum, p.B, misc + kMiscTot);
-  }
+  sum_rows<kWarpRows>(p.B, cum, misc + kMiscMost, misc + kMiscTot, warp == Hc, count_row);
   const int T = cum[p.B];
-  // Shares: either T / n tiles each, of which a CTA takes at least q (a share streams
-  // in about 0.5 us a tile, and the longest row's pieces, R / q of them, are then added
-  // at about G / 40 us each, so q = sqrt(R G / 20) is the least of both; one row of 8000
-  // tokens, 8 q heads of one kv head: 179 us with q = 1, 23 us with q = 14), or whole
-  // rows, which need no merge: that takes 2.5 us (4.8 us against 7.3 for a few rows of
-  // a tile or two), as long as 6 tiles.
-  const int most = misc[kMiscMost];
-  const int q = max(1, static_cast<int>(sqrtf(static_cast<float>(most) * (0.05f * G)) + 0.5f));
-  const int rows_each = (p.B + p.N - 1) / p.N;
-  const bool by_row = most * rows_each <= max(q, T / p.N) + 6;
-  const int n_eff = by_row ? 0 : min(p.N, (T + q - 1) / q);  // CTAs that share the tiles
-  int t0 = 0, t1 = 0, b0 = 0;
-  if (by_row) {
-    b0 = min(c * rows_each, p.B);
-    t0 = cum[b0];
-    t1 = cum[min(b0 + rows_each, p.B)];
-  } else if (c < n_eff) {
-    const int each = T / n_eff, rest = T - each * n_eff;  // the first `rest` CTAs take one tile more
-    t0 = c * each + min(c, rest);
-    t1 = t0 + each + (c < rest ? 1 : 0);
-  }
+  // (a share streams in about 0.5 us a tile, and pieces are added at about G / 40 us each; one row
+  // of 8000 tokens, 8 q heads of one kv head: 179 us with one tile a CTA at least, 23 us with 14)
+  const Share share = share_of_cta(cum, p.B, c, p.N, misc[kMiscMost], 0.05f * G);
+  const int n_eff = share.n_eff, t0 = share.t0, t1 = share.t1;
+  int b0 = share.b0;
   const bool works = t1 > t0;
   if (works) b0 = row_of(cum, b0, p.B, t0);
   const int tpp = (p.P + kTile - 1) / kTile;  // tiles of a page
