@@ -38,8 +38,8 @@ namespace vh {
 
 namespace {
 
-constexpr int kMaxHeads = 8;                 // kv heads (consumer warps) of a CTA
-constexpr int kThreadsMax = 32 * (kMaxHeads + 1);
+template <int D>
+constexpr int kHeadsMost = 512 / D;          // kv heads (consumer warps) of a CTA
 constexpr int kWarpRows = 128;               // rows that the producer warp sums up alone
 enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscMost = 34, kMiscPart = 36, kMiscInts = 48 };  // part: 4 ints each
 constexpr float kGrow = 8.f;                 // log2 of the weight that raises the maximum
@@ -69,7 +69,7 @@ __device__ __forceinline__ float sum_of_keys(float x) {
 }
 
 template <int D, int G, typename E>
-__global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __grid_constant__ QuantDecodeParams p) {
+__global__ void __launch_bounds__(32 * (kHeadsMost<D> + 1), D == 128 ? 2 : 1) quant_decode_kernel(const __grid_constant__ QuantDecodeParams p) {
   constexpr int KS = D / 16;      // k-steps of the score product = m-tiles of the value product
   constexpr int CH = D / 16;      // 16-byte chunks of a key
   constexpr int PER = D / 32;
@@ -81,10 +81,11 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
   int* cum = reinterpret_cast<int*>(smem + p.cum_off);
   int* lens = reinterpret_cast<int*>(smem + p.len_off);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.bar_off);
-  int* misc = reinterpret_cast<int*>(bars + 2 * S + 2);
+  int* misc = reinterpret_cast<int*>(bars + 2 * S + 2 + kHeadsMost<D>);
   volatile int* abort_flag = misc + kMiscAbort;
   const uint32_t full0 = smem_addr(bars), empty0 = smem_addr(bars + S);
   const uint32_t qfull = smem_addr(bars + 2 * S), qempty = smem_addr(bars + 2 * S + 1);
+  const uint32_t merged0 = smem_addr(bars + 2 * S + 2);  // pieces have come, by consumer warp
   const int max_len = p.max_pages_per_seq * p.P;
   const bool p8 = p.P == 8;
   const float NEG_INF = __int_as_float(0xff800000);
@@ -115,6 +116,7 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
       }
       mbar_init(qfull, 1);
       mbar_init(qempty, Hc);
+      for (int x = 0; x < Hc; ++x) mbar_init(merged0 + 8 * x, 1);
       fence_barrier_init();
       cum[0] = 0;
     }
@@ -259,7 +261,16 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
   int nseg = 0, stage = 0, round = 0, npart = 0;
   int part_row[2];
   bool lost = false;
-  for (int t = t0; t < t1 && !lost; ++t) {
+  auto rescale = [&](float by0, float by1) {
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt) {
+      acc[mt][0] *= by0;
+      acc[mt][1] *= by1;
+      acc[mt][2] *= by0;
+      acc[mt][3] *= by1;
+    }
+  };
+  for (int t = t0; t < t1 && !lost;) {
     const bool next_row = t >= rt1;
     if (next_row) {
       do {
@@ -308,55 +319,87 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
 #pragma unroll
       for (int mt = 0; mt < KS; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
     }
-    const uint32_t mask = visible16(rt.tile(t - rt0), lens[b], p.window, p.sinks);
-    if (!mbar_wait(full0 + 8 * stage, round & 1)) {
+
+    // Two tiles at a time, x = 0 and 1.  Where the share of a row has an odd number, the last
+    // one stands in both places, invisible in the second.
+    const int k0 = t - rt0;
+    const bool two = t + 1 < min(t1, rt1);
+    const int stage1 = !two ? stage : (stage + 1 == S ? 0 : stage + 1);
+    const uint32_t round1 = two && stage1 == 0 ? round + 1 : round;
+    if (!mbar_wait(full0 + 8 * stage, round & 1) || !mbar_wait(full0 + 8 * stage1, round1 & 1)) {
       lost = true;
       break;
     }
-    const uint32_t stg = smem_addr(smem) + static_cast<uint32_t>(stage * p.stage_bytes);
-    if (mask != 0xFFFFu) {
-      // rows of V that are not visible meet the weight 0: make them zeros
-      for (int x = lane; x < kTile * CH; x += 32) {
-        const int r = x / CH;
-        if ((mask >> r) & 1u) continue;
-        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stg + tile_bytes + w * head_bytes + (r >> 3) * half_bytes + (r & 7) * D + (x % CH) * 16),
-                     "r"(0u)
-                     : "memory");
+    const uint32_t stg[2] = {smem_addr(smem) + static_cast<uint32_t>(stage * p.stage_bytes), smem_addr(smem) + static_cast<uint32_t>(stage1 * p.stage_bytes)};
+    // what is seen ends in a row's last tile, in its last tile of sinks or in the one behind them
+    uint32_t mask[2] = {0xFFFFu, two ? 0xFFFFu : 0u};
+    const bool edge = !two || k0 + 2 >= rt.count || (k0 <= rt.sink && k0 + 2 >= rt.sink);
+    if (edge) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x == 1 && !two) continue;
+        mask[x] = visible16(rt.tile(k0 + x), lens[b], p.window, p.sinks);
+        // rows of V that are not visible meet the weight 0: make them zeros
+        for (int y = lane; y < kTile * CH && mask[x] != 0xFFFFu; y += 32) {
+          const int r = y / CH;
+          if ((mask[x] >> r) & 1u) continue;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stg[x] + tile_bytes + w * head_bytes + (r >> 3) * half_bytes + (r & 7) * D + (y % CH) * 16),
+                       "r"(0u)
+                       : "memory");
+        }
       }
       __syncwarp();
     }
 
-    // scores: lane holds keys g4 and g4 + 8, heads 2 t4 and 2 t4 + 1
-    float sh[4] = {0.f, 0.f, 0.f, 0.f}, sl[4] = {0.f, 0.f, 0.f, 0.f};
-    uint32_t ka[KS], kb[KS];
+    // scores: lane holds keys g4 and g4 + 8 of each tile, heads 2 t4 and 2 t4 + 1
+    float s[2][4], va[2], vb[2];
 #pragma unroll
-    for (int x = 0; x < CH / 4; ++x) {
-      const uint32_t at = stg + k_row + (((t4 * (CH / 4) + x) ^ turn(g4)) << 4);
-      const uint4 u = lds16(at), v = lds16(at + half_bytes);
-      ka[4 * x] = u.x;
-      ka[4 * x + 1] = u.y;
-      ka[4 * x + 2] = u.z;
-      ka[4 * x + 3] = u.w;
-      kb[4 * x] = v.x;
-      kb[4 * x + 1] = v.y;
-      kb[4 * x + 2] = v.z;
-      kb[4 * x + 3] = v.w;
-    }
-    const float ks_a = lds(stg + s_row), ks_b = lds(stg + s_row + scale_half);
-    const float vs_a = lds(stg + s_row + scale_bytes), vs_b = lds(stg + s_row + scale_bytes + scale_half);
+    for (int x = 0; x < 2; ++x) {
+      uint32_t ka[KS], kb[KS];
 #pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const uint32_t a0 = e4m3x2_to_f16x2(ka[k]), a1 = e4m3x2_to_f16x2(kb[k]);
-      const uint32_t a2 = e4m3x2_to_f16x2_hi(ka[k]), a3 = e4m3x2_to_f16x2_hi(kb[k]);
-      mma_f16(sh, a0, a1, a2, a3, qh[k][0], qh[k][1]);
-      mma_f16(sl, a0, a1, a2, a3, ql[k][0], ql[k][1]);
+      for (int y = 0; y < CH / 4; ++y) {
+        const uint32_t at = stg[x] + k_row + (((t4 * (CH / 4) + y) ^ turn(g4)) << 4);
+        const uint4 u = lds16(at), v = lds16(at + half_bytes);
+        ka[4 * y] = u.x;
+        ka[4 * y + 1] = u.y;
+        ka[4 * y + 2] = u.z;
+        ka[4 * y + 3] = u.w;
+        kb[4 * y] = v.x;
+        kb[4 * y + 1] = v.y;
+        kb[4 * y + 2] = v.z;
+        kb[4 * y + 3] = v.w;
+      }
+      const float ks_a = lds(stg[x] + s_row), ks_b = lds(stg[x] + s_row + scale_half);
+      va[x] = lds(stg[x] + s_row + scale_bytes);
+      vb[x] = lds(stg[x] + s_row + scale_bytes + scale_half);
+      float sh[4] = {0.f, 0.f, 0.f, 0.f}, sl[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const uint32_t a0 = e4m3x2_to_f16x2(ka[k]), a1 = e4m3x2_to_f16x2(kb[k]);
+        const uint32_t a2 = e4m3x2_to_f16x2_hi(ka[k]), a3 = e4m3x2_to_f16x2_hi(kb[k]);
+        mma_f16(sh, a0, a1, a2, a3, qh[k][0], qh[k][1]);
+        mma_f16(sl, a0, a1, a2, a3, ql[k][0], ql[k][1]);
+      }
+      s[x][0] = (sh[0] + sl[0]) * (ks_a * f0);
+      s[x][1] = (sh[1] + sl[1]) * (ks_a * f1);
+      s[x][2] = (sh[2] + sl[2]) * (ks_b * f0);
+      s[x][3] = (sh[3] + sl[3]) * (ks_b * f1);
     }
-    const bool va = (mask >> g4) & 1u, vb = (mask >> (g4 + 8)) & 1u;
-    const float s0 = va ? (sh[0] + sl[0]) * (ks_a * f0) : NEG_INF;
-    const float s1 = va ? (sh[1] + sl[1]) * (ks_a * f1) : NEG_INF;
-    const float s2 = vb ? (sh[2] + sl[2]) * (ks_b * f0) : NEG_INF;
-    const float s3 = vb ? (sh[3] + sl[3]) * (ks_b * f1) : NEG_INF;
-    const float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
+    if (edge) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (!((mask[x] >> g4) & 1u)) {
+          s[x][0] = s[x][1] = NEG_INF;
+          va[x] = 0.f;
+        }
+        if (!((mask[x] >> (g4 + 8)) & 1u)) {
+          s[x][2] = s[x][3] = NEG_INF;
+          vb[x] = 0.f;
+        }
+      }
+    }
+    const float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
+    const float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
     if (__any_sync(0xffffffffu, mx0 > m0 + kGrow || mx1 > m1 + kGrow)) {
       const float n0 = fmaxf(m0, max_of_keys(mx0)), n1 = fmaxf(m1, max_of_keys(mx1));
       const float by0 = exp2f(m0 - (n0 == NEG_INF ? 0.f : n0)), by1 = exp2f(m1 - (n1 == NEG_INF ? 0.f : n1));
@@ -364,70 +407,85 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
       m1 = n1;
       l0 *= by0;
       l1 *= by1;
-#pragma unroll
-      for (int mt = 0; mt < KS; ++mt) {
-        acc[mt][0] *= by0;
-        acc[mt][1] *= by1;
-        acc[mt][2] *= by0;
-        acc[mt][3] *= by1;
-      }
+      rescale(by0, by1);
     }
     // (a max of -inf, from scores that are, is subtracted as 0)
     const float ms0 = m0 == NEG_INF ? 0.f : m0, ms1 = m1 == NEG_INF ? 0.f : m1;
-    const float p0 = exp2f(s0 - ms0), p2 = exp2f(s2 - ms0);
-    const float p1 = exp2f(s1 - ms1), p3 = exp2f(s3 - ms1);
-    l0 += p0 + p2;
-    l1 += p1 + p3;
-    const float xa = va ? vs_a : 0.f, xb = vb ? vs_b : 0.f;
-    float w0 = p0 * (xa * c0), w1 = p1 * (xa * c1), w2 = p2 * (xb * c0), w3 = p3 * (xb * c1);
-    if (__any_sync(0xffffffffu, fmaxf(fmaxf(w0, w1), fmaxf(w2, w3)) > kWeightMost)) {
-      // c so that the largest weight of the tile lies in [2^13, 2^14), if that is less than before
+    float wt[2][4], top = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      s[x][0] = exp2f(s[x][0] - ms0);
+      s[x][1] = exp2f(s[x][1] - ms1);
+      s[x][2] = exp2f(s[x][2] - ms0);
+      s[x][3] = exp2f(s[x][3] - ms1);
+      l0 += s[x][0] + s[x][2];
+      l1 += s[x][1] + s[x][3];
+    }
+    auto weigh = [&]() {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        wt[x][0] = s[x][0] * (va[x] * c0);
+        wt[x][1] = s[x][1] * (va[x] * c1);
+        wt[x][2] = s[x][2] * (vb[x] * c0);
+        wt[x][3] = s[x][3] * (vb[x] * c1);
+        top = fmaxf(fmaxf(top, fmaxf(wt[x][0], wt[x][1])), fmaxf(wt[x][2], wt[x][3]));
+      }
+    };
+    weigh();
+    if (__any_sync(0xffffffffu, top > kWeightMost)) {
+      // c so that the largest weight of the tiles lies in [2^13, 2^14), if that is less than before
       constexpr float kSmall = 1.52587890625e-5f;  // 2^-16: p vs stays finite
-      auto lower = [&](float u, float c_old) -> float {
+      auto lower = [&](int n, float c_old) -> float {
+        float u = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) u = fmaxf(u, fmaxf(s[x][n] * (va[x] * kSmall), s[x][2 + n] * (vb[x] * kSmall)));
         const uint32_t e = __float_as_uint(max_of_keys(u)) & 0x7f800000u;
         // 2^(13 - 16 - exponent of u), at least 2^-120
         const int bits = static_cast<int>((127u + 127u - 3u) << 23) - static_cast<int>(e);
         return fminf(c_old, __int_as_float(max(bits, 7 << 23)));
       };
-      const float d0 = lower(fmaxf(p0 * (xa * kSmall), p2 * (xb * kSmall)), c0);
-      const float d1 = lower(fmaxf(p1 * (xa * kSmall), p3 * (xb * kSmall)), c1);
-      const float by0 = d0 / c0, by1 = d1 / c1;  // (powers of two)
+      const float d0 = lower(0, c0), d1 = lower(1, c1);
+      rescale(d0 / c0, d1 / c1);  // (powers of two)
       c0 = d0;
       c1 = d1;
-      w0 = p0 * (xa * c0);
-      w1 = p1 * (xa * c1);
-      w2 = p2 * (xb * c0);
-      w3 = p3 * (xb * c1);
-#pragma unroll
-      for (int mt = 0; mt < KS; ++mt) {
-        acc[mt][0] *= by0;
-        acc[mt][1] *= by1;
-        acc[mt][2] *= by0;
-        acc[mt][3] *= by1;
-      }
+      weigh();
     }
-    const uint32_t bw0 = movm_t(pack_f16x2(w0, w1)), bw1 = movm_t(pack_f16x2(w2, w3));
+    uint32_t bw[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      bw[x][0] = movm_t(pack_f16x2(wt[x][0], wt[x][1]));
+      bw[x][1] = movm_t(pack_f16x2(wt[x][2], wt[x][3]));
+    }
 #pragma unroll
     for (int mt = 0; mt < KS; mt += 2) {
-      uint32_t r[4];
-      ldsm_x4_t(stg + v_row + (((mt + v_next) ^ v_turn) << 4), r[0], r[1], r[2], r[3]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        // (token 2 t4, token 2 t4 + 1) of column 2 g4 in the lower half, of column 2 g4 + 1 in the upper one
-        const uint32_t u = __byte_perm(r[2 * x], 0u, 0x3120), v = __byte_perm(r[2 * x + 1], 0u, 0x3120);
-        mma_f16(acc[mt + x], e4m3x2_to_f16x2(u), e4m3x2_to_f16x2_hi(u), e4m3x2_to_f16x2(v), e4m3x2_to_f16x2_hi(v), bw0, bw1);
+        uint32_t r[4];
+        ldsm_x4_t(stg[x] + v_row + (((mt + v_next) ^ v_turn) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          // (token 2 t4, token 2 t4 + 1) of column 2 g4 in the lower half, of column 2 g4 + 1 in the upper one
+          const uint32_t u = __byte_perm(r[2 * y], 0u, 0x3120), v = __byte_perm(r[2 * y + 1], 0u, 0x3120);
+          mma_f16(acc[mt + y], e4m3x2_to_f16x2(u), e4m3x2_to_f16x2_hi(u), e4m3x2_to_f16x2(v), e4m3x2_to_f16x2_hi(v), bw[x][0], bw[x][1]);
+        }
       }
     }
-    if (mask != 0xFFFFu) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
+    if (edge) fence_proxy_async_smem();  // the zeros, before the next copy into this stage
     __syncwarp();
-    if (lane == 0) mbar_arrive(empty0 + 8 * stage);
-    if (++stage == S) {
+    if (lane == 0) {
+      mbar_arrive(empty0 + 8 * stage);
+      if (two) mbar_arrive(empty0 + 8 * stage1);
+    }
+    t += two ? 2 : 1;
+    stage = stage1 + 1;
+    round = round1;
+    if (stage == S) {
       stage = 0;
       ++round;
     }
 
     // ---- end of this CTA's share of a row: finished output, or a partial one ------
-    if (t + 1 == t1 || t + 1 == rt1) {
+    if (t == t1 || t == rt1) {
       const float L0 = sum_of_keys(l0), L1 = sum_of_keys(l1);
       const int n0 = 2 * t4, n1 = 2 * t4 + 1;
       const bool whole = rt0 >= t0 && rt1 <= t1;
@@ -487,81 +545,110 @@ __global__ void __launch_bounds__(kThreadsMax, 1) quant_decode_kernel(const __gr
   named_sync(1, 32 * Hc);
 
   // ---- the last CTA of a row adds its pieces: warp w those of kv head w -------------
-  for (int k = 0; k < npart; ++k) {
-    const int* v = misc + kMiscPart + 4 * k;
-    if (!v[0]) continue;
-    const int first = v[1], np = v[2], slot0 = v[3];
-    auto piece = [&](int j) -> long long {
-      return ((static_cast<long long>(gy) * p.N + first + j) * 2 + (j == 0 ? slot0 : 0)) * HG + w * G;
-    };
-    float M[G], sum[G], o[G][PER];
+  // The warp's share of the stages (all tiles have been consumed) takes the pieces by bulk
+  // copies, up to 32 a trip to memory; both rows' come in one where there is room.
+  constexpr int PIECE = G * D * 4;
+  const uint32_t share_bytes = static_cast<uint32_t>(S * p.stage_bytes / Hc) & ~127u;
+  const uint32_t room = smem_addr(smem) + static_cast<uint32_t>(w) * share_bytes;
+  const int cap = min(32, static_cast<int>(share_bytes / PIECE));
+  const int* const part = misc + kMiscPart;
+  const int n0 = part[0] ? part[2] : 0, n1 = npart > 1 && part[4] ? part[6] : 0;
+  const bool together = n0 + n1 <= cap;
+  float lse[G], wt[G], M[G], sum[G], o[G][PER];
+  uint32_t trips = 0;
+  // pieces j0 .. j0 + n - 1 of row k, each to a lane's slot from lane `lo` on
+  auto fetch = [&](int k, int j0, int lo, int n) {
+    if (lane < lo || lane >= lo + n) return;
+    const int* v = part + 4 * k;
+    const int j = j0 + lane - lo;
+    const long long at = ((static_cast<long long>(gy) * p.N + v[1] + j) * 2 + (j == 0 ? v[3] : 0)) * HG + w * G;
+    bulk_g2s(room + lane * PIECE, p.part_o + at * D, PIECE, merged0 + 8 * w);
 #pragma unroll
-    for (int n = 0; n < G; ++n) {
-      M[n] = NEG_INF;
-      sum[n] = 0.f;
+    for (int x = 0; x < G; ++x) lse[x] = __ldcg(p.part_lse + at + x);
+  };
+  auto expect = [&](int n) {
+    // what was read and written there by loads and stores comes before the copies, and
+    // what other CTAs wrote (seen by the counter's acquire) too
+    asm volatile("fence.proxy.async;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive_expect_tx(merged0 + 8 * w, static_cast<uint32_t>(n * PIECE));
+    __syncwarp();
+  };
+  // adds the pieces of lanes lo .. lo + n - 1
+  auto add = [&](int lo, int n) -> bool {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) o[n][i] = 0.f;
+    for (int x = 0; x < G; ++x) {
+      const float mine = lane >= lo && lane < lo + n ? lse[x] : NEG_INF;
+      float mx = mine;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      mx = fmaxf(mx, M[x]);
+      const float ms = mx == NEG_INF ? 0.f : mx, sc = exp2f(M[x] - ms);
+      M[x] = mx;
+      wt[x] = mine == NEG_INF ? 0.f : at_least_tiny(exp2f(mine - ms));
+      float all = wt[x];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+      sum[x] = sum[x] * sc + all;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) o[x][i] *= sc;
     }
-    for (int j0 = 0; j0 < np; j0 += 32) {
-      const int nj = min(32, np - j0);
-      // weights: lane j that of piece j0 + j; the sums so far in the new maximum's terms
-      float wt[G];
+    if (!mbar_wait(merged0 + 8 * w, trips & 1u)) return false;
+    for (int j = lo; j < lo + n; ++j) {
+      const uint32_t at = room + static_cast<uint32_t>(j * PIECE + lane * PER * 4);
 #pragma unroll
-      for (int n = 0; n < G; ++n) {
-        const float lse = lane < nj ? __ldcg(p.part_lse + piece(j0 + lane) + n) : NEG_INF;
-        float mx = lse;
+      for (int x = 0; x < G; ++x) {
+        const float f = __shfl_sync(0xffffffffu, wt[x], j);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        mx = fmaxf(mx, M[n]);
-        const float ms = mx == NEG_INF ? 0.f : mx;
-        const float sc = exp2f(M[n] - ms);
-        M[n] = mx;
-        wt[n] = lse == NEG_INF ? 0.f : at_least_tiny(exp2f(lse - ms));
-        float add = wt[n];
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
-        sum[n] = sum[n] * sc + add;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) o[n][i] *= sc;
-      }
-      constexpr int U = 16 / G;  // pieces loaded at a time: 16 loads in flight
-      for (int j = 0; j < nj; j += U) {
-        float x[U][G][PER];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int n = 0; n < G; ++n) {
-            const float* src = p.part_o + (piece(j0 + min(j + u, nj - 1)) + n) * D + lane * PER;
-            if constexpr (PER == 4) {
-              const float4 f = __ldcg(reinterpret_cast<const float4*>(src));
-              x[u][n][0] = f.x;
-              x[u][n][1] = f.y;
-              x[u][n][2] = f.z;
-              x[u][n][3] = f.w;
-            } else {
-              const float2 f = __ldcg(reinterpret_cast<const float2*>(src));
-              x[u][n][0] = f.x;
-              x[u][n][1] = f.y;
-            }
-          }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int n = 0; n < G; ++n) {
-            const float f = __shfl_sync(0xffffffffu, wt[n], min(j + u, 31));
-            if (j + u < nj) {
-#pragma unroll
-              for (int i = 0; i < PER; ++i) o[n][i] += f * x[u][n][i];
-            }
-          }
+        for (int i = 0; i < PER; i += 2) {
+          float2 y;
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(y.x), "=f"(y.y) : "r"(at + x * D * 4 + i * 4));
+          o[x][i] += f * y.x;
+          o[x][i + 1] += f * y.y;
+        }
       }
     }
+    return true;
+  };
+  if (together && n0 + n1 > 0) {
+    expect(n0 + n1);
+    fetch(0, 0, 0, n0);
+    fetch(1, 0, n0, n1);
+  }
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int n = k ? n1 : n0;
+    if (n == 0) continue;
 #pragma unroll
-    for (int n = 0; n < G; ++n) {
-      const float il = 1.f / sum[n];
-      uint16_t* dst = p.out + (static_cast<long long>(part_row[k]) * p.Hq + static_cast<long long>(h) * G + n) * D + lane * PER;
+    for (int x = 0; x < G; ++x) {
+      M[x] = NEG_INF;
+      sum[x] = 0.f;
 #pragma unroll
-      for (int i = 0; i < PER; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = E::pack2(o[n][i] * il, o[n][i + 1] * il);
+      for (int i = 0; i < PER; ++i) o[x][i] = 0.f;
+    }
+    bool came = true;
+    if (together) {
+      came = add(k ? n0 : 0, n);
+    } else {
+      for (int j0 = 0; j0 < n && came; j0 += cap) {
+        expect(min(cap, n - j0));
+        fetch(k, j0, 0, min(cap, n - j0));
+        came = add(0, min(cap, n - j0));
+        ++trips;
+        __syncwarp();
+      }
+    }
+    if (!came) {
+      if (lane == 0) flag_error(p.err_flag, VH_ERR_TIMEOUT);
+      (void)mbar_wait(merged0 + 8 * w, trips & 1u);  // (no copy outlives the CTA)
+      return;
+    }
+#pragma unroll
+    for (int x = 0; x < G; ++x) {
+      const float il = 1.f / sum[x];
+      uint16_t* dst = p.out + (static_cast<long long>(k ? part_row[1] : part_row[0]) * p.Hq + static_cast<long long>(h) * G + x) * D + lane * PER;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = E::pack2(o[x][i] * il, o[x][i + 1] * il);
     }
   }
 }

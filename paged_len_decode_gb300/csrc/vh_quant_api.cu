@@ -44,7 +44,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kMaxHc = 8;
 constexpr int kMaxStages = 8;
-constexpr int kStageTarget = 65536;  // bytes in flight of a CTA
+constexpr int kStageTarget = 102400;  // bytes in flight of a CTA
 
 // Shared-memory plan and automatic CTA count of the decode kernel.
 struct DecodePlan {
@@ -64,7 +64,7 @@ bool layout_decode(vh::QuantDecodeParams& p, const DeviceInfo& dev) {
     p.stage_bytes = static_cast<int>(align_up(2 * 16 * static_cast<size_t>(hc) * p.D + 2 * static_cast<size_t>(p.scale_bytes), 1024));
     const size_t q = static_cast<size_t>(hc) * p.G * p.D * 4;
     const size_t cum = align_up(4 * (static_cast<size_t>(p.B) + 1), 16), len = align_up(4 * static_cast<size_t>(p.B), 16);
-    const size_t fixed = 1024 + q + cum + len + 8 * (2 * kMaxStages + 2) + 48 * 4 + 128;
+    const size_t fixed = 1024 + q + cum + len + 8 * (2 * kMaxStages + 2 + kMaxHc) + 48 * 4 + 128;
     const size_t budget = static_cast<size_t>(dev.smem_optin);
     if (fixed + 2 * static_cast<size_t>(p.stage_bytes) > budget) continue;
     p.stages = static_cast<int>(std::min<size_t>((budget - fixed) / p.stage_bytes,
@@ -74,7 +74,7 @@ bool layout_decode(vh::QuantDecodeParams& p, const DeviceInfo& dev) {
     p.cum_off = static_cast<int>(off += q);
     p.len_off = static_cast<int>(off += cum);
     p.bar_off = static_cast<int>(off += len);
-    off += 8 * (2 * static_cast<size_t>(p.stages) + 2) + 48 * 4;
+    off += 8 * (2 * static_cast<size_t>(p.stages) + 2 + kMaxHc) + 48 * 4;
     p.smem_bytes = static_cast<int>(align_up(off, 128) + 1024);  // + up to 1024 to align the base
     return true;
   }
