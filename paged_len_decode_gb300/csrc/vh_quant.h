@@ -67,11 +67,12 @@ struct QuantReadParams {
   int32_t* err_flag;
   int f16;
   int B, Hkv, D, P, out_P;
-  int ctas;
+  uint32_t hkv_inverse;        // ceil(2^32 / Hkv), 0 for Hkv == 1: y / Hkv of small y is the high word of y times it
 };
+inline size_t quant_read_smem(int B) { return 4 * (3 * static_cast<size_t>(B) + 1); }
 
 cudaError_t prepare_quant_read(int max_smem);
-cudaError_t launch_quant_read(const QuantReadParams& p, cudaStream_t stream);
+cudaError_t launch_quant_read(const QuantReadParams& p, int sm_count, cudaStream_t stream);
 cudaError_t prepare_quant_decode(int max_smem);  // once per device, every variant
 cudaError_t quant_decode_occupancy(const QuantDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_quant_decode(const QuantDecodeParams& p, cudaStream_t stream);

@@ -250,7 +250,7 @@ int vh_quant_kv_read(const vh_e4m3* k_cache, const vh_e4m3* v_cache, int64_t pag
     return VH_EALIGN;
   const DeviceInfo* dev = device_info();
   if (!dev || !prepared(*dev)) return VH_ENODEV;
-  if (4 * (static_cast<size_t>(B) + 1) > static_cast<size_t>(dev->smem_optin) - 1024) return VH_EINVAL;
+  if (vh::quant_read_smem(B) > static_cast<size_t>(dev->smem_optin) - 1024) return VH_EINVAL;
   p.num_pages = num_pages;
   p.page_table = page_table;
   p.max_pages_per_seq = max_pages_per_seq;
@@ -273,8 +273,8 @@ int vh_quant_kv_read(const vh_e4m3* k_cache, const vh_e4m3* v_cache, int64_t pag
   p.D = D;
   p.P = page_size;
   p.out_P = out_page_size;
-  p.ctas = dev->sm_count * 4;
-  return status_of(vh::launch_quant_read(p, static_cast<cudaStream_t>(stream)));
+  p.hkv_inverse = Hkv == 1 ? 0u : static_cast<uint32_t>(((1ULL << 32) + Hkv - 1) / Hkv);
+  return status_of(vh::launch_quant_read(p, dev->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"
