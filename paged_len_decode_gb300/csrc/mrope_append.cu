@@ -38,15 +38,22 @@ constexpr int kThreads = 64;  // (small CTAs: no two warps need each other)
 
 __device__ __forceinline__ uint4 ldg16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-// Bits of |x|, the largest of a and b: a NaN's are above an infinity's, so neither is lost.
-__device__ __forceinline__ uint32_t larger_bits(uint32_t a, float x) { return max(a, __float_as_uint(x) & 0x7fffffffu); }
-
-// Of 8 values of a head, whose largest has the bits `top` over the `lanes` neighbouring lanes
-// that hold the head: the scale, and the e4m3 values.  (Divisions that round to nearest: a value
+// The largest of top, |x| and |y|, NaN if one of them is.
+__device__ __forceinline__ float larger(float top, float x, float y) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(x)), "f"(fabsf(y)));
+  return r;
+}
+// The same of pairs of 16-bit elements, by their bits without the sign (a NaN's are above an infinity's).
+__device__ __forceinline__ uint32_t larger_bits(uint32_t top, uint32_t w) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(top), "r"(w & 0x7fff7fffu));
+  return r;
+}
+// The scale of a head whose largest value is `top`.  (Divisions that round to nearest: a value
 // that another program quantises by the same rule has the same bits.)
-__device__ __forceinline__ float scale_of(uint32_t top, int lanes) {
-  for (int off = 1; off < lanes; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-  return top >= 0x7f800000u ? __int_as_float(0x7fffffff) : fmaxf(__fdiv_rn(__uint_as_float(top), kE4m3Max), kScaleMin);
+__device__ __forceinline__ float scale_of(float top) {
+  return top < __int_as_float(0x7f800000) ? fmaxf(__fdiv_rn(top, kE4m3Max), kScaleMin) : __int_as_float(0x7fffffff);
 }
 __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float inv) {
   uint32_t h[4];
@@ -55,12 +62,16 @@ __device__ __forceinline__ uint2 e4m3x8(const float (&x)[8], float inv) {
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-template <typename E, int D, bool Q8>
-__global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
+// Form of the kernel: into a cache of 16 bits, or of 8 for few tokens or many.
+enum { k16, k8Few, k8Many };
+
+template <typename E, int D, int FORM>
+__global__ void __launch_bounds__(kThreads, FORM == k16 ? 10 : (FORM == k8Few ? 8 : 14)) mrope_kv_append_kernel(const __grid_constant__ MropeParams p) {
   constexpr int HALF = D / 2;
   constexpr int UPH = HALF / 8;  // lanes of a head
   constexpr int HPW = 32 / UPH;  // heads that a warp rotates at a time
-  constexpr int U = 3;           // of those, in flight
+  constexpr int U = FORM == k8Many ? 2 : 3;  // of those, in flight
+  constexpr bool Q8 = FORM != k16;
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
   const int t = unit / p.warps, part = unit - t * p.warps;
@@ -153,16 +164,17 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
     // 8 elements a lane, D / 8 neighbouring lanes a head (every lane runs each round)
     auto put = [&](int u, const uint4& w) {
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      uint32_t top2 = larger_bits(larger_bits(larger_bits(ws[0] & 0x7fff7fffu, ws[1]), ws[2]), ws[3]);
+#pragma unroll
+      for (int off = 1; off < D / 8; off <<= 1) top2 = larger_bits(top2, __shfl_xor_sync(0xffffffffu, top2, off));
+      const float scale = scale_of(E::to_float(static_cast<uint16_t>(max(top2 & 0xffffu, top2 >> 16))));
       float x[8];
-      uint32_t top = 0u;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = E::to_float2(ws[k]);
         x[2 * k] = f.x;
         x[2 * k + 1] = f.y;
-        top = larger_bits(larger_bits(top, f.x), f.y);
       }
-      const float scale = scale_of(top, D / 8);
       if (u >= nv || !page_ok) return;
       const int h = u / (D / 8), c = u % (D / 8);
       *reinterpret_cast<uint2*>(p.v8 + slot_off + h * p.head_stride + c * 8) = e4m3x8(x, __frcp_rn(scale));
@@ -249,19 +261,22 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
         }
       }
       if constexpr (Q8) {
-        uint32_t top = 0u;
+        const bool is_k = !is_q && h < heads;
+        if (__any_sync(0xffffffffu, is_k)) {  // (a round of q heads alone skips this)
+          float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = larger_bits(larger_bits(top, o0[k]), o1[k]);
-        const float scale = scale_of(top, UPH);
-        if (h >= heads || !(is_q || page_ok)) continue;
-        if (!is_q) {
-          const float inv = __frcp_rn(scale);
-          uint8_t* dst = p.k8 + slot_off + (h - p.Hq) * p.head_stride;
-          *reinterpret_cast<uint2*>(dst + e0) = e4m3x8(o0, inv);
-          *reinterpret_cast<uint2*>(dst + e1) = e4m3x8(o1, inv);
-          if (lane % UPH == 0) p.k_scale[scale_at + (h - p.Hq) * p.scale_head] = scale;
-          continue;
+          for (int k = 0; k < 8; ++k) top = larger(top, o0[k], o1[k]);
+#pragma unroll
+          for (int off = 1; off < UPH; off <<= 1) top = larger(top, top, __shfl_xor_sync(0xffffffffu, top, off));
+          const float scale = scale_of(top), inv = __frcp_rn(scale);
+          if (is_k && page_ok) {
+            uint8_t* dst = p.k8 + slot_off + (h - p.Hq) * p.head_stride;
+            *reinterpret_cast<uint2*>(dst + e0) = e4m3x8(o0, inv);
+            *reinterpret_cast<uint2*>(dst + e1) = e4m3x8(o1, inv);
+            if (lane % UPH == 0) p.k_scale[scale_at + (h - p.Hq) * p.scale_head] = scale;
+          }
         }
+        if (!is_q) continue;
       }
       if (is_q && !p.q16) {
         float* dst = static_cast<float*>(p.q_rot) + (static_cast<long long>(t) * p.Hq + h) * D;
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 10) mrope_kv_append_kernel(const __g
 
 }  // namespace
 
-cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
+cudaError_t launch_mrope_kv_append(const MropeParams& pp, int sm_count, cudaStream_t stream) {
   MropeParams p = pp;
   // A token's heads over several warps while the tokens do not fill the GPU.  16 / 8
   // heads of 128 with the norm, 8, 2 and 1 warps a token: 1 token 3.3, 3.7 and 4.9 us,
@@ -291,12 +306,17 @@ cudaError_t launch_mrope_kv_append(const MropeParams& pp, cudaStream_t stream) {
   // tokens 3.1, 3.1 and 3.8, 2000 14.7, 8.0 and 8.0.
   p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32)));
+  // Into a cache of 8 bits: 16 warps an SM with three heads' loads a lane while they hold all tokens
+  // (2413 of them, with the norm: 9.2 us, and 10.7 with 28 warps and two loads), 28 with two
+  // otherwise (16384 tokens: 66.5 us, and 76 with 16 warps, 70.5 with 20).
   using Kernel = void (*)(MropeParams);
-  const Kernel kernels[8] = {mrope_kv_append_kernel<ElemBf16, 64, false>,  mrope_kv_append_kernel<ElemBf16, 64, true>,
-                             mrope_kv_append_kernel<ElemF16, 64, false>,   mrope_kv_append_kernel<ElemF16, 64, true>,
-                             mrope_kv_append_kernel<ElemBf16, 128, false>, mrope_kv_append_kernel<ElemBf16, 128, true>,
-                             mrope_kv_append_kernel<ElemF16, 128, false>,  mrope_kv_append_kernel<ElemF16, 128, true>};
-  return launch_dependent(kernels[(p.D == 128 ? 4 : 0) + (p.f16 ? 2 : 0) + (p.k8 ? 1 : 0)], p, grid, kThreads, 0, stream);
+  const int form = !p.k8 ? k16 : (p.T <= 16 * sm_count ? k8Few : k8Many);
+  const Kernel kernels[4][3] = {
+      {mrope_kv_append_kernel<ElemBf16, 64, k16>, mrope_kv_append_kernel<ElemBf16, 64, k8Few>, mrope_kv_append_kernel<ElemBf16, 64, k8Many>},
+      {mrope_kv_append_kernel<ElemF16, 64, k16>, mrope_kv_append_kernel<ElemF16, 64, k8Few>, mrope_kv_append_kernel<ElemF16, 64, k8Many>},
+      {mrope_kv_append_kernel<ElemBf16, 128, k16>, mrope_kv_append_kernel<ElemBf16, 128, k8Few>, mrope_kv_append_kernel<ElemBf16, 128, k8Many>},
+      {mrope_kv_append_kernel<ElemF16, 128, k16>, mrope_kv_append_kernel<ElemF16, 128, k8Few>, mrope_kv_append_kernel<ElemF16, 128, k8Many>}};
+  return launch_dependent(kernels[(p.D == 128 ? 2 : 0) + (p.f16 ? 1 : 0)][form], p, grid, kThreads, 0, stream);
 }
 
 }  // namespace vh

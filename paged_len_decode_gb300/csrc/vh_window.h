@@ -145,7 +145,7 @@ bool valid_cache(int B, int Hq, int Hkv, int D, int P, int64_t page_stride, int6
 bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, const void* base, int rank, const cuuint64_t* dims,
                   const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 
-cudaError_t launch_mrope_kv_append(const MropeParams& p, cudaStream_t stream);
+cudaError_t launch_mrope_kv_append(const MropeParams& p, int sm_count, cudaStream_t stream);
 cudaError_t prepare_window_decode(int max_smem);  // once per device, every variant
 cudaError_t window_decode_occupancy(const WindowDecodeParams& p, int* blocks_per_sm);
 cudaError_t launch_window_decode(const WindowDecodeParams& p, cudaStream_t stream);

@@ -305,11 +305,12 @@ int append(vh::MropeParams& p, const uint8_t* pair_axis, unsigned flags, void* s
   if (q8 ? !vh::aligned_quant({p.k8, p.v8, p.page_stride, p.token_stride, p.head_stride, p.k_scale, p.v_scale, p.scale_page, p.scale_head})
          : !aligned_cache(k, v, p.page_stride, p.token_stride, p.head_stride))
     return VH_EALIGN;
-  if (!device_info()) return VH_ENODEV;
+  const DeviceInfo* dev = device_info();
+  if (!dev) return VH_ENODEV;
   p.q16 = (flags & VH_FLAG_Q16) != 0;
   p.rope_interleaved = (flags & VH_FLAG_ROPE_INTERLEAVED) != 0;
   p.f16 = (flags & VH_FLAG_FP16) != 0;
-  return status_of(vh::launch_mrope_kv_append(p, static_cast<cudaStream_t>(stream)));
+  return status_of(vh::launch_mrope_kv_append(p, dev->sm_count, static_cast<cudaStream_t>(stream)));
 }
 
 // Both calls on ragged batches: with tree_mask, the drafted tokens' ancestors instead of all earlier ones.
