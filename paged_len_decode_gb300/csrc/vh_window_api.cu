@@ -270,10 +270,9 @@ bool small_blocks(int T, int B, int G, int Hkv, const DeviceInfo& dev) {
 // 25 us with 16, of which half the clusters wait for the others; over 300 keys 8.4
 // us with one and 9.8 with 2; 128 tokens over 4200 30, 23 and 19 us with 1, 2 and 4,
 // and 33 with 8.)
-int prompt_splits(const vh::PromptParams& p, const int (&clusters)[5]) {
+int prompt_splits(const vh::PromptParams& p, long long blocks, const int (&clusters)[5]) {
   const long long longest = std::min<long long>(static_cast<long long>(p.max_pages_per_seq) * p.P,
                                                 static_cast<long long>(p.window) + p.sinks + (1 << p.shift_block));
-  const long long blocks = likely_blocks(p.T, p.B, p.shift_block);
   int x = 0;
   while (x < 4 && blocks * p.Hkv <= clusters[x + 1] && (longest + 127) / 128 >= (2LL << (x + 1))) ++x;
   return 1 << x;
@@ -368,9 +367,15 @@ int prompt(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_
   p.P = page_size;
   const int(&clusters)[5] = (mask_words ? g_tree : g_prepared)[dev->index].clusters;
   p.shift_g = __builtin_ctz(p.G);
-  p.pair = small_blocks(T, B, p.G, Hkv, *dev);
+  // Drafted trees are of a size, one a request: small blocks where a tree of the mean size fits one (32
+  // requests of 33 tokens, 2 q heads a kv head: 25.0 us, and 28.9 with blocks of 256 rows), large
+  // ones otherwise (8 requests of 64, 4 q heads: 168 us, and 177 with two small blocks each).
+  const int mean = (T + B - 1) / B;
+  p.pair = mask_words ? mean * p.G <= 128 : small_blocks(T, B, p.G, Hkv, *dev);
   p.shift_block = (p.pair ? 7 : 8) - p.shift_g;
-  p.splits = num_splits > 0 ? num_splits : prompt_splits(p, clusters);
+  const long long likely = mask_words ? static_cast<long long>(B) * ((mean + (1 << p.shift_block) - 1) >> p.shift_block)
+                                      : likely_blocks(T, B, p.shift_block);
+  p.splits = num_splits > 0 ? num_splits : prompt_splits(p, likely, clusters);
   while (p.splits > 1 && clusters[__builtin_ctz(p.splits)] < 1) p.splits /= 2;
   const long long blocks = (static_cast<long long>(T) >> p.shift_block) + B, units = blocks * Hkv * p.splits;
   if (units > INT32_MAX / 2 || blocks * Hkv > (1LL << 32) / Hkv - 1 || !encode_prompt_maps(p)) return VH_EINVAL;
