@@ -424,10 +424,11 @@ __global__ void __launch_bounds__(32 * (kHeadsMost<D> + 1), D == 128 ? 2 : 1) qu
     auto weigh = [&]() {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        wt[x][0] = s[x][0] * (va[x] * c0);
-        wt[x][1] = s[x][1] * (va[x] * c1);
-        wt[x][2] = s[x][2] * (vb[x] * c0);
-        wt[x][3] = s[x][3] * (vb[x] * c1);
+        // (in this order: vs c may be infinite where p is 0)
+        wt[x][0] = s[x][0] * va[x] * c0;
+        wt[x][1] = s[x][1] * va[x] * c1;
+        wt[x][2] = s[x][2] * vb[x] * c0;
+        wt[x][3] = s[x][3] * vb[x] * c1;
         top = fmaxf(fmaxf(top, fmaxf(wt[x][0], wt[x][1])), fmaxf(wt[x][2], wt[x][3]));
       }
     };

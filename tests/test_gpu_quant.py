@@ -294,6 +294,19 @@ def test_decode_all_zero_heads():
     check_decode(r, q=torch.zeros(2, 4, 128))
 
 
+def test_decode_large_value_without_weight_among_tiny_ones():
+    """Values near the least scale, and a huge one under a score that leaves it no weight."""
+    r = Q.make([40], [1], Hq=4, Hkv=2, seed=24)
+    x = torch.randn(r.pool.shape, generator=torch.Generator().manual_seed(2))
+    x[:, 1] *= 2.0 ** -112
+    page = int(r.table[0, 0])
+    q = torch.full((1, 4, 128), 4.0)
+    x[page, 0, 3], x[page, 1, 3] = -64.0, 2.0 ** 60   # (its score: 128 * 4 * -64 / sqrt(128) = -2896)
+    x[:, 0][x[:, 0].abs() < 64] = 0.0
+    Q.set_pool(r, *Q.quantised(x))
+    check_decode(r, q=q)
+
+
 def test_decode_nonfinite_scales_and_queries():
     """A key whose scale is NaN makes its rows NaN, a value its outputs, a query its head; others stay."""
     base = Q.make([300, 90, 40], [1, 1, 1], Hq=8, Hkv=2, window=200, sinks=4, seed=25)
