@@ -15,14 +15,14 @@
 //    fills with zeros.
 //  * A consumer warp per kv head: S^T = K q^T and O^T += V^T P^T on mma.sync
 //    m16n8k16 in fp16, which holds every e4m3 value: the bytes become fp16 pairs in
-//    registers (cvt, two values an instruction), and are read only once from shared
+//    registers (cvt, two values an instruction), and each is read once from shared
 //    memory.  The products' order of dimensions is free as long as q and K agree,
 //    so a lane takes 16 neighbouring bytes of a key and no transposition is needed;
 //    V is transposed by ldmatrix in pairs of bytes, and a byte permutation parts the
 //    pairs: a lane then has two neighbouring columns of the output.
 //  * q, divided by a power of two that brings its largest element into [1, 2), is
-//    split into an fp16 high part and residual: 22 bits of that.  ks multiplies the
-//    score.  The weight w = p_j vs_j c carries the value's scale, and c, a power of
+//    split into an fp16 high part and residual: 22 bits of that (and so are the weights
+//    of an fp16 output).  ks multiplies the score.  The weight w = p_j vs_j c carries the value's scale, and c, a power of
 //    two a head, keeps the largest weight so far below 2^15: fp16 then holds
 //    those down to 2^-29 of it with 11 bits.  p refers to a maximum that is raised,
 //    and c lowered, only when a weight would grow too large (p above 2^8, w above
@@ -451,11 +451,21 @@ __global__ void __launch_bounds__(32 * (kHeadsMost<D> + 1), D == 128 ? 2 : 1) qu
       c1 = d1;
       weigh();
     }
-    uint32_t bw[2][2];
+    // Weights rounded to fp16 add to the error of a bf16 output a tenth of its own rounding; of an
+    // fp16 output they would add as much again, so there the residuals are multiplied too.
+    uint32_t bw[2][2], bl[2][2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      bw[x][0] = movm_t(pack_f16x2(wt[x][0], wt[x][1]));
-      bw[x][1] = movm_t(pack_f16x2(wt[x][2], wt[x][3]));
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        if constexpr (E::kF16) {
+          split2<ElemF16>(wt[x][2 * y], wt[x][2 * y + 1], bw[x][y], bl[x][y]);
+          bl[x][y] = movm_t(bl[x][y]);
+        } else {
+          bw[x][y] = pack_f16x2(wt[x][2 * y], wt[x][2 * y + 1]);
+        }
+        bw[x][y] = movm_t(bw[x][y]);
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < KS; mt += 2) {
@@ -467,7 +477,9 @@ __global__ void __launch_bounds__(32 * (kHeadsMost<D> + 1), D == 128 ? 2 : 1) qu
         for (int y = 0; y < 2; ++y) {
           // (token 2 t4, token 2 t4 + 1) of column 2 g4 in the lower half, of column 2 g4 + 1 in the upper one
           const uint32_t u = __byte_perm(r[2 * y], 0u, 0x3120), v = __byte_perm(r[2 * y + 1], 0u, 0x3120);
-          mma_f16(acc[mt + y], e4m3x2_to_f16x2(u), e4m3x2_to_f16x2_hi(u), e4m3x2_to_f16x2(v), e4m3x2_to_f16x2_hi(v), bw[x][0], bw[x][1]);
+          const uint32_t a0 = e4m3x2_to_f16x2(u), a1 = e4m3x2_to_f16x2_hi(u), a2 = e4m3x2_to_f16x2(v), a3 = e4m3x2_to_f16x2_hi(v);
+          mma_f16(acc[mt + y], a0, a1, a2, a3, bw[x][0], bw[x][1]);
+          if constexpr (E::kF16) mma_f16(acc[mt + y], a0, a1, a2, a3, bl[x][0], bl[x][1]);
         }
       }
     }

@@ -6,8 +6,8 @@ a = scale max_j ks_j sum_d |q_d| |k8_jd|, a1 the same with the head's largest |q
 keys and head dim D:
   * q is held to 2^-22 of the head's largest element, so a score is off by at most 2^-22 a1; its products are summed in
     fp32 and multiplied by the scales: a (D + 4) 2^-23;
-  * a weight is off by that relatively, by exp2 and the maximum's subtraction (2^-20 covers both), and by its rounding,
-    2^-11; the sum too, hence the factor 2 on the first;
+  * a weight is off by that relatively, by exp2 and the maximum's subtraction (2^-20 covers both), and by its rounding
+    u_p, 2^-11, or 2^-22 where the output is fp16; the sum too, hence the factor 2 on the first;
   * weights far below the largest one lose at most 2^-40 of the largest w_j each, and a value is at most 448:
     448 n 2^-40 max_j w_j;
   * n fp32 additions lose at most n 2^-23; the output is rounded once.
@@ -65,7 +65,7 @@ def on_gpu(r, pad=0):
                 starts=i32(r.starts), lens=i32(r.lens), active=i32(r.active), err=torch.zeros(1, dtype=torch.int32, device="cuda"))
 
 
-def attention(r, q, scale=0.0, contiguous=False):
+def attention(r, q, scale=0.0, contiguous=False, dtype=torch.bfloat16):
     """(out, tol without the output's rounding) [B, Hq, D] of one query a row, q [B, Hq, D] fp32."""
     D, G = r.D, r.Hq // r.Hkv
     f = scale if scale > 0 else 1 / math.sqrt(D)
@@ -88,7 +88,8 @@ def attention(r, q, scale=0.0, contiguous=False):
         n = len(at)
         top = (p * vvs.t()[:, None]).amax(-1).reshape(r.Hq, 1)
         delta = a * (D + 4) * 2.0 ** -23 + a1 * 2.0 ** -22 + 2.0 ** -20
-        tol[b] = A * (2 * delta + 2.0 ** -11 + n * 2.0 ** -23) + 448 * n * 2.0 ** -40 * top
+        u_p = 2.0 ** -22 if dtype == torch.float16 else 2.0 ** -11
+        tol[b] = A * (2 * delta + u_p + n * 2.0 ** -23) + 448 * n * 2.0 ** -40 * top
     return out, tol
 
 

@@ -184,7 +184,7 @@ def check_decode(r, dtype=BF, q=None, **kw):
     q = R.queries(r, torch.float32) if q is None else q
     out, err = decode(r, q, dtype, **kw)
     assert err == 0
-    bad = Q.differs(out, Q.attention(r, q, kw.get("scale", 0.0), contiguous=not kw.get("table", True)), dtype)
+    bad = Q.differs(out, Q.attention(r, q, kw.get("scale", 0.0), not kw.get("table", True), dtype), dtype)
     assert bad is None, bad
 
 

@@ -72,7 +72,7 @@ class Layer:
 
     def check8(self, q_rot, out, lens, window=0, sinks=0):
         r = self.held8(lens, [1] * self.B, window, sinks)
-        bad = Q.differs(out, Q.attention(r, q_rot.cpu()), self.dtype)
+        bad = Q.differs(out, Q.attention(r, q_rot.cpu(), dtype=self.dtype), self.dtype)
         assert bad is None, bad
 
 
