@@ -25,7 +25,10 @@
 //
 // Into a cache of 8 bits (Q8) go e4m3_rne(x / s) and the scale s = max |x| / 448 of the head
 // (at least 2^-126), each from the fp32 values before any other rounding: the lanes of a head
-// agree on its largest value, and write 8 bytes a run instead of 16.
+// agree on its largest value, and write 8 bytes a run instead of 16.  That takes more
+// instructions than bytes it saves: 16384 tokens (32 / 8 heads, 370 MB) 66.5 us = 5.6 TB/s, an
+// instruction issued in 59 % of the cycles; 71 with the q heads' largest values found too and
+// 78 with a comparison for every element.
 #include "vh_e4m3.cuh"
 #include "vh_ragged.cuh"
 #include "vh_window.h"

@@ -10,6 +10,9 @@
 //    bytes each, multiply by the slot's scale and write 32; a thread has eight such
 //    loads under way.  The pages of a tile's two halves (8 tokens lie in one page,
 //    whatever the page sizes) are looked up once a tile, a lane each.
+// Measured: 16 rows of up to 16384 tokens, 8 heads of 128 (993 MB) 160 us = 6.2 TB/s, 92 % of a
+// copy's rate; with four loads a thread 169-179, a first form that looked up pages and divided
+// for every 16 bytes 266.
 #include <algorithm>
 
 #include "vh_e4m3.cuh"
