@@ -142,9 +142,10 @@ struct Cache {
     NP = static_cast<int>(kt.size(0));
     P = static_cast<int>(kt.size(1));
     Hkv = static_cast<int>(kt.size(2));
-    page = kt.stride(0);
-    token = kt.stride(1);
-    head = kt.stride(2);
+    // (torch gives a dimension of one element any stride)
+    head = Hkv > 1 ? kt.stride(2) : D;
+    token = P > 1 ? kt.stride(1) : Hkv * D;
+    page = NP > 1 ? kt.stride(0) : static_cast<int64_t>(P) * Hkv * D;
   }
   void locate(PyObject* table_o, int B, int dev, const char* table_name = "page_table") {
     k = static_cast<uint16_t*>(address(kt, type, dev, k_name, false));
@@ -170,8 +171,8 @@ struct Scales {
     if (!shape_is(kt, {c.NP, c.Hkv, c.P}) || vt.sizes() != kt.sizes() || vt.strides() != kt.strides() || (c.P > 1 && kt.stride(2) != 1))
       raise(PyExc_ValueError, "k_scale / v_scale must be [%d, %d, %d] views (pages, kv heads, slots) with equal strides and "
                               "contiguous slots", c.NP, c.Hkv, c.P);
-    page = kt.stride(0);
-    head = kt.stride(1);
+    head = c.Hkv > 1 ? kt.stride(1) : (c.P + 3) / 4 * 4;
+    page = c.NP > 1 ? kt.stride(0) : c.Hkv * head;
   }
   void locate(int dev) {
     k = static_cast<float*>(address(kt, at::kFloat, dev, "k_scale", false));

@@ -205,6 +205,24 @@ def test_decode_heads(heads, D, dtype):
                  pad=1)
 
 
+def test_one_head_or_page_with_any_stride():
+    """torch gives dimensions of one element strides of its own: they are not looked at."""
+    v = vh()
+    for lens, P in (([40, 9], 16), ([7], 8)):
+        r = Q.make(lens, [1] * len(lens), Hq=4, Hkv=1, P=P, seed=P, spare=0 if len(lens) > 1 else -1, table_extra=0)
+        if len(lens) == 1:
+            r.table.zero_()
+            Q.set_pool(r, *Q.quantised(torch.randn(r.pool.shape)))
+        c, q = Q.on_gpu(r), R.queries(r, torch.float32).cuda()
+        NP = c["k"].shape[0]
+        scale = [s.squeeze(1).contiguous().as_strided((NP, 1, P), (P if NP > 1 else 1, 1, 1)) for s in (c["ks"], c["vs"])]
+        cache = [x.squeeze(2).contiguous().as_strided((NP, P, 1, 128), (P * 128 if NP > 1 else 3, 128, 1, 1)) for x in (c["k"], c["v"])]
+        out = torch.zeros(len(lens), 4, 128, dtype=BF, device="cuda")
+        v.vh_quant_decode_attn(q, *cache, *scale, c["table"], c["lens"], c["active"], out, v.alloc_workspace(len(lens), 4, 1, 128, P))
+        bad = Q.differs(out, Q.attention(r, q.cpu()), BF)
+        assert bad is None, bad
+
+
 @pytest.mark.parametrize("num_ctas", [1, 2, 3, 7, 40, 1000])
 def test_decode_split_rows(num_ctas):
     check_decode(Q.make([900, 3, 411, 1], [1] * 4, window=700, sinks=20, seed=num_ctas), num_ctas=num_ctas)
