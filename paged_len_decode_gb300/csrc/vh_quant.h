@@ -47,8 +47,9 @@ struct QuantDecodeParams {
 };
 
 // What a row's piece costs in the merge, by q head of a kv head, in the time that a CTA takes for a
-// tile: as in the windowed decode (0.1 instead measured the same on rows of 200 to 32768 tokens).
-constexpr float kQuantPiece = 0.05f;
+// tile.  (0.05, 0.1, 0.2 and 0.4: one row of up to 30000 tokens, 64 / 8 heads of 128, 40.1, 38.6, 36.9 and
+// 41.8 us; 40 / 5 heads 30.8, 30.3, 31.9 and 37.9; four rows of 16000, 64 / 8 heads of 64, 52.4, 43.4, 45.1 and 47.6.)
+constexpr float kQuantPiece = 0.1f;
 
 struct QuantReadParams {
   QuantMemory memory;

