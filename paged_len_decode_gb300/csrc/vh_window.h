@@ -30,10 +30,6 @@ struct MropeParams {
   uint16_t* k_cache;
   uint16_t* v_cache;
   long long page_stride, token_stride, head_stride;
-  // a cache of 8 bits instead: e4m3 values with the same strides, and a scale for every slot and head
-  uint8_t *k8, *v8;            // null: the cache has 16 bits
-  float *k_scale, *v_scale;
-  long long scale_page, scale_head;  // strides; a page's slots follow one another
   int num_pages;
   const int32_t* page_table;   // null: contiguous cache
   int max_pages_per_seq;
@@ -46,6 +42,10 @@ struct MropeParams {
   int32_t* err_flag;
   int T, B, Hq, Hkv, D, P;
   int warps;                   // that share a token
+  // a cache of 8 bits instead: e4m3 values with the same strides, and a scale for every slot and head
+  uint8_t *k8, *v8;            // null: the cache has 16 bits
+  float *k_scale, *v_scale;
+  long long scale_page, scale_head;  // strides; a page's slots follow one another
 };
 
 struct WindowDecodeParams {
@@ -100,8 +100,6 @@ struct PromptParams {
   const int32_t* token_start;
   const int32_t* seq_lens;
   const int32_t* active;
-  const uint32_t* tree_mask;   // [T][mask_words] (the tree's kernels)
-  int mask_words;
   int window, sinks;
   uint16_t* out;
   float scale_log2;
@@ -116,6 +114,9 @@ struct PromptParams {
   int shift_g, shift_splits, shift_page;  // log2 of G, splits and P (-1: not a power of two)
   uint32_t hkv_inverse;        // ceil(2^32 / Hkv), 0 for Hkv == 1: v / Hkv of v < 2^32 / Hkv is the high word of v times it
   int* counter;                // the next unit to be drawn (splits == 1); zero between calls
+  // the tree's kernels (behind the rest: between the others these made 24 ragged prompts 43.0 us instead of 42.1)
+  const uint32_t* tree_mask;   // [T][mask_words]
+  int mask_words;
 };
 
 // The launch of kernels that begin with pdl_begin (vh_ragged.cuh).

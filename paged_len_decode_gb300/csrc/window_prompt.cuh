@@ -56,6 +56,8 @@
 //    the rows.
 #pragma once
 
+#include <type_traits>
+
 #include "vh_ragged.cuh"
 #include "vh_tcgen05.cuh"
 #include "vh_window.h"
@@ -88,10 +90,9 @@ constexpr uint32_t kTmem = 512;  // columns: scores of both row tiles, then thei
 enum { kPlain, kWithout, kPlusInf, kMinusInf, kNaN, kNoWeight, kSettle };
 
 // One CTA's work: queries of one request and kv head, and a share of their key tiles.
-struct Unit {
+struct PlainUnit {
   int row, first, ntok;         // request, first token, tokens
   int slot;                     // slot of the first token
-  int low;                      // the least slot that a window counts back from: the first token's, in a tree its root's
   int h, z;                     // kv head, share of the keys
   int sink_boxes, from, boxes;  // boxes 0 .. sink_boxes - 1 of the row, then `from` on; `boxes` in all
   int count;                    // key tiles
@@ -102,6 +103,19 @@ struct Unit {
   int all0, all1;               // k0 and k1 of the first run
   int more;                     // 0: no unit, the CTA is done
 };
+// (and of a tree: its root's slot, the least that a window counts back from)
+struct TreeUnit : PlainUnit {
+  int low;
+};
+template <bool TREE>
+using Unit = std::conditional_t<TREE, TreeUnit, PlainUnit>;
+
+// What a window of the unit's queries counts back from at least: a tree's root, or `first`.
+template <bool TREE>
+__device__ __forceinline__ int low_of(const Unit<TREE>& u, int first) {
+  if constexpr (TREE) return u.low;
+  else return first;
+}
 
 // The slots of key tile k: column c holds slot base + c, from column `jump` on base + c + gap.
 struct Columns {
@@ -135,12 +149,12 @@ struct Tiles {
   __device__ bool has(int k) const { return k < s_end || (k >= w_begin && k < w_end); }
 };
 template <bool TREE>
-__device__ __forceinline__ Tiles tiles_of(const PromptParams& p, const Unit& u, int m) {
+__device__ __forceinline__ Tiles tiles_of(const PromptParams& p, const Unit<TREE>& u, int m) {
   const int per_tile = kRows >> p.shift_g, last = u.slot + u.ntok - 1, f = u.slot + m * per_tile, e = min(last, f + per_tile - 1);
   const int shift = 7 - p.shift_box, to = u.sink_boxes + (e >> p.shift_box) - u.from;
   Tiles t;
   t.s_end = f > last ? 0 : min((u.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
-  t.w_begin = (u.sink_boxes + max(0, (max(0, (TREE ? u.low : f) - p.window + 1) >> p.shift_box) - u.from)) >> shift;
+  t.w_begin = (u.sink_boxes + max(0, (max(0, low_of<TREE>(u, f) - p.window + 1) >> p.shift_box) - u.from)) >> shift;
   t.w_end = f > last || to < u.sink_boxes ? 0 : (to >> shift) + 1;
   return t;
 }
@@ -175,8 +189,8 @@ __device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
     x.blocks = n > 0 ? (n + per - 1) >> p.shift_block : 0;
     if (x.r.ok && n > 0) {
       int a, b;
-      const int slot = x.r.len - min(n, per);
-      list_boxes(p, TREE ? x.r.len - n : slot, slot, min(n, per), a, b, weight);
+      if constexpr (TREE) list_boxes(p, x.r.len - n, x.r.len - min(n, per), min(n, per), a, b, weight);
+      else list_boxes(p, x.r.len - min(n, per), x.r.len - min(n, per), min(n, per), a, b, weight);
     }
   }
   int rank = 0;
@@ -194,8 +208,8 @@ __device__ __forceinline__ Rows rows_of(const PromptParams& p, int lane) {
 // Unit u, by one warp.  Tokens of inactive and flagged requests are written as
 // zeros here.
 template <bool TREE>
-__device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows, int u, int lane) {
-  Unit r{};
+__device__ __forceinline__ Unit<TREE> unit_of(const PromptParams& p, const Rows& rows, int u, int lane) {
+  Unit<TREE> r{};
   r.more = 1;
   const int per = 1 << p.shift_block;
   r.z = u & (p.splits - 1);
@@ -235,8 +249,8 @@ __device__ __forceinline__ Unit unit_of(const PromptParams& p, const Rows& rows,
     return r;
   }
   r.slot = g.len - (g.end - r.first);
-  r.low = TREE ? g.len - (g.end - g.start) : r.slot;
-  list_boxes(p, r.low, r.slot, r.ntok, r.sink_boxes, r.from, r.boxes);
+  if constexpr (TREE) r.low = g.len - (g.end - g.start);
+  list_boxes(p, low_of<TREE>(r, r.slot), r.slot, r.ntok, r.sink_boxes, r.from, r.boxes);
   r.count = (r.boxes + (kKeys >> p.shift_box) - 1) >> (7 - p.shift_box);
   if (p.splits == 1) {
     r.k1 = r.count;
@@ -256,50 +270,52 @@ __device__ __forceinline__ uint32_t visible32(int above, int low, int sink) {
   return below32(above) & (~below32(low) | below32(sink));
 }
 
-// What a query sees: the one in slot i, with a tree's drafted tokens in the slots from `base`
+// The keys of columns c .. c + 31 that the query in slot i sees.
+__device__ __forceinline__ uint32_t visible_of(const Columns& cols, int c, int i, int window, int sinks) {
+  const int jc = cols.base + c;
+  uint32_t vis = visible32(i + 1 - jc, i - window + 1 - jc, sinks - jc);
+  if (cols.jump < kKeys) {
+    const int jg = jc + cols.gap;  // the word's first slot behind the jump
+    const uint32_t lead = below32(cols.jump - c);
+    vis = (vis & lead) | (visible32(i + 1 - jg, i - window + 1 - jg, sinks - jg) & ~lead);
+  }
+  return vis;
+}
+
+// What a drafted token sees: the one in slot i, with the tree's tokens in the slots from `base`
 // on, `words` the bits of its ancestors among them, and `at` its position (the context's
 // length and its ancestors).
-template <bool TREE>
-struct Sight {
-  int i, window, sinks;
-  int base, at, mask_words;
+struct TreeSight {
+  int i, base, at;
   const uint32_t* words;
-  __device__ Sight(const PromptParams& p, const Unit& u, int token) : i(u.slot + min(token, u.ntok - 1)), window(p.window), sinks(p.sinks) {
-    if constexpr (TREE) {
-      base = u.low;
-      mask_words = p.mask_words;
-      words = p.tree_mask + static_cast<long long>(u.first + min(token, u.ntok - 1)) * mask_words;
-      at = base;
-      if (window < kNoWindow)
-        for (int x = 0; 32 * x < i - base; ++x) at += __popc(__ldg(words + x) & below32(i - base - 32 * x));
-    }
-  }
   // Bit x: the slot j0 + x.
-  __device__ uint32_t from(int j0) const {
-    if constexpr (!TREE) {
-      return visible32(i + 1 - j0, i - window + 1 - j0, sinks - j0);
-    } else {
-      uint32_t vis = visible32(base - j0, at - window + 1 - j0, sinks - j0);
-      const int d = j0 - base, self = i - base;  // bits d .. d + 31 of the mask
-      if (d > -32 && d <= self) {
-        const int w = d >> 5;
-        const uint32_t lo = w >= 0 ? __ldg(words + w) : 0u, hi = w + 1 < mask_words ? __ldg(words + w + 1) : 0u;
-        vis |= __funnelshift_r(lo, hi, d & 31) & below32(self - d);
-        if (self - d < 32) vis |= 1u << (self - d);
-      }
-      return vis;
+  __device__ __forceinline__ uint32_t from(const PromptParams& p, int j0) const {
+    uint32_t vis = visible32(base - j0, at - p.window + 1 - j0, p.sinks - j0);
+    const int d = j0 - base, self = i - base;  // bits d .. d + 31 of the mask
+    if (d > -32 && d <= self) {
+      const int w = d >> 5;
+      const uint32_t lo = w >= 0 ? __ldg(words + w) : 0u, hi = w + 1 < p.mask_words ? __ldg(words + w + 1) : 0u;
+      vis |= __funnelshift_r(lo, hi, d & 31) & below32(self - d);
+      if (self - d < 32) vis |= 1u << (self - d);
     }
+    return vis;
   }
 };
 
-// The keys of columns c .. c + 31 that a query sees.
-template <bool TREE>
-__device__ __forceinline__ uint32_t visible_of(const Columns& cols, int c, const Sight<TREE>& q) {
+__device__ __forceinline__ TreeSight tree_sight(const PromptParams& p, const Unit<true>& u, int token) {
+  token = min(token, u.ntok - 1);
+  TreeSight q{u.slot + token, u.low, u.low, p.tree_mask + static_cast<long long>(u.first + token) * p.mask_words};
+  if (p.window < kNoWindow)
+    for (int x = 0; 32 * x < q.i - q.base; ++x) q.at += __popc(__ldg(q.words + x) & below32(q.i - q.base - 32 * x));
+  return q;
+}
+
+__device__ __forceinline__ uint32_t visible_of(const PromptParams& p, const Columns& cols, int c, const TreeSight& q) {
   const int jc = cols.base + c;
-  uint32_t vis = q.from(jc);
+  uint32_t vis = q.from(p, jc);
   if (cols.jump < kKeys) {
     const uint32_t lead = below32(cols.jump - c);
-    vis = (vis & lead) | (q.from(jc + cols.gap) & ~lead);  // (the word's first slot behind the jump)
+    vis = (vis & lead) | (q.from(p, jc + cols.gap) & ~lead);
   }
   return vis;
 }
@@ -373,7 +389,7 @@ __device__ __forceinline__ float reached(float old, int mode) {
 // column for +inf, -inf and NaN, in its part of `staging`).  bars: s_full of both row tiles,
 // then p_full, o_full and o_seen.  Returns the key tiles done, or -1 if a wait ran out.
 template <typename E, int D, bool PAIR, bool TREE>
-__device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit& u, int tiles, int blocks, uint32_t tmem,
+__device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit<TREE>& u, int tiles, int blocks, uint32_t tmem,
                                               uint32_t bars, uint32_t staging) {
   const int m = threadIdx.x >> 7, warp = threadIdx.x >> 5;
   const uint32_t noted = staging + static_cast<uint32_t>(warp) * 4096 + 2048;
@@ -381,7 +397,9 @@ __device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit&
   constexpr uint32_t kOne = E::kF16 ? 0x3C00u : 0x3F80u;
   const int lane = threadIdx.x & 31, r = threadIdx.x & (kRows - 1), mode = u.mode;
   const int before = tiles, per_tile = kRows >> p.shift_g, mq = PAIR ? 0 : m, token = mq * per_tile + (r >> p.shift_g);
-  const Sight<TREE> q(p, u, token);
+  const int last = u.slot + u.ntok - 1, i = min(u.slot + token, last);
+  TreeSight q{};
+  if constexpr (TREE) q = tree_sight(p, u, token);
   const uint32_t scores = tmem + static_cast<uint32_t>(m * kKeys);
   const Tiles sees = tiles_of<TREE>(p, u, mq);
 #pragma unroll 1
@@ -393,7 +411,8 @@ __device__ __forceinline__ int look_at_values(const PromptParams& p, const Unit&
     uint32_t vis[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-      vis[c] = visible_of(cols, 32 * c, q);
+      if constexpr (TREE) vis[c] = visible_of(p, cols, 32 * c, q);
+      else vis[c] = visible_of(cols, 32 * c, i, p.window, p.sinks);
       if (mode == kNoWeight) {
         uint32_t x[32], low = 0u;
         tmem_ld32(scores + 32 * c, x);
@@ -487,12 +506,12 @@ __device__ __forceinline__ void note_met(uint32_t met, uint32_t bits) {
 }
 
 // What the warps of a CTA share, beside the dynamic shared memory.
-template <int D>
+template <int D, bool TREE>
 struct Shared {
   static constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
   uint64_t bars[3 * ST + 2 * QB + 11 + 2 * kSlots];
-  Unit units[kSlots];
-  Unit join;        // the block whose partial results a cluster joins
+  Unit<TREE> units[kSlots];
+  Unit<TREE> join;  // the block whose partial results a cluster joins
   int met[kSlots];  // of the unit in the slot (see kPlain)
   int span[kSlots][2];  // its key tiles that hold values that are no numbers: the first, and the one behind the last
   uint32_t tmem;
@@ -508,7 +527,7 @@ struct Shared {
     bool more = false;
 #pragma unroll
     for (int x = 0; x < kSlots; ++x) {
-      const volatile Unit& u = units[x];
+      const volatile Unit<TREE>& u = units[x];
       more = more || (u.more != 0 && (u.mode != kPlain || (*static_cast<volatile int*>(&met[x]) & 1) != 0));
     }
     return !more;
@@ -537,13 +556,13 @@ struct Bars {
   __device__ uint32_t landed(int s) const { return at + 8 * (2 * ST + 2 * QB + 11 + 2 * kSlots + s); }  // V, to be filtered
 };
 
-template <int D>
-__device__ __forceinline__ void Shared<D>::release(int n, int lane) {
+template <int D, bool TREE>
+__device__ __forceinline__ void Shared<D, TREE>::release(int n, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(Bars<D>{smem_addr(bars)}.u_empty(n % kSlots));
 }
-template <int D>
-__device__ __forceinline__ bool Shared<D>::next(int& n, bool& lost, int lane) {
+template <int D, bool TREE>
+__device__ __forceinline__ bool Shared<D, TREE>::next(int& n, bool& lost, int lane) {
   for (;; ++n) {
     lost = !mbar_wait(Bars<D>{smem_addr(bars)}.u_full(n % kSlots), (n / kSlots) & 1);
     if (lost) return false;
@@ -558,8 +577,8 @@ __device__ __forceinline__ bool Shared<D>::next(int& n, bool& lost, int lane) {
 // phases: of the stages' barriers, a bit each.  Returns them as they are then, or
 // kLostPhase if a wait ran out.
 constexpr uint32_t kLostPhase = 0x80000000u;
-template <typename E, int D>
-__device__ __forceinline__ uint32_t pass_on_values(Shared<D>& sh, uint32_t stages, int first, int count, uint32_t phases, int mode, int slot) {
+template <typename E, int D, bool TREE>
+__device__ __forceinline__ uint32_t pass_on_values(Shared<D, TREE>& sh, uint32_t stages, int first, int count, uint32_t phases, int mode, int slot) {
   constexpr int ST = kPromptStages<D>;
   constexpr uint32_t kStage = kKeys * D * 2;
   const Bars<D> bar{smem_addr(sh.bars)};
@@ -605,7 +624,7 @@ struct DrawPlace {
 // the slot is given to another.  In those runs this warp takes V from the copies, and passes it
 // on filtered.
 template <typename E, int D, bool TREE, bool AGAIN>
-__device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh, uint32_t stages, DrawPlace& at) {
+__device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D, TREE>& sh, uint32_t stages, DrawPlace& at) {
   const Bars<D> bar{smem_addr(sh.bars)};
   const int lane = threadIdx.x & 31;
   Rows rows{};
@@ -616,7 +635,7 @@ __device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh,
   uint32_t landings = 0u;       // phases of the stages' barriers
   bool lost = false;
   for (;; ++n) {
-    Unit& slot = sh.units[n % kSlots];
+    Unit<TREE>& slot = sh.units[n % kSlots];
     int mode = kPlain;
     if (n >= kSlots) {
       lost = !mbar_wait(bar.u_empty(n % kSlots), ((n / kSlots) - 1) & 1);
@@ -644,7 +663,7 @@ __device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh,
         break;
       }
     }
-    Unit x{};
+    Unit<TREE> x{};
     if (mode != kPlain) {
       x = slot;
       if (x.mode == kPlain) {
@@ -677,7 +696,7 @@ __device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh,
     lost = *static_cast<volatile int*>(&sh.abort) != 0;
     if (lost) break;
     if (AGAIN && x.mode != kPlain) {
-      landings = pass_on_values<E, D>(sh, stages, tiles, x.k1 - x.k0, landings, x.mode, n % kSlots);
+      landings = pass_on_values<E, D, TREE>(sh, stages, tiles, x.k1 - x.k0, landings, x.mode, n % kSlots);
       lost = landings == kLostPhase;
       if (lost) break;
     }
@@ -702,7 +721,7 @@ __device__ __forceinline__ void draw_units(const PromptParams& p, Shared<D>& sh,
 
 // The same from a unit that runs once more on, out of line.
 template <typename E, int D, bool TREE>
-__device__ __noinline__ bool draw_again(const PromptParams& p, Shared<D>& sh, uint32_t stages, int n, int u, int tiles) {
+__device__ __noinline__ bool draw_again(const PromptParams& p, Shared<D, TREE>& sh, uint32_t stages, int n, int u, int tiles) {
   DrawPlace at{n, u, tiles, false, false};
   draw_units<E, D, TREE, true>(p, sh, stages, at);
   return at.lost;
@@ -719,7 +738,7 @@ struct SoftmaxPlace {
 // The softmax warps' work on units from at.nu on: to the first that runs once more, or
 // (AGAIN) all that follow.
 template <typename E, int D, bool PAIR, bool TREE, bool AGAIN>
-__device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& sh, uint32_t base, SoftmaxPlace& at) {
+__device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D, TREE>& sh, uint32_t base, SoftmaxPlace& at) {
   constexpr int ST = kPromptStages<D>, QB = kPromptQueries<D>;
   const uint32_t sOut = base + (QB * 2 + ST) * kRows * D * 2, sPart = base, sLse = sOut + 7 * 4096 + 1024;
   const Bars<D> bar{smem_addr(sh.bars)};
@@ -745,7 +764,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     ++meets;
   };
   for (; !lost && sh.next(nu, lost, lane); ++nu) {
-    const Unit& blk = sh.units[nu % kSlots];  // (not released before the block is done)
+    const Unit<TREE>& blk = sh.units[nu % kSlots];  // (not released before the block is done)
     if (blk.k0 == blk.soft) {
       if (!AGAIN && blk.mode != kPlain) {
         at.again = true;
@@ -768,7 +787,9 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
     }
     const int mq = PAIR ? 0 : m, token = mq * per_tile + (r >> shift_g);
     const int last = blk.slot + blk.ntok - 1;
-    const Sight<TREE> q(p, blk, token);
+    const int i = min(blk.slot + token, last);
+    TreeSight q{};
+    if constexpr (TREE) q = tree_sight(p, blk, token);
     const int f = blk.slot + mq * per_tile;                // first and last query of the tile
     const int e = min(last, f + per_tile - 1);
     const Tiles sees = tiles_of<TREE>(p, blk, mq);  // (as the products' warp has them)
@@ -780,12 +801,15 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
       if (PAIR ? ((k - blk.k0) & 1) != m : !sees.has(k)) continue;  // not this row tile's
       // which keys this row sees, found while the scores are on their way
       const Columns cols = columns_of(blk.sink_boxes, blk.from, k, p.shift_box);
-      const bool edge = (k << (7 - p.shift_box)) < blk.sink_boxes || cols.base + kKeys - 1 > (TREE ? blk.low - 1 : f) || cols.base <= e - p.window;
+      const bool edge = (k << (7 - p.shift_box)) < blk.sink_boxes || cols.base + kKeys - 1 > (TREE ? low_of<TREE>(blk, f) - 1 : f) || cols.base <= e - p.window;
       uint32_t vis[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
       if (edge) {
         // sinks, or an edge of the causal mask or of the window
 #pragma unroll
-        for (int c = 0; c < 4; ++c) vis[c] = visible_of(cols, c * 32, q);
+        for (int c = 0; c < 4; ++c) {
+          if constexpr (TREE) vis[c] = visible_of(p, cols, c * 32, q);
+          else vis[c] = visible_of(cols, c * 32, i, p.window, p.sinks);
+        }
       }
       if (!mbar_wait(bar.s_full(m), tiles & 1)) {
         lost = true;
@@ -991,7 +1015,7 @@ __device__ __forceinline__ void softmax_units(const PromptParams& p, Shared<D>& 
 
 // The same from a unit that runs once more on, out of line.
 template <typename E, int D, bool PAIR, bool TREE>
-__device__ __noinline__ bool softmax_again(const PromptParams& p, Shared<D>& sh, uint32_t base, int nu, int tiles, int blocks,
+__device__ __noinline__ bool softmax_again(const PromptParams& p, Shared<D, TREE>& sh, uint32_t base, int nu, int tiles, int blocks,
                                            uint32_t meets) {
   SoftmaxPlace at{nu, tiles, blocks, meets, false, false};
   softmax_units<E, D, PAIR, TREE, true>(p, sh, base, at);
@@ -1009,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
   constexpr uint32_t kScores = tc_kind_f16(kRows, kKeys, !E::kF16, false);
   constexpr uint32_t kValues = tc_kind_f16(kRows, D, !E::kF16, true);
   extern __shared__ __align__(128) unsigned char smem_raw[];
-  __shared__ Shared<D> sh;
+  __shared__ Shared<D, TREE> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const int shift_g = p.shift_g, per_tile = kRows >> shift_g;  // tokens of a row tile
   const long long tok_stride = static_cast<long long>(p.Hq) * D;
@@ -1098,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
       int issued = kv, nq = 0;  // number in the ring, blocks of queries
       bool lost = false;
       for (int n = 0; !lost && sh.next(n, lost, lane); ++n) {
-        const Unit u = sh.units[n % kSlots];
+        const Unit<TREE> u = sh.units[n % kSlots];
         release_unit(n);
         if (u.k0 == u.k1) continue;
         // (the drawing warp passes on V of a unit that runs once more)
@@ -1190,9 +1214,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           wait(u_full(n % kSlots), (n / kSlots) & 1);
           lost = __any_sync(0xffffffffu, ran_out);
           auto field = [&](const int& x) { return __shfl_sync(0xffffffffu, x, 0); };  // (uniform, and known to be)
-          const Unit& from = sh.units[n % kSlots];
+          const Unit<TREE>& from = sh.units[n % kSlots];
           if (lost || field(from.more) == 0) break;
-          Unit blk;
+          Unit<TREE> blk;
           blk.slot = field(from.slot);
           blk.ntok = field(from.ntok);
           blk.sink_boxes = field(from.sink_boxes);
@@ -1202,7 +1226,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
           const int k0 = field(from.k0), k1 = field(from.k1);
           release_unit(n);
           if (k0 == k1) continue;
-          const int last = blk.slot + blk.ntok - 1, low = max(0, (TREE ? blk.low : blk.slot) - p.window + 1);
+          const int last = blk.slot + blk.ntok - 1, low = max(0, low_of<TREE>(blk, blk.slot) - p.window + 1);
           const int qb = nq % QB;
           // the key tiles that row tile m sees: below s_end, and from w_begin to w_end
           int s_end[2], w_begin[2], w_end[2];
@@ -1212,7 +1236,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
             const int f = blk.slot + m * per_tile, e = min(last, f + per_tile - 1);
             const int to = blk.sink_boxes + (e >> p.shift_box) - blk.from;  // last box, if it is one of the window's
             s_end[m] = f > last ? 0 : min((blk.sink_boxes + (1 << shift) - 1) >> shift, (e >> 7) + 1);
-            w_begin[m] = (blk.sink_boxes + max(0, (max(0, (TREE ? blk.low : f) - p.window + 1) >> p.shift_box) - blk.from)) >> shift;
+            w_begin[m] = (blk.sink_boxes + max(0, (max(0, low_of<TREE>(blk, f) - p.window + 1) >> p.shift_box) - blk.from)) >> shift;
             w_end[m] = f > last || to < blk.sink_boxes ? 0 : (to >> shift) + 1;
           }
           auto sees_k = [&](int m, int k) -> bool { return k < s_end[m] || (k >= w_begin[m] && k < w_end[m]); };
@@ -1364,7 +1388,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prompt_kernel(const __grid
 
   // ======================= the cluster's partial results ============================
   // (all CTAs of a cluster work on one block: they agree on whether there is one)
-  const Unit& u = sh.join;
+  const Unit<TREE>& u = sh.join;
   if (u.count == 0) return;
   cluster_sync();
   if (!*abort_flag) {
@@ -1444,12 +1468,13 @@ cudaError_t prepare_t(int (&clusters)[5]) {
 template <bool TREE>
 cudaError_t prepare_prompt(int (&clusters)[5]) {
   for (int& c : clusters) c = 1 << 20;
-  cudaError_t e = prepare_t<ElemBf16, 64, false, TREE>(clusters);
+  cudaError_t e = cudaSuccess;
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 64, false, TREE>(clusters);
   if (e == cudaSuccess) e = prepare_t<ElemBf16, 64, true, TREE>(clusters);
-  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, false, TREE>(clusters);
-  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, true, TREE>(clusters);
   if (e == cudaSuccess) e = prepare_t<ElemF16, 64, false, TREE>(clusters);
   if (e == cudaSuccess) e = prepare_t<ElemF16, 64, true, TREE>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, false, TREE>(clusters);
+  if (e == cudaSuccess) e = prepare_t<ElemBf16, 128, true, TREE>(clusters);
   if (e == cudaSuccess) e = prepare_t<ElemF16, 128, false, TREE>(clusters);
   if (e == cudaSuccess) e = prepare_t<ElemF16, 128, true, TREE>(clusters);
   return e;
