@@ -237,6 +237,67 @@ def test_small_workspaces_are_refused():
         v.vh_quant_decode_attn(q, c["k"], c["v"], c["ks"].cpu(), c["vs"].cpu(), *args[5:], ws)
 
 
+@pytest.mark.parametrize("P", [1, 3, 15, 100])
+def test_caches_of_one_small_page_a_row(P):
+    """Contiguous caches whose page, and so their tiles' boxes, are of any size."""
+    v = vh()
+    B, D_ = 3, 64
+    cache = v.alloc_quant_cache(B, P, 2, D_)
+    g = torch.Generator().manual_seed(P)
+    lens = [P, max(1, P // 2), 1]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    x = torch.randn(sum(lens), 8, D_, generator=g).to(torch.bfloat16).cuda()
+    cs = v.vh_rope_table(torch.empty(128, D_, device="cuda"))
+    q16 = torch.empty(sum(lens), 4, D_, dtype=torch.bfloat16, device="cuda")
+    starts, act = i32(starts_of(lens)), i32([1] * B)
+    v.vh_quant_kv_append(x[:, :4], x[:, 4:6], x[:, 6:], cs, *cache, None, i32(lens), act, q16, token_start=starts, err_flag=err)
+    q, out = torch.randn(B, 4, D_, generator=g), torch.zeros(B, 4, D_, dtype=torch.bfloat16, device="cuda")
+    v.vh_quant_decode_attn(q.cuda(), *cache, None, i32(lens), act, out, v.alloc_workspace(B, 4, 2, D_, P), err_flag=err)
+    back = torch.zeros(B, 2, P, 2, D_, dtype=torch.bfloat16, device="cuda")
+    v.vh_quant_kv_read(*cache, None, i32(lens), act, back[:, 0], back[:, 1], None, err_flag=err)
+    mask = v.tree_masks([list(range(-1, n - 1)) for n in lens])
+    tree_out = torch.zeros_like(q16)
+    v.vh_tree_attn(q16, back[:, 0], back[:, 1], None, starts, i32(lens), act, mask, tree_out,
+                   v.alloc_prompt_workspace(sum(lens), B, 4, 2, D_), err_flag=err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    r = R.Ragged(4, 2, D_, P, None, "NHD", torch.arange(B, dtype=torch.int32).view(B, 1), lens, [1] * B, [1] * B, 0, 0)
+    q8 = torch.stack([c.view(torch.uint8).cpu() for c in cache[:2]], 1)
+    Q.set_pool(r, q8.view(Q.E4M3), torch.stack([c.cpu() for c in cache[2:]], 1).transpose(2, 3).contiguous())
+    bad = Q.differs(out, Q.attention(r, q, contiguous=True), torch.bfloat16)
+    assert bad is None, bad
+    assert torch.equal(back.cpu().double()[0], r.pool[0].float().to(torch.bfloat16).double())
+    r16 = R.Ragged(4, 2, D_, P, back.cpu(), "NHD", r.table, lens, lens, [1] * B, 0, 0)
+    bad = R.close(tree_out, R.attention(r16, q16.cpu()), torch.bfloat16, D_, False)
+    assert bad is None, bad
+
+
+def test_thousands_of_rows():
+    lens = [1 + b % 3 for b in range(9000)]
+    lens[4321] = 700
+    r = Q.make(lens, [1] * 9000, Hq=1, Hkv=1, D=64, seed=1, table_extra=0, active=[int(b % 11 != 5) for b in range(9000)])
+    TQ.check_decode(r)
+    assert TQ.check_read(r, contiguous=False, P2=16) == 0
+
+
+def test_empty_calls():
+    v = vh()
+    cache, dev = v.alloc_quant_cache(4, 16, 2, 64), dict(device="cuda")
+    table, rows, act = i32([[1, 2]]), i32([0]), i32([0])
+    none = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, **dev)  # noqa: E731
+    cs = v.vh_rope_table(torch.empty(8, 64, **dev))
+    v.vh_quant_kv_append(none(0, 4, 64), none(0, 2, 64), none(0, 2, 64), cs, *cache, table, rows, act, none(0, 4, 64, dt=torch.float32),
+                         token_start=i32([0, 0]))
+    out = torch.full((1, 4, 64), 7.0, dtype=torch.bfloat16, **dev)
+    v.vh_quant_decode_attn(none(1, 4, 64, dt=torch.float32), *cache, table, rows, act, out, v.alloc_workspace(1, 4, 2, 64, 16))
+    pool = torch.full((4, 2, 16, 2, 64), 7.0, dtype=torch.bfloat16, **dev)
+    v.vh_quant_kv_read(*cache, table, rows, act, pool[:, 0], pool[:, 1], table)
+    v.vh_tree_attn(none(0, 4, 64), pool[:, 0], pool[:, 1], table, i32([0, 0]), rows, act, none(0, 1, dt=torch.int64), none(0, 4, 64),
+                   v.alloc_prompt_workspace(0, 1, 4, 2, 64))
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (pool == 7.0).all() and not cache[0].float().any()
+
+
 # ---- seeded random cases ---------------------------------------------------------------------------------------------
 
 def pick(rng, one_each):
