@@ -589,8 +589,8 @@ int vh_quant_kv_append(const vh_e16* q, const vh_e16* k_new, const vh_e16* v_new
  * token), with the scales beside the cache.  Scores are scale <q_rot, k8_j> ks_j
  * and the output sum_j p_j vs_j v8_j: nothing is rounded to 16 bits on the way but
  * the weights (p_j vs_j, 2^-11 relatively; 2^-22 where out is fp16) and q (to 2^-22
- * of a head's largest element).  Weights far below a head's largest one lose 2^-40 of
- * that, and p_j vs_j below 2^-126 counts as zero.  A query head with an infinity or a NaN gives NaN; a
+ * of a head's largest element).  Weights far below a head's largest one lose 2^-38 of
+ * that, and a p_j or p_j vs_j below 2^-126 may count as zero.  A query head with an infinity or a NaN gives NaN; a
  * visible key whose scale is NaN makes its rows NaN, a value its outputs.  A page id
  * outside [0, num_pages) is flagged VH_ERR_PAGE and its keys and values are
  * taken as zeros.  VH_FLAG_FP16: out is fp16. */

@@ -22,11 +22,13 @@
 //    pairs: a lane then has two neighbouring columns of the output.
 //  * q, divided by a power of two that brings its largest element into [1, 2), is
 //    split into an fp16 high part and residual: 22 bits of that (and so are the weights
-//    of an fp16 output).  ks multiplies the score.  The weight w = p_j vs_j c carries the value's scale, and c, a power of
-//    two a head, keeps the largest weight so far below 2^15: fp16 then holds
-//    those down to 2^-29 of it with 11 bits.  p refers to a maximum that is raised,
-//    and c lowered, only when a weight would grow too large (p above 2^8, w above
-//    2^15): no shuffles in most tiles.
+//    of an fp16 output).  ks multiplies the score.  The weight w = p_j vs_j c carries the value's
+//    scale, and c, a power of two a head, is lowered when a weight would leave fp16 (w above 2^15),
+//    to where the largest one lies in [2^13, 2^14): fp16 then holds weights down to 2^-27 of the
+//    largest so far with 11 bits, and loses at most 2^-38 of that of smaller ones.  p refers
+//    to a maximum that is raised only when a p would grow above 2^8 (no shuffles in most tiles), and c
+//    rises with it by the power of two that the weights lost: a large scale early in the row,
+//    whose key has no weight in the end, must not leave c too low for those that have it.
 //  * Keys outside V get the score -inf and the scale 0, and their rows of V are zeroed in
 //    shared memory, so nothing they hold counts.
 //  * Two tiles at a time: one set of waits, votes and masks, and two independent chains
@@ -55,7 +57,8 @@ constexpr int kWarpRows = 128;               // rows that the producer warp sums
 enum { kMiscTot = 0, kMiscAbort = 32, kMiscLost = 33, kMiscMost = 34, kMiscPart = 36, kMiscInts = 48 };  // part: 4 ints each
 constexpr float kGrow = 8.f;                 // log2 of the weight that raises the maximum
 constexpr float kWeightMost = 32768.f;       // the weight that lowers c
-constexpr float kFactorMost = 1.2980742e33f; // 2^110: c at first
+constexpr float kFactorMost = 1.2980742e33f; // 2^110: c at first, and at most
+constexpr int kFactorExp = 127 + 110;        // its exponent's bits
 
 __device__ __forceinline__ float lds(uint32_t addr) {
   float x;
@@ -412,12 +415,20 @@ __global__ void __launch_bounds__(32 * (kHeadsMost<D> + 1), D == 128 ? 2 : 1) qu
     const float mx0 = fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2]));
     const float mx1 = fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3]));
     if (__any_sync(0xffffffffu, mx0 > m0 + kGrow || mx1 > m1 + kGrow)) {
+      // All weights so far shrink by 2^d, d = n - m, and c rises by 2^k, k = ceil(d), at most to its
+      // first value: what they are in units of c stays, so that c never follows a weight that
+      // no longer counts.  (k = 0 while m is -inf: nothing has lowered c.)
+      auto raise = [&](float n, float& m, float& l, float& f) -> float {
+        const int e = static_cast<int>(__float_as_uint(f) >> 23);
+        const int k = min(static_cast<int>(ceilf(fminf(n - m, 256.f))), kFactorExp - e);
+        const float by = exp2f(m - (n == NEG_INF ? 0.f : n) + static_cast<float>(k));
+        l *= by * __uint_as_float(static_cast<uint32_t>(max(127 - k, 0)) << 23);
+        f = __uint_as_float(static_cast<uint32_t>(e + k) << 23);
+        m = n;
+        return by;
+      };
       const float n0 = fmaxf(m0, max_of_keys(mx0)), n1 = fmaxf(m1, max_of_keys(mx1));
-      const float by0 = exp2f(m0 - (n0 == NEG_INF ? 0.f : n0)), by1 = exp2f(m1 - (n1 == NEG_INF ? 0.f : n1));
-      m0 = n0;
-      m1 = n1;
-      l0 *= by0;
-      l1 *= by1;
+      const float by0 = raise(n0, m0, l0, c0), by1 = raise(n1, m1, l1, c1);
       rescale(by0, by1);
     }
     // (a max of -inf, from scores that are, is subtracted as 0)
