@@ -536,6 +536,11 @@ int vh_window_prompt_attn(const vh_e16* q, const vh_e16* k_cache, const vh_e16* 
  * its position; the drafted tokens of its mask (a window does not hide
  * them); and itself.  With masks of all ones this is vh_window_prompt_attn's
  * causal attention, but for a window's hold on the drafted tokens.
+ * A model with a window hides ancestors too, those W or more positions before a token.
+ * Where every token has fewer than W ancestors there are none; in deeper trees leave them out of the
+ * masks (but for those whose positions are below S): a token keeps its last W - 1
+ * ancestors then, its position counts as base + W - 1 or more, and that hides the context but
+ * for the sinks, as its true position does.
  * workspace: vh_prompt_workspace_bytes, as for vh_window_prompt_attn (the same
  *        buffer may serve both, one after the other). */
 #define VH_TREE_WORDS_MAX 16

@@ -441,20 +441,38 @@ def alloc_prompt_workspace(T: int, B: int, Hq: int, Hkv: int, D: int, device=Non
     return torch.zeros(vh_prompt_workspace_bytes(T, B, Hq, Hkv, D), dtype=torch.uint8, device=device or "cuda")
 
 
-def tree_masks(parents, device=None) -> torch.Tensor:
+def tree_masks(parents, device=None, window: int = 0, sinks: int = 0, contexts=None) -> torch.Tensor:
     """tree_mask of vh_tree_attn (int64 [T, words]) for the rows' drafted tokens: for
     every row the sequence of its tokens' parents, each the number of an earlier token of the
-    row, or -1 for a token that follows the context."""
+    row, or -1 for a token that follows the context.
+
+    The call's own window holds for the context only.  With `window` (the call's, 0: none) the
+    masks leave out the ancestors that it hides, those `window` or more positions before a token, so
+    that a tree of any depth is attended as its branches would be, one token after the other.
+    With `sinks` too, ancestors among a row's first `sinks` positions stay: `contexts` (the tokens
+    that every row holds before its drafted ones) says which they are."""
     parents = [[int(x) for x in row] for row in parents]
+    if window < 0 or sinks < 0:
+        raise ValueError("window and sinks must not be negative")
+    if window and sinks and contexts is None:
+        raise ValueError("sinks among the drafted tokens need the rows' contexts")
+    contexts = [int(n) for n in contexts] if contexts is not None else [sinks] * len(parents)
+    if len(contexts) != len(parents):
+        raise ValueError(f"contexts of {len(contexts)} rows for the parents of {len(parents)}")
     words = max(1, -(-max((len(row) for row in parents), default=0) // 64))
     masks = []
-    for row in parents:
+    for row, context in zip(parents, contexts):
         own = []
         for i, up in enumerate(row):
             if not -1 <= up < i:
                 raise ValueError(f"token {i} has the parent {up}: an earlier token of its row, or -1, is needed")
             own.append((own[up] | 1 << up) if up >= 0 else 0)
-        masks += own
+        for i, m in enumerate(own):
+            hidden = m.bit_count() - (window - 1) if window else 0  # the first ones of the branch
+            if hidden > 0:
+                branch = [k for k in range(i) if m >> k & 1]
+                m = sum(1 << k for x, k in enumerate(branch) if x >= hidden or context + x < sinks)
+            masks.append(m)
     signed = [[w - (1 << 64) if w >> 63 else w for w in ((m >> 64 * k) & (1 << 64) - 1 for k in range(words))] for m in masks]
     return torch.tensor(signed, dtype=torch.int64, device=device or "cuda").view(len(masks), words)
 

@@ -4,6 +4,8 @@
 // Operation: a row's n drafted tokens lie in the slots from base = L - n on; token i sees
 //   {j < base: at_i - j < W or j < S}, the drafted tokens k < i of its mask, and itself,
 // at_i = base + popcount(mask_i & (2^i - 1)): its position, which its window counts back from.
+// (Masks without the ancestors that a window hides keep this right: the W - 1 that are left put at_i at
+// base + W - 1, where the window ends behind the context.)
 // All that is seen lies before the token's own slot, so the lists of key tiles are the prompt's
 // (windows begin at the root's place), and only what a row sees of a tile differs: the bits of
 // 32 keys come from two words of its mask, in the one or two tiles that hold drafted tokens.
