@@ -17,7 +17,7 @@
 // first of them and the values are under way before anything is looked up.
 // What counts is bytes in flight and the length of the chain of look-ups: 20 warps
 // an SM with three heads' loads a lane each measured 64 us on 16384 tokens (32 / 8
-// heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.6 us on 2413 with the norm;
+// heads, 403 MB: 6.3 TB/s, 92 % of the copy peak) and 9.6 us on 1981 with the norm;
 // 24 warps with two 63.6 and 10.1 us.  In an earlier form four heads took 68 us
 // where two took 66, and a CTA of 4 tokens with its angles in shared memory
 // behind a barrier 82 us.  Angles gathered beside
@@ -309,9 +309,11 @@ cudaError_t launch_mrope_kv_append(const MropeParams& pp, int sm_count, cudaStre
   // tokens 3.1, 3.1 and 3.8, 2000 14.7, 8.0 and 8.0.
   p.warps = p.T <= 128 ? 8 : (p.T <= 1216 ? 2 : 1);
   const dim3 grid(static_cast<unsigned>((static_cast<long long>(p.T) * p.warps + kThreads / 32 - 1) / (kThreads / 32)));
-  // Into a cache of 8 bits: 16 warps an SM with three heads' loads a lane while they hold all tokens
-  // (2413 of them, with the norm: 9.2 us, and 10.7 with 28 warps and two loads), 28 with two
-  // otherwise (16384 tokens: 66.5 us, and 76 with 16 warps, 70.5 with 20).
+  // Into a cache of 8 bits: 16 warps an SM with three heads' loads a lane while they hold all tokens,
+  // 28 with two otherwise.  Prompts (16 / 8 heads, with the norm), 16 warps and 28: 1981 tokens 9.6 and
+  // 10.7 us; four inputs in turn, 1216 6.2 and 10.3, 1981 11.2 and 12.5, 2432 (16 warps on each of 152 SMs)
+  // 12.4 and 16.6, 2700 18.1 and 16.8, 4000 20.4 and 18.0; 32 / 8 heads without it 2432 14.5 and 17.8, 2700 20.8
+  // and 18.2; 16384 tokens 76.1 and 66.7 (70.5 with 20 warps).
   using Kernel = void (*)(MropeParams);
   const int form = !p.k8 ? k16 : (p.T <= 16 * sm_count ? k8Few : k8Many);
   const Kernel kernels[4][3] = {

@@ -12,9 +12,12 @@
 //
 // Bound by HBM for small trees (2 D bytes of a key and value against 4 D G n flops), by HBM and
 // the tensor cores alike for 64 tokens of 4 q heads a kv head: 256 rows over 180,000 keys
-// (745 MB, 188 GFLOP) take 168 us, 4.4 TB/s and 1120 TFLOP/s at once.  Keys shared by any number of
-// CTAs through memory (units of the same counter, joined by a second kernel) filled every SM
-// and took 174-191; one CTA a block 286, two blocks of 128 rows a request 177.  32 ragged trees of
+// (745 MB, 188 GFLOP), which need 110 and 100 us, take 168.  What they lose is balance: every
+// (request, kv head) has a cluster of two, 128 CTAs on 152 SMs, and the longest of the eight requests
+// has 1.25 times the mean's keys: 0.84 x 0.80 of the machine is 0.67, which is 110 / 168.  Equal
+// shares of every block through memory (2 to 8 units of the same counter, joined by a second kernel)
+// filled every SM, kept the shares of the long requests long, paid a start each, and took
+// 174-191; one CTA a block 286, two blocks of 128 rows a request 177.  32 ragged trees of
 // up to 59 tokens (head_dim 64, window 1024) take 25 us, 16 tokens over 5000 14.5: start 4.5,
 // five key tiles 4.5, outputs and the cluster's join 5.
 #include "window_prompt.cuh"
