@@ -13,6 +13,7 @@ count as zero, and so may an output: with values of at most 448 and a sum of wei
 and their outputs are about 2^-139.)
 """
 import math
+import random
 
 import pytest
 import torch
@@ -23,13 +24,11 @@ from test_gpu_quant import BF, FP, decode
 
 pytestmark = pytest.mark.gpu
 
-HQ, HKV, D = 8, 2, 128
-
-
-def batch(lens, groups, seed=0, **kw):
+def batch(lens, groups, seed=0, heads=(8, 2), D=128, **kw):
     """A batch whose keys have the scores and value scales of `groups`: (slots, lowest and highest score in base 2, log2 of
     the values' size); the last group goes on to the row's end.  Queries are 4 everywhere, so a key of the constant x
     has the score 4 D x / sqrt(D) log2(e)."""
+    HQ, HKV = heads
     r = Q.make(lens, [1] * len(lens), Hq=HQ, Hkv=HKV, D=D, seed=seed, **kw)
     g = torch.Generator().manual_seed(seed)
     x = torch.randn(r.pool.shape, generator=g)
@@ -50,6 +49,7 @@ def batch(lens, groups, seed=0, **kw):
 
 
 def check(r, q, dtype, num_ctas, raises=1):
+    HQ, HKV, D = r.Hq, r.Hkv, r.D
     out, err = decode(r, q, dtype, num_ctas=num_ctas)
     assert err == 0
     ref, tol = Q.attention(r, q, dtype=dtype)
@@ -107,3 +107,20 @@ def test_a_window_hides_the_large_values_and_sinks_keep_them():
     for sinks in (0, 8):
         r, q = batch([300, 96], [(32, 0, 1, 20), (32, 0, 7, 0), (1, 50, 55, -12)], seed=sinks, window=200, sinks=sinks)
         check(r, q, BF, 1, 2)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_runs_of_scores_and_scales(seed):
+    rng = random.Random(seed)
+    dtype = rng.choice([BF, FP])
+    groups, most = [], 40 if dtype == BF else 10
+    for _ in range(rng.randint(2, 8)):
+        low = rng.choice([0, rng.uniform(-60, 60)])
+        groups.append((rng.choice([1, 5, 16, 32, 33, 70]), low, low + rng.choice([0.0, 1.0, 9.0]), rng.randint(-most, most)))
+    hkv = rng.choice([1, 2, 3, 8])
+    heads = (hkv * rng.choice([1, 2, 4, 8]), hkv)
+    lens = [rng.randint(1, 500) for _ in range(rng.randint(1, 6))]
+    r, q = batch(lens, groups, seed, heads, rng.choice([64, 128]), P=rng.choice([8, 16, 48]), layout=rng.choice(["NHD", "HND"]),
+                 window=rng.choice([0, 0, 100, 300]), sinks=rng.choice([0, 4, 20]))
+    for num_ctas in (0, 1, rng.randint(2, 20)):
+        check(r, q, dtype, num_ctas, len(groups))
