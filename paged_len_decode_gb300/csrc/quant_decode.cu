@@ -38,8 +38,8 @@
 //  * Merge: the last CTA of a row fetches the pieces by bulk copies into the stages,
 //    one trip to memory for up to 32 of them and for both its rows, where loads in
 //    rounds of four pieces took 110 us instead of 108 (16 rows, 676 MB).
-// Measured: 16 rows of 4096-32768 tokens (32 / 8 heads of 128, 676 MB) 108 us = 6.2 TB/s,
-// 256 rows under a window of 2048 (1133 MB) 172 us = 6.6 TB/s (97 % of a copy's rate), 64
+// Measured: 16 rows of 4096-32768 tokens (32 / 8 heads of 128, 676 MB) 108-110 us = 6.2 TB/s,
+// 256 rows under a window of 2048 (1133 MB) 172-175 us = 6.5-6.6 TB/s (96-97 % of a copy's rate), 64
 // rows of 200-1200 tokens (86 MB) 23.9 us: start 3 us, SMs that end 5 us apart, merge 3 us.
 // Without any arithmetic the same copies take 104, 169 and 21.9 us.
 #include "vh_e4m3.cuh"

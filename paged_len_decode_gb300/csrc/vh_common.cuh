@@ -315,6 +315,9 @@ __device__ __forceinline__ void flag_error(int32_t* err_flag, int bits) {
 // Tiles are 16 consecutive tokens of one row; a page holds P/16 tiles.
 constexpr int kTile = 16;
 
+// Where share c of n equal ones of `total` begins (the first total % n have one more).
+__device__ __forceinline__ int share_begin(int c, int n, int total) { return c * (total / n) + min(c, total % n); }
+
 // Number of 16-token tiles a row contributes to the attention work list
 // (0 for padding rows and for rows whose seq_len is out of range).
 __device__ __forceinline__ int row_tiles(int active, int L, int max_len) {

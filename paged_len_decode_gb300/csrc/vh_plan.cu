@@ -108,8 +108,6 @@ static int choose_hc(int Hkv, int D) {
 // of a launch.
 constexpr int kDefaultStages = 2;
 
-static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 // Shared-memory plan of the attention kernel (fused or not): kDefaultStages
 // pipeline stages; if two stages do not fit, fewer kv heads go to each CTA.
 // Returns false if even one head per CTA cannot have two stages.

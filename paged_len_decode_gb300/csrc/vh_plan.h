@@ -1,6 +1,7 @@
 // vh_plan.h -- launch planning of the decode kernels (internal; host side).
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -22,6 +23,29 @@ struct DeviceInfo {
 
 // The current device's info, or null if no usable sm_103 device is current.
 const DeviceInfo* device_info();
+
+// What a file's first call on a device sets once (kernel attributes); a call that could not set
+// it leaves it to the next one.
+struct Prepared {
+  std::mutex mu;
+  std::atomic<bool> ok{false};
+  int clusters[5] = {};  // clusters of 2^x CTAs of a prompt kernel that run at a time
+
+  template <typename F>
+  bool once(F prepare) {
+    if (ok.load(std::memory_order_acquire)) return true;
+    std::lock_guard<std::mutex> lk(mu);
+    if (ok.load(std::memory_order_relaxed)) return true;
+    if (!prepare(*this)) {
+      cudaGetLastError();
+      return false;
+    }
+    ok.store(true, std::memory_order_release);
+    return true;
+  }
+};
+
+inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void* p);
 bool valid_shape(int B, int Hq, int Hkv, int D, int P);

@@ -2,7 +2,6 @@
 // read-back (declared in include/vh.h): checks, launch plans, launches on the
 // caller's stream.  Nothing here synchronises, allocates or reads device memory.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -15,32 +14,19 @@
 namespace {
 
 using vh::DeviceInfo;
+using vh::align_up;
 using vh::aligned16;
 using vh::device_info;
 using vh::kMaxDevices;
 using vh::valid_cache;
 
-struct Prepared {
-  std::mutex mu;
-  std::atomic<bool> ok{false};
-};
-Prepared g_prepared[kMaxDevices];
+vh::Prepared g_prepared[kMaxDevices];
 
-// Kernel attributes, set on the first call on a device (a call that could not set them leaves it to the next one).
 bool prepared(const DeviceInfo& dev) {
-  Prepared& s = g_prepared[dev.index];
-  if (s.ok.load(std::memory_order_acquire)) return true;
-  std::lock_guard<std::mutex> lk(s.mu);
-  if (s.ok.load(std::memory_order_relaxed)) return true;
-  if (vh::prepare_quant_read(dev.smem_optin - 1024) != cudaSuccess || vh::prepare_quant_decode(dev.smem_optin) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  s.ok.store(true, std::memory_order_release);
-  return true;
+  return g_prepared[dev.index].once([&](vh::Prepared&) {
+    return vh::prepare_quant_read(dev.smem_optin - 1024) == cudaSuccess && vh::prepare_quant_decode(dev.smem_optin) == cudaSuccess;
+  });
 }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 constexpr int kMaxHc = 8;
 constexpr int kMaxStages = 8;

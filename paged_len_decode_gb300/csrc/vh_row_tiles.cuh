@@ -6,10 +6,6 @@
 
 namespace vh {
 
-__device__ __forceinline__ int share_begin(int c, int n, int total) {
-  return c * (total / n) + min(c, total % n);
-}
-
 __device__ __forceinline__ int share_of(int t, int n, int total) {
   const int q = total / n, r = total % n, big = r * (q + 1);
   return t < big ? t / (q + 1) : r + (t - big) / q;

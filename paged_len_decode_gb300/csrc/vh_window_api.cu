@@ -3,7 +3,6 @@
 // of scalars and alignment, launch plans, launches on the caller's stream.
 // Nothing here synchronises, allocates or reads device memory.
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -62,6 +61,7 @@ bool encode_tiled(CUtensorMap* m, CUtensorMapDataType type, const void* base, in
 namespace {
 
 using vh::DeviceInfo;
+using vh::align_up;
 using vh::aligned16;
 using vh::device_info;
 using vh::valid_cache;
@@ -72,40 +72,18 @@ constexpr int kMaxHc = 8;
 constexpr int kMaxStages = 8;
 constexpr int kStageTarget = 65536;  // bytes in flight of a CTA, two CTAs on an SM
 
-// Kernel attributes of this file's kernels, set on the first call on a device
-// (a call that could not set them leaves it to the next one).
-struct Prepared {
-  std::mutex mu;
-  std::atomic<bool> ok{false};
-  int clusters[5] = {};  // clusters of 2^x CTAs of the prompt kernel that run at a time
-};
-Prepared g_prepared[kMaxDevices];
-Prepared g_tree[kMaxDevices];  // the tree's kernels
-
-template <typename F>
-bool prepared(Prepared& s, F prepare) {
-  if (s.ok.load(std::memory_order_acquire)) return true;
-  std::lock_guard<std::mutex> lk(s.mu);
-  if (s.ok.load(std::memory_order_relaxed)) return true;
-  if (!prepare(s)) {
-    cudaGetLastError();
-    return false;
-  }
-  s.ok.store(true, std::memory_order_release);
-  return true;
-}
+vh::Prepared g_prepared[kMaxDevices];
+vh::Prepared g_tree[kMaxDevices];  // the tree's kernels
 
 bool prepared(const DeviceInfo& dev) {
-  return prepared(g_prepared[dev.index], [&](Prepared& s) {
+  return g_prepared[dev.index].once([&](vh::Prepared& s) {
     return vh::prepare_window_decode(dev.smem_optin) == cudaSuccess && vh::prepare_window_prompt(s.clusters) == cudaSuccess;
   });
 }
 
 bool prepared_tree(const DeviceInfo& dev) {
-  return prepared(g_tree[dev.index], [](Prepared& s) { return vh::prepare_tree_attn(s.clusters) == cudaSuccess; });
+  return g_tree[dev.index].once([](vh::Prepared& s) { return vh::prepare_tree_attn(s.clusters) == cudaSuccess; });
 }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Shared-memory plan and automatic CTA count of the windowed decode kernel.
 struct DecodePlan {
@@ -313,15 +291,14 @@ int append(vh::MropeParams& p, const uint8_t* pair_axis, unsigned flags, void* s
 }
 
 // Both calls on ragged batches: with tree_mask, the drafted tokens' ancestors instead of all earlier ones.
-int prompt(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride,
-                          int64_t token_stride, int64_t head_stride, int num_pages, const int32_t* page_table,
-                          int max_pages_per_seq, const int32_t* token_start, const int32_t* seq_lens,
-                          const int32_t* active, const int64_t* tree_mask, int mask_words, int window, int sinks, vh_e16* out, float sm_scale, int num_splits,
-                          void* workspace, size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B,
-                          int Hq, int Hkv, int D, int page_size, void* stream) {
+int prompt(const vh_e16* q, const vh_e16* k_cache, const vh_e16* v_cache, int64_t page_stride, int64_t token_stride,
+           int64_t head_stride, int num_pages, const int32_t* page_table, int max_pages_per_seq,
+           const int32_t* token_start, const int32_t* seq_lens, const int32_t* active, const int64_t* tree_mask,
+           int mask_words, int window, int sinks, vh_e16* out, float sm_scale, int num_splits, void* workspace,
+           size_t workspace_bytes, int32_t* err_flag, unsigned flags, int T, int B, int Hq, int Hkv, int D,
+           int page_size, void* stream) {
   if ((flags & ~VH_FLAG_FP16) != 0 || T < 0 || window < 0 || sinks < 0 || num_splits < 0 || num_splits > 16 ||
-      (num_splits & (num_splits - 1)) != 0 || mask_words < 0 ||
-      !(sm_scale == sm_scale) ||
+      (num_splits & (num_splits - 1)) != 0 || mask_words < 0 || !(sm_scale == sm_scale) ||
       !valid_cache(B, Hq, Hkv, D, page_size, page_stride, token_stride, head_stride, num_pages, page_table,
                    max_pages_per_seq))
     return VH_EINVAL;

@@ -133,8 +133,6 @@ __device__ __forceinline__ Columns columns_of(int sink_boxes, int from, int k, i
   return x;
 }
 
-__device__ __forceinline__ int share_begin(int c, int n, int total) { return c * (total / n) + min(c, total % n); }
-
 // The boxes of `ntok` queries from `slot` on; windows count back from `low` at least.
 __device__ __forceinline__ void list_boxes(const PromptParams& p, int low, int slot, int ntok, int& sink_boxes, int& from, int& boxes) {
   const int last = slot + ntok - 1;
