@@ -577,7 +577,7 @@ PyMethodDef g_methods[] = {
               "int64 [T, words]: bit k % 64 of word k / 64 says that the row's k-th drafted\n"
               "token is an ancestor (see tree_masks).  A window counts back from the context's\n"
               "length plus the number of ancestors, and hides slots of the context only: where a\n"
-              "tree is as deep as the window, give tree_masks the window too.  Returns out."),
+              "tree has more levels than that, give tree_masks the window too.  Returns out."),
     VH_METHOD("vh_quant_kv_append", kv_append<true>,
               "vh_quant_kv_append(q, k_new, v_new, cos_sin, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, "
               "active, q_rot, token_start=None, positions=None, pair_axis=None, err_flag=None, q_norm_w=None, "
